@@ -57,6 +57,15 @@ extern "C" {
 #define QMM_EHIP (-4)         /* the HIP runtime reported an error at launch */
 #define QMM_ESPACE (-5)       /* workspace smaller than the *_workspace() query returned */
 
+/* value types of the tensors of qmm_rmsnorm, qmm_dequantize_q8_1, qmm_moe_route and qmm_lora */
+#define QMM_TYPE_F32 1
+#define QMM_TYPE_F16 2  /* binary16 */
+#define QMM_TYPE_BF16 3 /* bfloat16 */
+
+/* scores of qmm_moe_route */
+#define QMM_SCORE_SOFTMAX 0
+#define QMM_SCORE_SIGMOID 1
+
 /* flags */
 #define QMM_FLAG_DEBUG_INTERMEDIATES 1u /* also write fp32 intermediates into the workspace */
 
@@ -322,6 +331,105 @@ int qgemv_planes(int wtype, const void* planes, int64_t nrows, int64_t k, const 
 int qmm_moe_combine(const float* y, int64_t nrows, int64_t hidden, const int32_t* row_idx,
                     const float* weights, int64_t ntok, int topk, float* out, int64_t ldo,
                     void* stream);
+
+/* Root-mean-square norm with the residual's addition, for the activations the products take.
+ * For row t, in binary32:
+ *   r[j]  = x[j] + res[j]                          (r = x when res is NULL)
+ *   y[j]  = (r[j] * (1 / sqrt(sum r^2 / hidden + eps))) * w[j]
+ * and writes any of: res_out = r rounded once to rtype, y rounded once to ytype, yq = q8_1(y)
+ * (qmm_quantize_q8_1's bytes for the binary32 y).  The norm is taken of the binary32 r, not of
+ * the rounded res_out.  The sum of squares is binary32: rows whose sum passes its range give y = 0.
+ *   x       : xtype [ntok][ldx], ldx >= hidden.
+ *   res, res_out : rtype [ntok][ldr], [ntok][ldro]; either may be NULL.
+ *   w       : float [hidden].   eps >= 0.
+ *   y       : ytype [ntok][ldy], or NULL.   yq : q8_1 [ntok][hidden/32][36], or NULL.
+ *   hidden  : 1 .. 32768; a multiple of 32 when yq is given.
+ *   Pointers and strides need their type's alignment only (yq: 4 bytes); 16-byte aligned rows are
+ *   read and written 16 bytes at a time.  res_out may be res, and y or res_out may be x, if the
+ *   types and row strides agree; otherwise outputs must not overlap inputs.
+ * Errors: QMM_EINVAL (no output, unknown type, sizes, strides, eps negative or not finite),
+ *         QMM_EALIGN, QMM_EUNSUPPORTED (hidden above 32768, 2^31 rows or more). */
+int qmm_rmsnorm(int xtype, const void* x, int64_t ldx, int rtype, const void* res, int64_t ldr,
+                void* res_out, int64_t ldro, const float* w, float eps, int64_t ntok,
+                int64_t hidden, int ytype, void* y, int64_t ldy, void* yq, void* stream);
+
+/* The values q8_1 blocks stand for: out[c*ldo + j] = d * q_j of column c, the exact product rounded
+ * once to the output type.
+ *   xq   : q8_1 [ncols][k/32][36], 4-byte aligned.   k : a multiple of 32, > 0.
+ *   out  : otype (QMM_TYPE_F32 or QMM_TYPE_F16) [ncols][ldo], ldo >= k.
+ * Errors: QMM_EINVAL, QMM_EALIGN, QMM_EUNSUPPORTED (2^31 blocks or more). */
+int qmm_dequantize_q8_1(const void* xq, int64_t k, int64_t ncols, int otype, void* out, int64_t ldo,
+                        void* stream);
+
+/* Routing of tokens to experts.  For each row of logits l[0..nexperts), in binary32:
+ *   s[e] = softmax(l)[e]  or  1 / (1 + exp(-l[e]))                        (score)
+ *   c[e] = s[e] + bias[e]   (bias NULL: s[e]; a softmax without bias whose groups, if any, go by
+ *          their best member is compared by l[e] itself, the same order without its rounding)
+ *   an expert whose l[e] or c[e] is -inf or NaN is never chosen (nor counted in the softmax);
+ *   ngroups > 1: the experts form ngroups equal runs; a run's score is the sum of its group_top
+ *     (1 or 2) largest c (-inf where it has fewer), the topk_groups best runs stay, the experts of
+ *     the others are not chosen;
+ *   the topk largest c, in descending order; ties, of experts and of runs, go to the lowest index;
+ *   weights = s of the chosen (without the bias), with QMM_ROUTE_RENORM divided by their sum (left
+ *     at 0 where that sum is 0), times `scale`.
+ * Where fewer than topk experts can be chosen the remaining ids are -1 and their weights 0 (a row
+ * of -inf gives only those).  A softmax over +inf logits shares 1 among them.
+ *   logits : ltype [ntok][ldl], ldl >= nexperts.   bias : float [nexperts] or NULL.
+ *   ids : int32 [ntok][topk];  weights : float [ntok][topk].
+ *   nexperts 1 .. 1024 and a multiple of ngroups; ngroups 1 .. 64; 1 <= topk_groups <= ngroups;
+ *   group_top <= nexperts / ngroups; 1 <= topk <= min(64, topk_groups * nexperts / ngroups).
+ * Errors: QMM_EINVAL, QMM_EALIGN, QMM_EUNSUPPORTED (nexperts above 1024, ngroups or topk above 64,
+ *         2^31 rows or more). */
+#define QMM_ROUTE_RENORM 1u
+int qmm_moe_route(int ltype, const void* logits, int64_t ldl, const float* bias, int64_t ntok,
+                  int nexperts, int score, int ngroups, int topk_groups, int group_top, int topk,
+                  float scale, int32_t* ids, float* weights, unsigned flags, void* stream);
+
+/* Workspace bytes qmm_moe_dispatch needs (host); 0 for sizes it does not take. */
+size_t qmm_moe_dispatch_workspace(int64_t ntok, int topk, int nexperts);
+
+/* The expert-sorted entry lists that the grouped products and the combine take, from a routing's
+ * ids [ntok][topk]: the entries (t, k) whose id is in [0, nexperts), ordered by expert, then by token,
+ * then by k; an id outside adds no entry.  With n entries in all:
+ *   sorted_tok[p] = the token of entry p for p < n, -1 up to ntok*topk
+ *                   (qgemm_prefill_experts' sorted_tok, qgemv_grouped_experts' entry_col);
+ *   row_idx[t*topk + k] = the entry's p, or -1                    (qmm_moe_combine's row_idx);
+ *   expert_off[e] = entries of experts below e, e = 0 .. nexperts (qgemm_prefill_experts');
+ *   group_expert[g], group_off[g], g < G = min(nexperts, ntok*topk): the experts that have entries,
+ *                   ascending, and their first entry; beyond them expert -1 and offset n;
+ *                   group_off[G] = n  (qgemv_grouped_experts' groups).  Both NULL: not written.
+ *   ws   : qmm_moe_dispatch_workspace() bytes, 4-byte aligned.
+ *   nexperts 1 .. 1024, topk 1 .. 64, ntok * topk below 2^31.  ntok 0 writes the offsets.
+ * Errors: QMM_EINVAL, QMM_EALIGN, QMM_EUNSUPPORTED, QMM_ESPACE. */
+int qmm_moe_dispatch(const int32_t* ids, int64_t ntok, int topk, int nexperts, int32_t* sorted_tok,
+                     int32_t* row_idx, int32_t* expert_off, int32_t* group_expert, int32_t* group_off,
+                     void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace bytes qmm_lora needs (host); 0 for sizes it does not take. */
+size_t qmm_lora_workspace(int64_t ntok, int max_rank);
+
+/* Low-rank adapters of many requests beside a shared projection (qgemv_dense*, qgemm_dense): tokens
+ * seg_off[s] .. seg_off[s+1]-1 belong to request s and use adapter i = seg_adapter[s]:
+ *   y[t][r] = base[t][r] + scales[i] * sum_j B[i][r][j] * (sum_c A[i][j][c] * x[t][c]),  j < ranks[i]
+ * with binary32 sums; the inner sums enter the outer product with at least 20 bits below the
+ * token's largest one.  A segment whose adapter is outside [0, nadapters) gives y = base.
+ *   x    : QMM_TYPE_F16 or QMM_TYPE_F32 [ntok][ldx], 16-byte aligned, ldx * element size a
+ *          multiple of 16.
+ *   a    : binary16 [nadapters][max_rank][k];  b : binary16 [nadapters][nrows][max_rank]; 16-byte
+ *          aligned.  Rows / columns at ranks[i] and beyond are not used.
+ *   ranks: int32 [nadapters] (clamped to [0, max_rank]);  scales : float [nadapters].
+ *   seg_off : int32 [nseg + 1], non-decreasing (each offset is clamped to [0, ntok]; tokens of no
+ *          segment are not written);  seg_adapter : int32 [nseg].
+ *   base : float [ntok][ldbase], may be y (then ldbase = ldy; segments without adapter are not
+ *          touched);  y : float [ntok][ldy]; strides >= nrows, 4-byte aligned.
+ *   k    : a multiple of 32, at most 32768;  max_rank : a multiple of 8, at most 256.
+ *   ws   : qmm_lora_workspace() bytes, 16-byte aligned.
+ * Errors: QMM_EINVAL, QMM_EALIGN, QMM_EUNSUPPORTED, QMM_ESPACE. */
+int qmm_lora(int xtype, const void* x, int64_t ldx, int64_t ntok, int64_t k, const uint16_t* a,
+             const uint16_t* b, const int32_t* ranks, const float* scales, int nadapters,
+             int max_rank, const int32_t* seg_off, const int32_t* seg_adapter, int nseg,
+             const float* base, int64_t ldbase, float* y, int64_t ldy, int64_t nrows, void* ws,
+             size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

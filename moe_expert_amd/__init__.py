@@ -11,7 +11,9 @@ library's HIP kernels; there is no CPU fallback, and a missing library raises at
 Names follow the C ABI: ``qmm_quantize_q8_1``, ``qmm_dequant_f16``, ``qgemv_dense``,
 ``qgemv_dense_f32``, ``qmm_debug_block_sums``, ``qgemv_grouped_experts``,
 ``qgemm_prefill_experts`` (and the measurement hooks ``qmm_debug_stream_read``,
-``qmm_debug_mfma_loop``).
+``qmm_debug_mfma_loop``); between the products ``qmm_rmsnorm``, ``qmm_dequantize_q8_1``,
+``qmm_moe_route``, ``qmm_moe_dispatch`` and ``qmm_lora``, which also take row-strided views of
+float32, float16 or bfloat16 tensors where their docstrings say so.
 """
 from __future__ import annotations
 
@@ -23,12 +25,16 @@ LIB_PATH = os.path.join(HERE, "libqmm.so")
 
 QMM_Q8_0, QMM_IQ4_NL, QMM_CB3, QMM_F16 = 1, 2, 3, 4
 QMM_FLAG_DEBUG_INTERMEDIATES = 1
+QMM_TYPE_F32, QMM_TYPE_F16, QMM_TYPE_BF16 = 1, 2, 3
+QMM_SCORE_SOFTMAX, QMM_SCORE_SIGMOID = 0, 1
+QMM_ROUTE_RENORM = 1
 BLOCK_VALUES = {QMM_Q8_0: 32, QMM_IQ4_NL: 32, QMM_CB3: 256, QMM_F16: 1}
 BLOCK_BYTES = {QMM_Q8_0: 34, QMM_IQ4_NL: 18, QMM_CB3: 110, QMM_F16: 2}
 Q8_1_BYTES = 36
 GRID_BYTES = 2048
 
-_P, _I64, _I32, _U32, _U64, _SZ = C.c_void_p, C.c_int64, C.c_int, C.c_uint, C.c_uint64, C.c_size_t
+_P, _I64, _I32, _U32, _U64, _SZ, _F32 = (C.c_void_p, C.c_int64, C.c_int, C.c_uint, C.c_uint64, C.c_size_t,
+                                         C.c_float)
 SIGNATURES = {
     "qmm_version": (_I32, []),
     "qmm_status_str": (C.c_char_p, [_I32]),
@@ -58,6 +64,14 @@ SIGNATURES = {
     "qgemm_prefill_experts_workspace": (_SZ, [_I32, _I64, _I64, _U32]),
     "qgemm_prefill_experts": (_I32, [_I32, _P, _P, _I64, _I32, _P, _I64, _I32, _I64, _I64, _P, _I64,
                                      _P, _P, _I64, _P, _P, _SZ, _U32, _P]),
+    "qmm_rmsnorm": (_I32, [_I32, _P, _I64, _I32, _P, _I64, _P, _I64, _P, _F32, _I64, _I64, _I32, _P, _I64, _P, _P]),
+    "qmm_dequantize_q8_1": (_I32, [_P, _I64, _I64, _I32, _P, _I64, _P]),
+    "qmm_moe_route": (_I32, [_I32, _P, _I64, _P, _I64, _I32, _I32, _I32, _I32, _I32, _I32, _F32, _P, _P, _U32, _P]),
+    "qmm_moe_dispatch_workspace": (_SZ, [_I64, _I32, _I32]),
+    "qmm_moe_dispatch": (_I32, [_P, _I64, _I32, _I32, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "qmm_lora_workspace": (_SZ, [_I64, _I32]),
+    "qmm_lora": (_I32, [_I32, _P, _I64, _I64, _I64, _P, _P, _P, _P, _I32, _I32, _P, _P, _I32, _P, _I64, _P, _I64, _I64,
+                        _P, _SZ, _P]),
 }
 
 _lib = None
@@ -517,3 +531,235 @@ def qgemm_prefill_experts_q8(wtype_gu, w_gate, w_up, wtype_down, w_down, nexpert
         _ptr(x_f16), ntok, _ptr(sorted_tok), _ptr(expert_off), nentries, _ptr(y), _ptr(ws), _nbytes(ws), flags,
         _stream(stream, dev)))
     return y, ws
+
+
+# ------------------------------------------------------------------ between the products
+#
+# These entry points launch kernels of a few microseconds, so their checks read each tensor's
+# attributes once.
+
+_TYPE_OF = None
+
+
+def _type_of(dtype):
+    """QMM_TYPE_* of a torch dtype, 0 if the kernels do not take it."""
+    global _TYPE_OF
+    if _TYPE_OF is None:
+        import torch
+        _TYPE_OF = {torch.float32: QMM_TYPE_F32, torch.float16: QMM_TYPE_F16, torch.bfloat16: QMM_TYPE_BF16}
+    return _TYPE_OF.get(dtype, 0)
+
+
+def _rows(t, name, ntok, ncols, device, types=(QMM_TYPE_F32, QMM_TYPE_F16, QMM_TYPE_BF16)):
+    """t must be a [ntok, ncols] GPU tensor of one of `types` whose rows are contiguous and do not
+    overlap (any row stride of at least ncols); returns (type code, row stride)."""
+    if not getattr(t, "is_cuda", False):
+        raise ValueError(f"{name} must be a GPU tensor")
+    if tuple(t.shape) != (ntok, ncols):
+        raise ValueError(f"{name} must be [{ntok}, {ncols}], not {list(t.shape)}")
+    code = _type_of(t.dtype)
+    if code not in types:
+        raise ValueError(f"{name} has dtype {t.dtype}, which this call does not take")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the call runs on {device}")
+    ld, step = t.stride()
+    if ntok <= 1:
+        ld = ncols  # the one row's stride says nothing
+    if (step != 1 and ncols > 1) or ld < ncols:
+        raise ValueError(f"{name} must have contiguous rows that do not overlap")
+    return code, ld
+
+
+def _call(fn, device, stream, *args):
+    """Call a library function on `device`'s current stream (or the one given)."""
+    import torch
+    if device.index is not None and device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            rc = getattr(lib(), fn)(*args, _stream(stream, device))
+    else:
+        rc = getattr(lib(), fn)(*args, _stream(stream, device))
+    if rc != 0:
+        raise QmmError(fn, rc)
+
+
+def _scratch(ws, nbytes, device, stream):
+    """A caller's workspace (checked), or a new one that stays reserved for the stream it is used on."""
+    import torch
+    if ws is not None:
+        return _need(ws, "ws", "u8", nbytes, device)
+    ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+    if stream is not None:
+        ws.record_stream(torch.cuda.ExternalStream(stream, device=device))
+    return ws
+
+
+def qmm_rmsnorm(x, w, eps, res=None, res_out=None, y=None, yq=None, stream=None):
+    """Root-mean-square norm of r = x + res (or of x), y = r / sqrt(mean r^2 + eps) * w.
+
+    x, res: [ntok, hidden] float32, float16 or bfloat16 with any row stride; w: float32 [hidden].
+    Outputs, at least one: y, a tensor or a dtype for a new one; yq, a uint8 tensor of ntok rows of
+    hidden/32*36 bytes or True for a new one (q8_1 of the float32 y, for the decode products);
+    res_out, a tensor of res' dtype (of any dtype without res) that takes r, res itself for an
+    update in place.  Returns (y, yq, res_out), None for those not asked for."""
+    import torch
+    if getattr(x, "dim", lambda: 0)() != 2:
+        raise ValueError("x must be [ntok, hidden]")
+    ntok, hidden = x.shape
+    dev = x.device
+    if hidden < 1:
+        raise ValueError("hidden must be positive")
+    if y is None and yq is None and res_out is None:
+        raise ValueError("no output asked for")
+    xt, ldx = _rows(x, "x", ntok, hidden, dev)
+    _need(w, "w", "f32", hidden * 4, dev)
+    rt = ldr = ldro = yt = ldy = 0
+    if res is not None:
+        rt, ldr = _rows(res, "res", ntok, hidden, dev)
+    if res_out is not None:
+        ot, ldro = _rows(res_out, "res_out", ntok, hidden, dev)
+        if rt and ot != rt:
+            raise ValueError("res_out must have res' dtype")
+        rt = ot
+    if y is not None:
+        if isinstance(y, torch.dtype):
+            y = torch.empty((ntok, hidden), dtype=y, device=dev)
+        yt, ldy = _rows(y, "y", ntok, hidden, dev)
+    if yq is not None:
+        if hidden % 32:
+            raise ValueError(f"hidden={hidden} is not a multiple of 32")
+        nbytes = ntok * (hidden // 32) * Q8_1_BYTES
+        if yq is True:
+            yq = torch.empty((ntok, (hidden // 32) * Q8_1_BYTES), dtype=torch.uint8, device=dev)
+        _need(yq, "yq", "u8", nbytes, dev)
+    _call("qmm_rmsnorm", dev, stream, xt, x.data_ptr(), ldx, rt, _addr(res), ldr, _addr(res_out), ldro, w.data_ptr(), eps,
+          ntok, hidden, yt, _addr(y), ldy, _addr(yq))
+    return y, yq, res_out
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def qmm_dequantize_q8_1(xq, k, out=None, stream=None):
+    """The values of q8_1 columns: xq uint8 [ncols, k/32*36] -> out [ncols, k], float32 or float16
+    (a tensor with any row stride, a dtype for a new one, None for float32)."""
+    import torch
+    if k < 32 or k % 32:
+        raise ValueError(f"k={k} is not a positive multiple of 32")
+    _need(xq, "xq", "u8", 0)
+    col = (k // 32) * Q8_1_BYTES
+    if _nbytes(xq) % col:
+        raise ValueError("xq must hold whole q8_1 columns of width k")
+    ncols, dev = _nbytes(xq) // col, xq.device
+    if out is None or isinstance(out, torch.dtype):
+        out = torch.empty((ncols, k), dtype=out or torch.float32, device=dev)
+    ot, ldo = _rows(out, "out", ncols, k, dev, (QMM_TYPE_F32, QMM_TYPE_F16))
+    _call("qmm_dequantize_q8_1", dev, stream, xq.data_ptr(), k, ncols, ot, out.data_ptr(), ldo)
+    return out
+
+
+def qmm_moe_route(logits, topk, score=QMM_SCORE_SOFTMAX, bias=None, ngroups=1, topk_groups=1, group_top=1, renorm=True,
+                  scale=1.0, ids=None, weights=None, stream=None):
+    """Experts of each token: logits [ntok, nexperts] (float32, float16 or bfloat16, any row stride)
+    -> (ids int32 [ntok, topk], weights float32 [ntok, topk]), best first, ties to the lowest expert.
+
+    Scores are the softmax or the sigmoid of the logits; experts are chosen by score + bias (float32
+    [nexperts]) among the topk_groups best of ngroups runs of experts, a run rated by the sum of its
+    group_top best; weights are the chosen scores, divided by their sum if renorm, times scale.
+    Experts whose logit is -inf or NaN are never chosen; missing choices are id -1, weight 0."""
+    import torch
+    if getattr(logits, "dim", lambda: 0)() != 2:
+        raise ValueError("logits must be [ntok, nexperts]")
+    ntok, nexperts = logits.shape
+    dev = logits.device
+    lt, ldl = _rows(logits, "logits", ntok, nexperts, dev)
+    if topk < 1 or max(topk, ngroups, topk_groups, group_top) > 0x7FFFFFFF:
+        raise ValueError("topk must be positive, and every count an int32")
+    if bias is not None:
+        _need(bias, "bias", "f32", nexperts * 4, dev)
+    ids = _out(ids, "ids", "i32", ntok * topk * 4, dev, (ntok, topk), torch.int32)
+    weights = _out(weights, "weights", "f32", ntok * topk * 4, dev, (ntok, topk), torch.float32)
+    _call("qmm_moe_route", dev, stream, lt, logits.data_ptr(), ldl, _addr(bias), ntok, nexperts, score, ngroups, topk_groups,
+          group_top, topk, scale, ids.data_ptr(), weights.data_ptr(), QMM_ROUTE_RENORM if renorm else 0)
+    return ids, weights
+
+
+def qmm_moe_dispatch_workspace(ntok, topk, nexperts):
+    return int(lib().qmm_moe_dispatch_workspace(ntok, topk, nexperts))
+
+
+def qmm_moe_dispatch(ids, nexperts, sorted_tok=None, row_idx=None, expert_off=None, group_expert=None, group_off=None,
+                     ws=None, stream=None):
+    """The entry lists of a routing: ids int32 [ntok, topk] (an id outside [0, nexperts) adds no
+    entry) -> (sorted_tok [ntok*topk], row_idx [ntok, topk], expert_off [nexperts+1],
+    group_expert [G], group_off [G+1]) with G = min(nexperts, ntok*topk), all int32:
+
+    qgemm_prefill_experts takes sorted_tok and expert_off, qgemv_grouped_experts group_expert,
+    group_off and sorted_tok (as entry_col), qmm_moe_combine row_idx.  Entries are ordered by expert,
+    then token, then k; sorted_tok is -1 past the last entry, row_idx -1 where there is none."""
+    import torch
+    if getattr(ids, "dim", lambda: 0)() != 2:
+        raise ValueError("ids must be [ntok, topk]")
+    ntok, topk = ids.shape
+    dev = ids.device
+    n = ntok * topk
+    g = min(nexperts, n)
+    _need(ids, "ids", "i32", n * 4)
+    if not 0 < nexperts <= 0x7FFFFFFF or topk < 1:
+        raise ValueError("nexperts and topk must be positive, nexperts an int32")
+    if (group_expert is None) != (group_off is None):
+        raise ValueError("group_expert and group_off go together")
+    i32 = torch.int32
+    sorted_tok = _out(sorted_tok, "sorted_tok", "i32", n * 4, dev, (n,), i32)
+    row_idx = _out(row_idx, "row_idx", "i32", n * 4, dev, (ntok, topk), i32)
+    expert_off = _out(expert_off, "expert_off", "i32", (nexperts + 1) * 4, dev, (nexperts + 1,), i32)
+    group_expert = _out(group_expert, "group_expert", "i32", g * 4, dev, (g,), i32)
+    group_off = _out(group_off, "group_off", "i32", (g + 1) * 4, dev, (g + 1,), i32)
+    ws = _scratch(ws, qmm_moe_dispatch_workspace(ntok, topk, nexperts), dev, stream)
+    _call("qmm_moe_dispatch", dev, stream, ids.data_ptr(), ntok, topk, nexperts, sorted_tok.data_ptr(), row_idx.data_ptr(),
+          expert_off.data_ptr(), group_expert.data_ptr(), group_off.data_ptr(), ws.data_ptr(), _nbytes(ws))
+    return sorted_tok, row_idx, expert_off, group_expert, group_off
+
+
+def qmm_lora_workspace(ntok, max_rank):
+    return int(lib().qmm_lora_workspace(ntok, max_rank))
+
+
+def qmm_lora(x, a, b, ranks, scales, seg_off, seg_adapter, y, base=None, ws=None, stream=None):
+    """Low-rank adapters beside a shared projection: y[t] = base[t] + scales[i] * b[i] (a[i] x[t]),
+    i = seg_adapter[s] for the tokens seg_off[s] .. seg_off[s+1]-1 (an i outside the adapters:
+    y = base).  base None: y itself, updated in place.
+
+    x: float16 or float32 [ntok, k], rows 16-byte aligned; a: float16 [nadapters, max_rank, k], b:
+    float16 [nadapters, nrows, max_rank], of which the first ranks[i] (int32) rows / columns are
+    used; scales: float32 [nadapters]; seg_off: int32 [nseg+1]; seg_adapter: int32 [nseg]; y, base:
+    float32 [ntok, nrows] with any row stride.  Returns y."""
+    if getattr(x, "dim", lambda: 0)() != 2 or getattr(a, "dim", lambda: 0)() != 3 or getattr(b, "dim", lambda: 0)() != 3:
+        raise ValueError("x must be [ntok, k], a [nadapters, max_rank, k], b [nadapters, nrows, max_rank]")
+    ntok, k = x.shape
+    na, max_rank, ka = a.shape
+    nrows = b.shape[1]
+    dev = x.device
+    if ka != k or tuple(b.shape) != (na, nrows, max_rank):
+        raise ValueError("a must be [nadapters, max_rank, k] and b [nadapters, nrows, max_rank]")
+    xt, ldx = _rows(x, "x", ntok, k, dev, (QMM_TYPE_F16, QMM_TYPE_F32))
+    for t, name in ((a, "a"), (b, "b")):
+        _need(t, name, "f16", na * max_rank * 2, dev)
+        if _type_of(t.dtype) != QMM_TYPE_F16:
+            raise ValueError(f"{name} must be float16")
+    _need(ranks, "ranks", "i32", na * 4, dev)
+    _need(scales, "scales", "f32", na * 4, dev)
+    nseg = int(seg_adapter.numel())
+    _need(seg_adapter, "seg_adapter", "i32", nseg * 4, dev)
+    _need(seg_off, "seg_off", "i32", (nseg + 1) * 4, dev)
+    _, ldy = _rows(y, "y", ntok, nrows, dev, (QMM_TYPE_F32,))
+    ldb = ldy
+    if base is None:
+        base = y
+    else:
+        _, ldb = _rows(base, "base", ntok, nrows, dev, (QMM_TYPE_F32,))
+    ws = _scratch(ws, qmm_lora_workspace(ntok, max_rank), dev, stream)
+    _call("qmm_lora", dev, stream, xt, x.data_ptr(), ldx, ntok, k, a.data_ptr(), b.data_ptr(), ranks.data_ptr(),
+          scales.data_ptr(), na, max_rank, seg_off.data_ptr(), seg_adapter.data_ptr(), nseg, base.data_ptr(), ldb,
+          y.data_ptr(), ldy, nrows, ws.data_ptr(), _nbytes(ws))
+    return y
