@@ -127,10 +127,16 @@ def _check(fn, rc):
 # The C library takes plain pointers and sizes and cannot see the allocations behind them, so
 # every tensor is checked here against what the call will touch.
 
+_DTYPES = {}
+
+
 def _dtypes(kind):
-    import torch
-    return {"u8": (torch.uint8,), "f32": (torch.float32,), "i32": (torch.int32,),
-            "f16": tuple(d for d in (torch.float16, torch.int16, getattr(torch, "uint16", None)) if d is not None)}[kind]
+    if not _DTYPES:
+        import torch
+        _DTYPES.update({"u8": (torch.uint8,), "f32": (torch.float32,), "i32": (torch.int32,),
+                        "f16": tuple(d for d in (torch.float16, torch.int16, getattr(torch, "uint16", None))
+                                     if d is not None)})
+    return _DTYPES[kind]
 
 
 def _nbytes(t) -> int:
@@ -555,12 +561,12 @@ def _rows(t, name, ntok, ncols, device, types=(QMM_TYPE_F32, QMM_TYPE_F16, QMM_T
     overlap (any row stride of at least ncols); returns (type code, row stride)."""
     if not getattr(t, "is_cuda", False):
         raise ValueError(f"{name} must be a GPU tensor")
-    if tuple(t.shape) != (ntok, ncols):
+    if t.shape != (ntok, ncols):
         raise ValueError(f"{name} must be [{ntok}, {ncols}], not {list(t.shape)}")
     code = _type_of(t.dtype)
     if code not in types:
         raise ValueError(f"{name} has dtype {t.dtype}, which this call does not take")
-    if device is not None and t.device != device:
+    if t.device != device:
         raise ValueError(f"{name} is on {t.device}, the call runs on {device}")
     ld, step = t.stride()
     if ntok <= 1:
@@ -573,11 +579,17 @@ def _rows(t, name, ntok, ncols, device, types=(QMM_TYPE_F32, QMM_TYPE_F16, QMM_T
 def _call(fn, device, stream, *args):
     """Call a library function on `device`'s current stream (or the one given)."""
     import torch
-    if device.index is not None and device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            rc = getattr(lib(), fn)(*args, _stream(stream, device))
+    here = torch.cuda.current_device()
+    at = here if device.index is None else device.index
+    if stream is None:
+        # the current stream's handle without the Stream object (2 us) where torch has it
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        stream = raw(at) if raw else torch.cuda.current_stream(device).cuda_stream
+    if at != here:
+        with torch.cuda.device(at):
+            rc = getattr(lib(), fn)(*args, stream)
     else:
-        rc = getattr(lib(), fn)(*args, _stream(stream, device))
+        rc = getattr(lib(), fn)(*args, stream)
     if rc != 0:
         raise QmmError(fn, rc)
 

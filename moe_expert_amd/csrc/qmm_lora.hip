@@ -3,7 +3,13 @@
 //
 // Two launches, each over tiles of the tokens of one segment (found by a scan of the segments, so
 // their lengths stay on the device): the inner values v = A_i x[t] in binary32 into the workspace,
-// then the outer product added to the base.
+// then the outer product added to the base.  (Both in one launch, each workgroup forming the inner
+// values for itself, measured slower: 9.4 against 8.0 us for 8 requests of one token at rank 16,
+// k 2560, 8192 rows; 40 against 13 us at rank 64, k 6144, 2560 rows.)
+//
+// Bound: the base and y.  8192 tokens x (2560 -> 8192), rank 16: 130 us for the 582 MB that cannot be
+// avoided (4.5 TB/s, a large copy reaches 5.0), of which the inner values 18 us; short calls are
+// bound by the chain of dependent loads segment -> adapter -> A, x -> inner values -> y.
 #include "qmm_values.h"
 
 namespace qmm {
@@ -26,6 +32,7 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 struct LoraTile {
     int t0, nt, adapter, rank;  // nt = 0: no such tile
+    float scale;
 };
 
 // Tile `tile` of the segments' tiles of T tokens each (the last of a segment holds what is left):
@@ -39,6 +46,14 @@ __device__ __forceinline__ LoraTile find_tile(const LoraArgs& a, int T, int tile
             o0 = a.seg_off[s];
             o1 = a.seg_off[s + 1];
             i = a.seg_adapter[s];
+        }
+        int rank = 0;
+        float scale = 0.0f;
+        if (i >= 0 && i < a.nadapters) {  // on their way during the scan
+            rank = a.ranks[i];
+            scale = a.scales[i];
+        } else {
+            i = -1;
         }
         o0 = o0 < 0 ? 0 : o0 > a.ntok ? a.ntok : o0;
         o1 = o1 < o0 ? o0 : o1 > a.ntok ? a.ntok : o1;
@@ -56,160 +71,130 @@ __device__ __forceinline__ LoraTile find_tile(const LoraArgs& a, int T, int tile
             const int left = __builtin_amdgcn_readlane(o1, src) - r.t0;
             r.nt = left < T ? left : T;
             r.adapter = __builtin_amdgcn_readlane(i, src);
-            if (r.adapter < 0 || r.adapter >= a.nadapters) r.adapter = -1;
-            r.rank = r.adapter < 0 ? 0 : a.ranks[r.adapter];
+            r.rank = __builtin_amdgcn_readlane(rank, src);
             r.rank = r.rank < 0 ? 0 : r.rank > a.max_rank ? a.max_rank : r.rank;
+            r.scale = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, scale), src));
             return r;
         }
         tile -= __builtin_amdgcn_readlane(end, 63);
     }
-    return {0, 0, -1, 0};
+    return {0, 0, -1, 0, 0.0f};
 }
 
 // ------------------------------------------------------------------ inner values
 
-// One step of 32 columns: 8 values of x for each of MT token rows, 8 values of A for each of NR
+// One step of 32 columns: 8 values of x of a token row, 8 values of A of each of NR blocks of 16
 // rank rows; lane l holds row l % 16 and columns 8 (l / 16) .. + 7 of the step.
-template <int XT, int NR, int MT>
+template <int XT, int NR>
 struct DownStep {
-    u32x4 x[MT][XT == kF32 ? 2 : 1];
+    u32x4 x[XT == kF32 ? 2 : 1];
     u32x4 a[NR];
 };
 
-// Workgroup (tile, split): W waves over the tile's 16 MT tokens and 16 NR rank rows, each wave a run
-// of the split's 32-column steps, summed through LDS in wave order.  Rows past the tile or the rank
-// read the last valid row; their sums are not stored (or stored as 0).
-template <int XT, int NR, int MT, int W>
-__global__ __launch_bounds__(64 * W) void lora_down_kernel(LoraArgs a) {
-    constexpr int T = 16 * MT, R = 16 * NR, U = NR <= 4 ? 4 : 2;
-    __shared__ float part[W][T][R + 1];
-    const LoraTile tile = find_tile(a, T, blockIdx.x);
-    if (tile.nt == 0 || tile.rank == 0) return;
-    const int w = threadIdx.x >> 6, l = threadIdx.x & 63, row = l & 15, q = l >> 4;
-    const char* xr[MT];
+// The inner values of a tile of up to 16 tokens into part[wave][token][rank row], each wave the
+// sum over its run of 32-column steps (wave `run` of `runs`).  Rows past the tile or the rank read
+// the last valid row; what they give is not used.
+template <int XT, int NR, int LD>
+__device__ __forceinline__ void down_tile(const LoraArgs& a, const LoraTile& tile, int run, int runs, float (*part)[LD]) {
+    constexpr int U = NR <= 2 ? 8 : NR <= 4 ? 4 : 2;  // steps whose loads are in flight together
+    const int l = threadIdx.x & 63, row = l & 15, q = l >> 4;
+    const char* xr = (const char*)a.x + ((int64_t)(tile.t0 + (row < tile.nt ? row : tile.nt - 1)) * a.ldx + 8 * q) * (XT == kF32 ? 4 : 2);
     const uint16_t* ar[NR];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        const int t = 16 * m + row;
-        xr[m] = (const char*)a.x + ((int64_t)(tile.t0 + (t < tile.nt ? t : tile.nt - 1)) * a.ldx + 8 * q) * (XT == kF32 ? 4 : 2);
-    }
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
         const int j = 16 * n + row;
         ar[n] = a.a + ((int64_t)tile.adapter * a.max_rank + (j < tile.rank ? j : tile.rank - 1)) * a.k + 8 * q;
     }
-    const int steps = a.k / 32, runs = W * a.split;
+    const int steps = a.k / 32;
     const int per = (steps + runs - 1) / runs;
-    const int c0 = ((int)blockIdx.y * W + w) * per, c1 = c0 + per < steps ? c0 + per : steps;
+    const int c0 = run * per, c1 = c0 + per < steps ? c0 + per : steps;
 
-    f32x4 acc[MT][NR];
+    f32x4 acc[NR];
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int n = 0; n < NR; ++n) acc[m][n] = f32x4{};
+    for (int n = 0; n < NR; ++n) acc[n] = f32x4{};
 
-    auto load = [&](DownStep<XT, NR, MT>& s, int c) {
-        c = c < c1 ? c : c1 - 1;
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            const u32x4* p = (const u32x4*)(xr[m] + (int64_t)c * (XT == kF32 ? 128 : 64));
-            s.x[m][0] = p[0];
-            if constexpr (XT == kF32) s.x[m][1] = p[1];
-        }
+    auto load = [&](DownStep<XT, NR>& s, int c) {
+        const u32x4* p = (const u32x4*)(xr + (int64_t)c * (XT == kF32 ? 128 : 64));
+        s.x[0] = p[0];
+        if constexpr (XT == kF32) s.x[1] = p[1];
 #pragma unroll
         for (int n = 0; n < NR; ++n) s.a[n] = *(const u32x4*)(ar[n] + (int64_t)c * 32);
     };
-    auto apply = [&](const DownStep<XT, NR, MT>& s) {
+    auto apply = [&](const DownStep<XT, NR>& s) {
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
             const half8 b = __builtin_bit_cast(half8, s.a[n]);
+            if constexpr (XT == kF32) {
+                const f32x4 x0 = __builtin_bit_cast(f32x4, s.x[0]), x1 = __builtin_bit_cast(f32x4, s.x[1]);
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                if constexpr (XT == kF32) {
-                    const f32x4 x0 = __builtin_bit_cast(f32x4, s.x[m][0]), x1 = __builtin_bit_cast(f32x4, s.x[m][1]);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        acc[m][n] = __builtin_amdgcn_mfma_f32_16x16x4f32(e < 4 ? x0[e] : x1[e - 4], (float)b[e], acc[m][n], 0, 0, 0);
-                } else {
-                    acc[m][n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8, s.x[m][0]), b, acc[m][n], 0, 0, 0);
-                }
+                for (int e = 0; e < 8; ++e)
+                    acc[n] = __builtin_amdgcn_mfma_f32_16x16x4f32(e < 4 ? x0[e] : x1[e - 4], (float)b[e], acc[n], 0, 0, 0);
+            } else {
+                acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8, s.x[0]), b, acc[n], 0, 0, 0);
             }
         }
     };
-    if (c0 < c1) {
-        for (int c = c0; c < c1; c += U) {
-            DownStep<XT, NR, MT> s[U];
+    for (int c = c0; c < c1; c += U) {
+        DownStep<XT, NR> s[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u) load(s[u], c + u);
+        for (int u = 0; u < U; ++u)
+            if (c + u < c1) load(s[u], c + u);
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (c + u < c1) apply(s[u]);
-        }
+        for (int u = 0; u < U; ++u)
+            if (c + u < c1) apply(s[u]);
     }
     // accumulator register r of lane l: token 4 (l / 16) + r, rank row l % 16
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int n = 0; n < NR; ++n)
 #pragma unroll
-        for (int n = 0; n < NR; ++n)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) part[w][16 * m + 4 * q + r][16 * n + row] = acc[m][n][r];
+        for (int r = 0; r < 4; ++r) part[4 * q + r][16 * n + row] = acc[n][r];
+}
+
+// The same for the blocks of 16 rank rows that the adapter uses, 1, 2, 4, ... up to the table's NR.
+template <int XT, int NR, int LD>
+__device__ __forceinline__ void down_tile_ranks(const LoraArgs& a, const LoraTile& tile, int run, int runs, float (*part)[LD]) {
+    if constexpr (NR > 1) {
+        if (tile.rank <= 8 * NR) return down_tile_ranks<XT, NR / 2, LD>(a, tile, run, runs, part);
+    }
+    down_tile<XT, NR, LD>(a, tile, run, runs, part);
+}
+
+// Workgroup (tile, split): the waves' sums joined in wave order into the split's inner values.
+template <int XT, int NR, int W>
+__global__ __launch_bounds__(64 * W) void lora_down_kernel(LoraArgs a) {
+    constexpr int T = 16, R = 16 * NR;
+    __shared__ float part[W][T][R + 1];
+    const LoraTile tile = find_tile(a, T, blockIdx.x);
+    if (tile.nt == 0 || tile.rank == 0) return;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    down_tile_ranks<XT, NR, R + 1>(a, tile, (int)blockIdx.y * W + w, W * a.split, part[w]);
     __syncthreads();
     float* v = a.v + ((int64_t)blockIdx.y * a.ntok + tile.t0) * a.max_rank;
     for (int i = threadIdx.x; i < tile.nt * R; i += 64 * W) {
         const int t = i / R, j = i % R;
+        if (j >= ((tile.rank + 7) & ~7)) continue;  // the outer product reads whole groups of 8
         float s = part[0][t][j];
 #pragma unroll
         for (int u = 1; u < W; ++u) s += part[u][t][j];
-        if (j < a.max_rank) v[(int64_t)t * a.max_rank + j] = j < tile.rank ? s : 0.0f;
+        v[(int64_t)t * a.max_rank + j] = j < tile.rank ? s : 0.0f;
     }
 }
 
 // ------------------------------------------------------------------ outer product
 
-constexpr int kUpRows = 256;  // rows of y per workgroup: 4 waves of two 32-row blocks
+constexpr int kUpTokens = 32, kUpRows = 256;  // of y per workgroup: one block of 64 rows a wave
 
-// Workgroup (row block, tile): NT blocks of 32 tokens by 256 rows of y.  The inner values (the sum
-// of the splits) are scaled per token by the power of two that puts the largest into [512, 1024)
-// and cut into binary16 high and low parts, v = hi + lo to 2^-24 of the largest, so the product
-// with B runs on binary16 MFMA with nothing lost to range: acc = hi B + lo B, y = base +
-// acc * (scale 2^e).
-template <int NT>
-__global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs a) {
-    constexpr int T = 32 * NT, G = 256 / T;  // G threads per token in the prologue
-    constexpr int MAXG = 4;                  // 8-rank groups per thread there
-    extern __shared__ u32x4 frag[];          // [hi, lo][step][half][token]
-    __shared__ uint32_t largest[T];
-    __shared__ float factor[T];
-    const LoraTile tile = find_tile(a, T, blockIdx.y);
-    if (tile.nt == 0) return;
-    const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, col = l & 31, h = l >> 5;
-    const int r0 = (int)blockIdx.x * kUpRows;
-    const float* base = a.base + (int64_t)tile.t0 * a.ldbase + r0;
-    float* y = a.y + (int64_t)tile.t0 * a.ldy + r0;
-    const int rows = a.nrows - r0 < kUpRows ? a.nrows - r0 : kUpRows;
-    if (tile.rank == 0) {  // no adapter: y = base
-        if (base == y && a.ldbase == a.ldy) return;
-        if (tid < rows)
-            for (int t = 0; t < tile.nt; ++t) y[t * a.ldy + tid] = base[t * a.ldbase + tid];
-        return;
-    }
-    const int steps = (tile.rank + 15) / 16;
-
-    // base: register r of token block n, row block c: token 32 n + 8 (r / 4) + 4 h + r % 4
-    float in[NT][2][16];
-    const bool full = tile.nt == T && rows == kUpRows;
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int t = 32 * n + 8 * (r / 4) + 4 * h + r % 4, j = 64 * w + 32 * c + col;
-                in[n][c][r] = full || (t < tile.nt && j < rows) ? base[t * a.ldbase + j] : 0.0f;
-            }
-
-    // inner values -> high and low parts
-    const int tok = tid % T, g0 = tid / T;
+// The inner values of a tile as binary16 fragments in LDS.  Each token's are scaled by the power of
+// two that puts the largest into [512, 1024) and cut into high and low parts, v = hi + lo to 2^-24
+// of the largest, so that the product with B runs on binary16 MFMA with nothing lost to its range:
+// acc = hi B + lo B, y = base + acc * factor, factor = scale 2^e.  frag: [hi, lo][step][half][token],
+// 8 consecutive ranks each.  fetch(token, j, v) adds the values j .. j+7 of a token to v.
+template <class F>
+__device__ __forceinline__ void make_fragments(const LoraTile& tile, u32x4* frag, uint32_t* largest, float* factor, F fetch) {
+    constexpr int T = kUpTokens, G = 256 / T;  // G threads per token
+    constexpr int MAXG = kLoraMaxRank / 8 / G;
+    const int tid = threadIdx.x, tok = tid % T, g0 = tid / T, steps = (tile.rank + 15) / 16;
+    if (tid < T) largest[tid] = 0;
     float v[MAXG][8];
     uint32_t big = 0;
 #pragma unroll
@@ -218,26 +203,21 @@ __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs a) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[i][e] = 0.0f;
         if (tok < tile.nt && j < tile.rank) {
-            for (int s = 0; s < a.split; ++s) {
-                const f32x4* p = (const f32x4*)(a.v + ((int64_t)s * a.ntok + tile.t0 + tok) * a.max_rank + j);
-                const f32x4 lo = p[0], hi = p[1];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[i][e] += e < 4 ? lo[e] : hi[e - 4];
-            }
+            fetch(tok, j, v[i]);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
+                if (j + e >= tile.rank) v[i][e] = 0.0f;
                 const uint32_t b = __builtin_bit_cast(uint32_t, v[i][e]) & 0x7FFFFFFFu;
                 if (b < 0x7F800000u && b > big) big = b;  // infinities and NaN keep to themselves
             }
         }
     }
-    if (tid < T) largest[tid] = 0;
     __syncthreads();
-    atomicMax(&largest[tok], big);
+    if (big) atomicMax(&largest[tok], big);
     __syncthreads();
     // the largest is in [2^ex, 2^(ex+1)) or subnormal; no scaling where there is no finite one but 0
     const int ex = largest[tok] ? (int)(largest[tok] >> 23) - 127 : 9;
-    if (tid < T) factor[tid] = ldexpf(a.scales[tile.adapter], ex - 9);
+    if (tid < T) factor[tid] = ldexpf(tile.scale, ex - 9);
     const int part = steps * 2 * T;
 #pragma unroll
     for (int i = 0; i < MAXG; ++i) {
@@ -255,49 +235,149 @@ __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs a) {
         }
     }
     __syncthreads();
+}
 
-    f32x16 acc[NT][2];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) acc[n][c] = f32x16{};
-    const uint16_t* br[2];
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-        const int j = 64 * w + 32 * c + col;
-        br[c] = a.b + ((int64_t)tile.adapter * a.nrows + r0 + (j < rows ? j : rows - 1)) * a.max_rank;
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+// A wave's block of y: the tile's 32 tokens by 64 rows (from row rb of the workgroup's).  Column l % 32
+// of product c takes row 2 (l % 32) + c, so a lane holds two neighbouring values of each token:
+// register r is token 8 (r / 4) + 4 (l / 32) + r % 4.  Every load is unconditional, at a clamped place
+// where the block ends inside the tile or the rows (with a branch around each load the wave waited
+// for one before the next: 8192 x 8192 took 190 us against 123).  VEC: an even number of rows, aligned.
+template <bool VEC>
+struct UpBlock {
+    static constexpr int CT = 2;
+    f32x2 in[16];
+    half8 b[2][CT];  // the next two 16-rank steps of B
+    const uint16_t* br[CT];
+    int j, h, col, rows;
+
+    __device__ __forceinline__ UpBlock(int rb, int rows_) : rows(rows_) {
+        const int l = threadIdx.x & 63;
+        col = l & 31;
+        h = l >> 5;
+        j = rb + CT * col;
     }
-    for (int s = 0; s < steps; ++s) {
-        const int j = 16 * s + 8 * h;
-        half8 b[2];
+    __device__ __forceinline__ int token(int r) const { return 8 * (r / 4) + 4 * h + r % 4; }
+    // steps s and s + 1 (those there are) of B, as they lie there
+    __device__ __forceinline__ void load_b(const LoraArgs& a, int s, int steps) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            b[c] = *(const half8*)(br[c] + (j < a.max_rank ? j : 0));
-            if (16 * s + 16 > tile.rank) {  // columns past the rank may hold anything
+        for (int u = 0; u < 2; ++u) {
+            if (s + u >= steps) break;
+            const int k = 16 * (s + u) + 8 * h;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) b[c][e] = j + e < tile.rank ? b[c][e] : (_Float16)0.0f;
+            for (int c = 0; c < CT; ++c) b[u][c] = *(const half8*)(br[c] + (k < a.max_rank ? k : 0));
+        }
+    }
+    __device__ __forceinline__ void load(const LoraArgs& a, const LoraTile& tile, int r0, const float* base) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const int t = token(r);
+            const float* p = base + (uint64_t)(uint32_t)(t < tile.nt ? t : tile.nt - 1) * (uint32_t)a.ldbase;
+            if constexpr (VEC) {
+                in[r] = __builtin_nontemporal_load((const f32x2*)(p + (j < rows ? j : 0)));
+            } else {
+#pragma unroll
+                for (int c = 0; c < CT; ++c) in[r][c] = p[j + c < rows ? j + c : rows - 1];
             }
         }
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const half8 hi = __builtin_bit_cast(half8, frag[(2 * s + h) * T + 32 * n + col]);
-            const half8 lo = __builtin_bit_cast(half8, frag[part + (2 * s + h) * T + 32 * n + col]);
+        for (int c = 0; c < CT; ++c)
+            br[c] = a.b + ((int64_t)tile.adapter * a.nrows + r0 + (j + c < rows ? j + c : rows - 1)) * a.max_rank;
+        load_b(a, 0, (tile.rank + 15) / 16);
+    }
+    __device__ __forceinline__ void multiply_store(const LoraArgs& a, const LoraTile& tile, const u32x4* frag,
+                                                   const float* factor, float* y) {
+        constexpr int T = kUpTokens;
+        const int steps = (tile.rank + 15) / 16, part = steps * 2 * T;
+        f32x16 acc[CT];
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                acc[n][c] = __builtin_amdgcn_mfma_f32_32x32x16_f16(lo, b[c], acc[n][c], 0, 0, 0);
-                acc[n][c] = __builtin_amdgcn_mfma_f32_32x32x16_f16(hi, b[c], acc[n][c], 0, 0, 0);
+        for (int c = 0; c < CT; ++c) acc[c] = f32x16{};
+        for (int s = 0; s < steps; s += 2) {
+            half8 cur[2][CT];
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int c = 0; c < CT; ++c) cur[u][c] = b[u][c];
+            if (s + 2 < steps) load_b(a, s + 2, steps);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                if (s + u < steps) {
+                    const int k = 16 * (s + u) + 8 * h;
+                    if (16 * (s + u) + 16 > tile.rank) {  // columns past the rank may hold anything
+#pragma unroll
+                        for (int c = 0; c < CT; ++c)
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) cur[u][c][e] = k + e < tile.rank ? cur[u][c][e] : (_Float16)0.0f;
+                    }
+                    const half8 hi = __builtin_bit_cast(half8, frag[(2 * (s + u) + h) * T + col]);
+                    const half8 lo = __builtin_bit_cast(half8, frag[part + (2 * (s + u) + h) * T + col]);
+#pragma unroll
+                    for (int c = 0; c < CT; ++c) {
+                        acc[c] = __builtin_amdgcn_mfma_f32_32x32x16_f16(lo, cur[u][c], acc[c], 0, 0, 0);
+                        acc[c] = __builtin_amdgcn_mfma_f32_32x32x16_f16(hi, cur[u][c], acc[c], 0, 0, 0);
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const int t = token(r);
+            const float f = factor[t];
+            f32x2 o;
+#pragma unroll
+            for (int c = 0; c < CT; ++c) o[c] = in[r][c] + acc[c][r] * f;
+            float* p = y + (uint64_t)(uint32_t)t * (uint32_t)a.ldy + j;
+            if constexpr (VEC) {
+                if (t < tile.nt && j < rows) __builtin_nontemporal_store(o, (f32x2*)p);
+            } else if (t < tile.nt) {
+#pragma unroll
+                for (int c = 0; c < CT; ++c)
+                    if (j + c < rows) p[c] = o[c];
             }
         }
     }
+};
+
+// A workgroup's part of a tile without an adapter: y = base.
+__device__ __forceinline__ void copy_base(const LoraArgs& a, const LoraTile& tile, const float* base, float* y, int rows) {
+    if (a.base == a.y) return;
+    for (int t = 0; t < tile.nt; ++t)
+        for (int j = threadIdx.x; j < rows; j += blockDim.x) y[t * a.ldy + j] = base[t * a.ldbase + j];
+}
+
+// Workgroup (row block, tile): 32 tokens by 256 rows of y, one UpBlock a wave, on the SPLIT parts of
+// the inner values that lora_down_kernel left.
+template <int SPLIT, bool VEC>
+__global__ __launch_bounds__(256, SPLIT > 2 ? 2 : 4) void lora_up_kernel(LoraArgs a) {
+    constexpr int T = kUpTokens, ROWS = kUpRows;
+    extern __shared__ u32x4 frag[];
+    __shared__ uint32_t largest[T];
+    __shared__ float factor[T];
+    const LoraTile tile = find_tile(a, T, blockIdx.y);
+    if (tile.nt == 0) return;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r0 = (int)blockIdx.x * ROWS;
+    const float* base = a.base + (int64_t)tile.t0 * a.ldbase + r0;
+    float* y = a.y + (int64_t)tile.t0 * a.ldy + r0;
+    const int rows = a.nrows - r0 < ROWS ? a.nrows - r0 : ROWS;
+    if (tile.rank == 0) return copy_base(a, tile, base, y, rows);
+    UpBlock<VEC> blk(64 * w, rows);
+    blk.load(a, tile, r0, base);
+    make_fragments(tile, frag, largest, factor, [&](int tok, int j, float* v) {
+        const float* p = a.v + ((int64_t)tile.t0 + tok) * a.max_rank + j;
+        f32x4 u[SPLIT][2];
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+        for (int s = 0; s < SPLIT; ++s) {
+            const f32x4* ps = (const f32x4*)(p + (int64_t)s * a.ntok * a.max_rank);
+            u[s][0] = ps[0];
+            u[s][1] = ps[1];
+        }
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
+        for (int s = 0; s < SPLIT; ++s)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int t = 32 * n + 8 * (r / 4) + 4 * h + r % 4, j = 64 * w + 32 * c + col;
-                if (full || (t < tile.nt && j < rows)) y[t * a.ldy + j] = in[n][c][r] + acc[n][c][r] * factor[t];
-            }
+            for (int e = 0; e < 8; ++e) v[e] += u[s][e / 4][e % 4];
+    });
+    blk.multiply_store(a, tile, frag, factor, y);
 }
 
 }  // namespace qmm
@@ -309,7 +389,9 @@ using namespace qmm;
 constexpr int64_t kLoraMaxTokens = 1 << 20;
 constexpr int kLoraMaxSegments = 1 << 14;
 
-// How many workgroups share the columns of one token tile: enough that few tiles still fill the GPU.
+// How many workgroups share the columns of one token tile, so that few tiles still fill the GPU; the
+// outer product reads that many parts.  517 ragged tokens, rank 64: 27.5 us with 2, 29.8 with 4, 35
+// with 1; 8 tokens of 8 requests, rank 16: 8.0 us with 8.
 static int lora_split(int64_t ntok) { return ntok <= 64 ? 8 : ntok <= 1024 ? 2 : 1; }
 
 extern "C" size_t qmm_lora_workspace(int64_t ntok, int max_rank) {
@@ -319,12 +401,21 @@ extern "C" size_t qmm_lora_workspace(int64_t ntok, int max_rank) {
 
 template <int XT>
 static void launch_down(const LoraArgs& p, hipStream_t st) {
-    const auto grid = [&](int T) { return dim3((unsigned)(p.ntok / T + p.nseg), (unsigned)p.split); };
-    if (p.max_rank <= 16) hipLaunchKernelGGL((lora_down_kernel<XT, 1, 2, 8>), grid(32), dim3(512), 0, st, p);
-    else if (p.max_rank <= 32) hipLaunchKernelGGL((lora_down_kernel<XT, 2, 2, 8>), grid(32), dim3(512), 0, st, p);
-    else if (p.max_rank <= 64) hipLaunchKernelGGL((lora_down_kernel<XT, 4, 2, 4>), grid(32), dim3(256), 0, st, p);
-    else if (p.max_rank <= 128) hipLaunchKernelGGL((lora_down_kernel<XT, 8, 1, 4>), grid(16), dim3(256), 0, st, p);
-    else hipLaunchKernelGGL((lora_down_kernel<XT, 16, 1, 2>), grid(16), dim3(128), 0, st, p);
+    const dim3 grid((unsigned)(p.ntok / 16 + p.nseg), (unsigned)p.split);
+    if (p.max_rank <= 16) hipLaunchKernelGGL((lora_down_kernel<XT, 1, 8>), grid, dim3(512), 0, st, p);
+    else if (p.max_rank <= 32) hipLaunchKernelGGL((lora_down_kernel<XT, 2, 8>), grid, dim3(512), 0, st, p);
+    else if (p.max_rank <= 64) hipLaunchKernelGGL((lora_down_kernel<XT, 4, 8>), grid, dim3(512), 0, st, p);
+    else if (p.max_rank <= 128) hipLaunchKernelGGL((lora_down_kernel<XT, 8, 4>), grid, dim3(256), 0, st, p);
+    else hipLaunchKernelGGL((lora_down_kernel<XT, 16, 2>), grid, dim3(128), 0, st, p);
+}
+
+template <bool VEC>
+static void launch_up(const LoraArgs& p, hipStream_t st) {
+    const dim3 grid((unsigned)((p.nrows + kUpRows - 1) / kUpRows), (unsigned)(p.ntok / kUpTokens + p.nseg));
+    const size_t lds = (size_t)((p.max_rank + 15) / 16) * 64 * kUpTokens;  // hi and lo fragments of every token
+    if (p.split == 8) hipLaunchKernelGGL((lora_up_kernel<8, VEC>), grid, dim3(256), lds, st, p);
+    else if (p.split == 2) hipLaunchKernelGGL((lora_up_kernel<2, VEC>), grid, dim3(256), lds, st, p);
+    else hipLaunchKernelGGL((lora_up_kernel<1, VEC>), grid, dim3(256), lds, st, p);
 }
 
 extern "C" int qmm_lora(int xtype, const void* x, int64_t ldx, int64_t ntok, int64_t k, const uint16_t* a, const uint16_t* b,
@@ -334,7 +425,8 @@ extern "C" int qmm_lora(int xtype, const void* x, int64_t ldx, int64_t ntok, int
     if ((xtype != QMM_TYPE_F16 && xtype != QMM_TYPE_F32) || ntok < 0 || k < 32 || k % 32 || ldx < k || nadapters < 1 || max_rank < 8 ||
         max_rank % 8 || nseg < 0 || nrows < 1 || ldbase < nrows || ldy < nrows)
         return QMM_EINVAL;
-    if (k > kMaxK || max_rank > kLoraMaxRank || ntok > kLoraMaxTokens || nseg > kLoraMaxSegments || nrows > 0x7FFFFF00) return QMM_EUNSUPPORTED;
+    if (k > kMaxK || max_rank > kLoraMaxRank || ntok > kLoraMaxTokens || nseg > kLoraMaxSegments || nrows > 0x7FFFFF00 || ldbase > 0x7FFFFFFF || ldy > 0x7FFFFFFF)
+        return QMM_EUNSUPPORTED;
     if (ntok == 0 || nseg == 0) return QMM_OK;
     if (!x || !a || !b || !ranks || !scales || !seg_off || !seg_adapter || !base || !y || !ws) return QMM_EINVAL;
     if (base == y && ldbase != ldy) return QMM_EINVAL;
@@ -347,11 +439,8 @@ extern "C" int qmm_lora(int xtype, const void* x, int64_t ldx, int64_t ntok, int
     const hipStream_t st = as_stream(stream);
     if (xtype == QMM_TYPE_F32) launch_down<kF32>(p, st);
     else launch_down<kBin16>(p, st);
-    const unsigned rowblocks = (unsigned)((nrows + kUpRows - 1) / kUpRows);
-    const size_t lds = (size_t)((max_rank + 15) / 16) * 64;  // hi and lo fragments per token
-    if (max_rank <= 128 && ntok >= 32 * (int64_t)nseg)
-        hipLaunchKernelGGL(lora_up_kernel<2>, dim3(rowblocks, (unsigned)(ntok / 64 + nseg)), dim3(256), lds * 64, st, p);
-    else
-        hipLaunchKernelGGL(lora_up_kernel<1>, dim3(rowblocks, (unsigned)(ntok / 32 + nseg)), dim3(256), lds * 32, st, p);
+    // y and base 8 bytes at a time
+    if (aligned(base, 8) && aligned(y, 8) && ldbase % 2 == 0 && ldy % 2 == 0 && nrows % 2 == 0) launch_up<true>(p, st);
+    else launch_up<false>(p, st);
     return launch_status();
 }
