@@ -348,7 +348,7 @@ int qmm_moe_combine(const float* y, int64_t nrows, int64_t hidden, const int32_t
  *   read and written 16 bytes at a time.  res_out may be res, and y or res_out may be x, if the
  *   types and row strides agree; otherwise outputs must not overlap inputs.
  * Errors: QMM_EINVAL (no output, unknown type, sizes, strides, eps negative or not finite),
- *         QMM_EALIGN, QMM_EUNSUPPORTED (hidden above 32768, 2^31 rows or more). */
+ *         QMM_EALIGN, QMM_EUNSUPPORTED (hidden above 32768, 2^22 rows or more). */
 int qmm_rmsnorm(int xtype, const void* x, int64_t ldx, int rtype, const void* res, int64_t ldr,
                 void* res_out, int64_t ldro, const float* w, float eps, int64_t ntok,
                 int64_t hidden, int ytype, void* y, int64_t ldy, void* yq, void* stream);
@@ -379,7 +379,7 @@ int qmm_dequantize_q8_1(const void* xq, int64_t k, int64_t ncols, int otype, voi
  *   nexperts 1 .. 1024 and a multiple of ngroups; ngroups 1 .. 64; 1 <= topk_groups <= ngroups;
  *   group_top <= nexperts / ngroups; 1 <= topk <= min(64, topk_groups * nexperts / ngroups).
  * Errors: QMM_EINVAL, QMM_EALIGN, QMM_EUNSUPPORTED (nexperts above 1024, ngroups or topk above 64,
- *         2^31 rows or more). */
+ *         2^25 rows or more). */
 #define QMM_ROUTE_RENORM 1u
 int qmm_moe_route(int ltype, const void* logits, int64_t ldl, const float* bias, int64_t ntok,
                   int nexperts, int score, int ngroups, int topk_groups, int group_top, int topk,
@@ -399,7 +399,7 @@ size_t qmm_moe_dispatch_workspace(int64_t ntok, int topk, int nexperts);
  *                   ascending, and their first entry; beyond them expert -1 and offset n;
  *                   group_off[G] = n  (qgemv_grouped_experts' groups).  Both NULL: not written.
  *   ws   : qmm_moe_dispatch_workspace() bytes, 4-byte aligned.
- *   nexperts 1 .. 1024, topk 1 .. 64, ntok * topk below 2^31.  ntok 0 writes the offsets.
+ *   nexperts 1 .. 1024, topk 1 .. 64, ntok * topk at most 2^30.  ntok 0 writes the offsets.
  * Errors: QMM_EINVAL, QMM_EALIGN, QMM_EUNSUPPORTED, QMM_ESPACE. */
 int qmm_moe_dispatch(const int32_t* ids, int64_t ntok, int topk, int nexperts, int32_t* sorted_tok,
                      int32_t* row_idx, int32_t* expert_off, int32_t* group_expert, int32_t* group_off,
@@ -422,7 +422,8 @@ size_t qmm_lora_workspace(int64_t ntok, int max_rank);
  *          segment are not written);  seg_adapter : int32 [nseg].
  *   base : float [ntok][ldbase], may be y (then ldbase = ldy; segments without adapter are not
  *          touched);  y : float [ntok][ldy]; strides >= nrows, 4-byte aligned.
- *   k    : a multiple of 32, at most 32768;  max_rank : a multiple of 8, at most 256.
+ *   k    : a multiple of 32, at most 32768;  max_rank : a multiple of 8, at most 256;  ntok at most
+ *          2^20, nseg at most 2^14, strides of y and base below 2^31.
  *   ws   : qmm_lora_workspace() bytes, 16-byte aligned.
  * Errors: QMM_EINVAL, QMM_EALIGN, QMM_EUNSUPPORTED, QMM_ESPACE. */
 int qmm_lora(int xtype, const void* x, int64_t ldx, int64_t ntok, int64_t k, const uint16_t* a,

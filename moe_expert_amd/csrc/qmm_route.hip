@@ -5,177 +5,362 @@ namespace qmm {
 
 constexpr int kRouteMaxExperts = 1024, kRouteMaxTopk = 64, kRouteMaxGroups = 64;
 
+// LDS written by some lanes of a wave and read by others of the same wave.
+__device__ __forceinline__ void wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
 struct RouteArgs {
     const void* logits;
     const float* bias;
-    int64_t ldl;
+    int64_t ldl, ntok;
     int ltype, nexperts, softmax, ngroups, topk_groups, group_top, topk, renorm;
     float scale;
     int32_t* ids;
     float* weights;
 };
 
-__device__ __forceinline__ float wave_max(float v) {
-    for (int m = 32; m; m >>= 1) v = fmaxf(v, __shfl_xor(v, m, 64));
-    return v;
-}
-__device__ __forceinline__ float wave_sum(float v) {
-    for (int m = 32; m; m >>= 1) v += __shfl_xor(v, m, 64);
-    return v;
-}
-
 constexpr float kNever = -__builtin_inff();
 
-// One wave per token.  score[e] and choice[e] in LDS (choice -inf: never chosen); the best of the
-// choices is taken topk times, ties to the lowest index.
-__global__ __launch_bounds__(64) void route_kernel(RouteArgs a) {
-    __shared__ float score[kRouteMaxExperts], choice[kRouteMaxExperts], run[kRouteMaxGroups], wsel[kRouteMaxTopk];
-    const int64_t t = blockIdx.x;
-    const int l = threadIdx.x, E = a.nexperts;
+// Maximum and sum over aligned groups of L lanes (16, 32, 64), in every lane.
+template <int L>
+__device__ __forceinline__ float lanes_max(float v) {
+    v = fmaxf(v, dpp<0xB1>(v));
+    v = fmaxf(v, dpp<0x4E>(v));
+    v = fmaxf(v, dpp<0x141>(v));
+    v = fmaxf(v, dpp<0x140>(v));
+    if constexpr (L >= 32) {
+        const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false, false);
+        const uint32_t r0 = r[0], r1 = r[1];
+        v = fmaxf(__builtin_bit_cast(float, r0), __builtin_bit_cast(float, r1));
+    }
+    if constexpr (L >= 64) {
+        const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false, false);
+        const uint32_t r0 = r[0], r1 = r[1];
+        v = fmaxf(__builtin_bit_cast(float, r0), __builtin_bit_cast(float, r1));
+    }
+    return v;
+}
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v) {
+    v += dpp<0xB1>(v);
+    v += dpp<0x4E>(v);
+    v += dpp<0x141>(v);
+    v += dpp<0x140>(v);
+    if constexpr (L >= 32) v += __shfl_xor(v, 16, 64);
+    if constexpr (L >= 64) v += __shfl_xor(v, 32, 64);
+    return v;
+}
+
+__device__ __forceinline__ float run_score(const RouteArgs& a, float best, float second) {
+    return a.group_top == 1 ? best : second == kNever ? kNever : best + second;
+}
+
+// L lanes per token, V experts a lane: lane q holds experts q V .. q V + V - 1, so the lowest lane that
+// holds a value holds the lowest expert.  Every token lives in one wave: the best choice is found topk
+// times by a maximum over its lanes and a ballot of who holds it, with no barrier.  VEC: rows in
+// aligned pieces of 8 (V = 8 or 16).
+template <int L, int V, bool VEC>
+__global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
+    constexpr int T = 256 / L;
+    __shared__ float scores[T][L * V], runs[T][kRouteMaxGroups];
+    __shared__ int chosen[T][kRouteMaxTopk];
+    const int q = threadIdx.x % L, g = threadIdx.x / L, E = a.nexperts, e0 = q * V;
+    const int64_t t = (int64_t)blockIdx.x * T + g;
+    const bool live = t < a.ntok;  // lanes past the tokens go along on the last one and store nothing
+    const int64_t row = (live ? t : a.ntok - 1) * a.ldl;
+    float c[V], s[V];
+    if constexpr (VEC) {
+        const char* p = (const char*)a.logits + row * (a.ltype == kF32 ? 4 : 2);
+        Raw8 raw[V / 8];
+#pragma unroll
+        for (int i = 0; i < V / 8; ++i) load_raw8(raw[i], p, e0 + 8 * i < E ? e0 + 8 * i : 0, a.ltype);
+#pragma unroll
+        for (int i = 0; i < V / 8; ++i) unpack8(raw[i], a.ltype, c + 8 * i);
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) c[v] = load_value(a.logits, row + (e0 + v < E ? e0 + v : 0), a.ltype);
+    }
     float top = kNever;
-    for (int e = l; e < E; e += 64) {
-        const float z = load_value(a.logits, t * a.ldl + e, a.ltype);
-        choice[e] = z == z ? z : kNever;
-        top = fmaxf(top, choice[e]);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        if (e0 + v >= E || c[v] != c[v]) c[v] = kNever;
+        top = fmaxf(top, c[v]);
     }
-    top = wave_max(top);
-    float sum = 0.0f;
+    // s: a factor of the score (softmax: over the sum, known for the whole row) or the score
+    float sum = 1.0f;
     if (a.softmax) {
-        for (int e = l; e < E; e += 64) {
-            const float z = choice[e];
-            score[e] = z == kNever ? 0.0f : z == top ? 1.0f : expf(z - top);
-            sum += score[e];
+        top = lanes_max<L>(top);
+        sum = 0.0f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            s[v] = c[v] == kNever ? 0.0f : c[v] == top ? 1.0f : expf(c[v] - top);
+            sum += s[v];
         }
-        sum = wave_sum(sum);
+        sum = lanes_sum<L>(sum);
+        if (sum == 0.0f) sum = 1.0f;  // no expert
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) s[v] = 1.0f / (1.0f + expf(-c[v]));
     }
-    const bool by_logit = a.softmax && !a.bias && (a.ngroups == 1 || a.group_top == 1);
-    for (int e = l; e < E; e += 64) {
-        const float z = choice[e];
-        const float s = a.softmax ? (sum > 0.0f ? score[e] / sum : 0.0f) : 1.0f / (1.0f + expf(-z));
-        score[e] = s;
-        if (!by_logit && z != kNever) {
-            const float c = a.bias ? s + a.bias[e] : s;
-            choice[e] = c == c ? c : kNever;
+#pragma unroll
+    for (int v = 0; v < V; ++v) scores[g][e0 + v] = s[v];
+    if (!a.softmax || a.bias || (a.ngroups > 1 && a.group_top > 1)) {  // chosen by score, else by logit
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const float sc = a.softmax ? s[v] / sum : s[v];
+            const float d = a.bias ? sc + a.bias[e0 + v < E ? e0 + v : 0] : sc;
+            c[v] = c[v] == kNever || d != d ? kNever : d;
         }
     }
-    __syncthreads();
     if (a.ngroups > 1) {
-        const int per = E / a.ngroups;
-        if (l < a.ngroups) {
-            float m0 = kNever, m1 = kNever;
-            for (int i = 0; i < per; ++i) {
-                const float c = choice[l * per + i];
-                if (c > m0) { m1 = m0; m0 = c; }
-                else if (c > m1) m1 = c;
+        // a run's score: by its lanes where it is a power of two of whole lanes, else from LDS
+        const int per = E / a.ngroups, lanes = per / V;
+        __shared__ float members[T][L * V];
+        float m0 = kNever, m1 = kNever;
+        if (lanes * V == per && (lanes & (lanes - 1)) == 0) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                m1 = fmaxf(m1, fminf(m0, c[v]));
+                m0 = fmaxf(m0, c[v]);
             }
-            run[l] = a.group_top == 2 ? (m1 == kNever ? kNever : m0 + m1) : m0;
+            for (int d = 1; d < lanes; d <<= 1) {
+                const float o0 = __shfl_xor(m0, d, 64), o1 = __shfl_xor(m1, d, 64);
+                m1 = fmaxf(fmaxf(m1, o1), fminf(m0, o0));
+                m0 = fmaxf(m0, o0);
+            }
+            if (e0 < E && e0 % per == 0) runs[g][e0 / per] = run_score(a, m0, m1);
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v) members[g][e0 + v] = c[v];
+            wave_sync();
+            for (int r = q; r < a.ngroups; r += L) {
+                m0 = m1 = kNever;
+                for (int i = 0; i < per; ++i) {
+                    const float x = members[g][r * per + i];
+                    m1 = fmaxf(m1, fminf(m0, x));
+                    m0 = fmaxf(m0, x);
+                }
+                runs[g][r] = run_score(a, m0, m1);
+            }
         }
-        __syncthreads();
-        if (l < a.ngroups) {
-            int better = 0;
-            for (int g = 0; g < a.ngroups; ++g) better += run[g] > run[l] || (run[g] == run[l] && g < l);
-            if (better >= a.topk_groups)
-                for (int i = 0; i < per; ++i) choice[l * per + i] = kNever;
+        wave_sync();
+        // experts of a run that at least topk_groups others beat are out
+        int last = -1;
+        bool out = false;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int r = (e0 + v) / per;
+            if (e0 + v < E && r != last) {
+                const float mine = runs[g][r];
+                int better = 0;
+                for (int o = 0; o < a.ngroups; ++o) better += runs[g][o] > mine || (runs[g][o] == mine && o < r);
+                out = better >= a.topk_groups;
+                last = r;
+            }
+            if (out) c[v] = kNever;
         }
-        __syncthreads();
     }
-    float total = 0.0f;
+    const int base = (threadIdx.x & 63) / L * L;  // this token's lanes in the ballot
     for (int k = 0; k < a.topk; ++k) {
-        float best = kNever;
-        int at = E;
-        for (int e = l; e < E; e += 64)
-            if (choice[e] > best) { best = choice[e]; at = e; }
-        const float m = wave_max(best);
-        if (best != m || m == kNever) at = E;
-        for (int d = 32; d; d >>= 1) {
-            const int o = __shfl_xor(at, d, 64);
-            at = o < at ? o : at;
+        float m = c[0];
+#pragma unroll
+        for (int v = 1; v < V; ++v) m = fmaxf(m, c[v]);
+        const float best = lanes_max<L>(m);
+        const uint64_t hold = __ballot(m == best) >> base;
+        const bool own = (int)__builtin_ctzll(hold) == q;
+        if (own) {
+            int at = 0;
+#pragma unroll
+            for (int v = V - 1; v >= 0; --v) at = c[v] == best ? v : at;
+#pragma unroll
+            for (int v = 0; v < V; ++v) c[v] = v == at ? kNever : c[v];
+            chosen[g][k] = best == kNever ? -1 : e0 + at;
         }
-        const bool found = at < E;
-        const float s = found ? score[at] : 0.0f;
-        total += s;
-        __syncthreads();
-        if (l == 0) {
-            if (found) choice[at] = kNever;
-            a.ids[t * a.topk + k] = found ? at : -1;
-            wsel[k] = s;
-        }
-        __syncthreads();
     }
-    if (l < a.topk) {
-        float w = wsel[l];
+    wave_sync();
+    float total = 0.0f;
+    for (int k = q; k < a.topk; k += L) {
+        const int e = chosen[g][k];
+        total += e >= 0 ? scores[g][e] / sum : 0.0f;
+    }
+    total = lanes_sum<L>(total);
+    if (!live) return;
+    for (int k = q; k < a.topk; k += L) {
+        const int e = chosen[g][k];
+        float w = e >= 0 ? scores[g][e] / sum : 0.0f;
         if (a.renorm && total > 0.0f) w = w / total;
-        a.weights[t * a.topk + l] = w * a.scale;
+        a.ids[t * a.topk + k] = e;
+        a.weights[t * a.topk + k] = w * a.scale;
     }
 }
 
 // ------------------------------------------------------------------ dispatch
 
+// A stable counting sort of the entries by expert.  One chunk (4096 entries): one workgroup counts,
+// scans and places.  More: one launch counts each chunk's experts, a second places every chunk from
+// the counts of the chunks before it; beyond 64 chunks a launch between them sums the counts over the
+// chunks, so that no workgroup reads them all.  Within a chunk a wave takes consecutive entries, 64
+// at a time; an entry's place among its wave's entries of the same expert comes from ballots over
+// the expert's bits, so the order needs no atomics.  Bound: launches and dependent loads (8192 tokens
+// of top-8, 128 experts: 0.8 MB).
+
+constexpr int kDispThreads = 1024, kDispWaves = 16, kDispPer = 4;
+constexpr int kDispChunk = kDispThreads * kDispPer;
+constexpr int kDispDirect = 64;  // chunks whose counts a placing workgroup adds up itself
+
 struct DispatchArgs {
     const int32_t* ids;
-    int n, topk, nexperts, ngroups;
     int32_t *sorted_tok, *row_idx, *expert_off, *group_expert, *group_off;
+    int32_t* counts;  // [chunk][expert]; summed: entries of the expert in the chunks before
+    int32_t* totals;  // [expert], summed only
+    int n, topk, nexperts, ngroups, chunks, bits;
 };
 
-constexpr int kDispThreads = 1024;
+__device__ __forceinline__ int expert_at(const DispatchArgs& a, int p) {
+    const int e = p < a.n ? a.ids[p] : -1;
+    return e >= 0 && e < a.nexperts ? e : -1;
+}
 
-// One workgroup: counts per expert, their prefix sums, then the entries in order, 64 at a time by
-// one wave, so that each expert's entries keep their order.
-__global__ __launch_bounds__(kDispThreads) void dispatch_kernel(DispatchArgs a) {
-    __shared__ int count[kRouteMaxExperts], scan[kDispThreads], live[kDispThreads];
-    const int i = threadIdx.x;
+// Inclusive scan over the workgroup (16 waves), each wave by lane exchanges, the waves through LDS.
+__device__ __forceinline__ int workgroup_scan(int v, int* part) {
+    const int l = threadIdx.x & 63, w = threadIdx.x >> 6;
+    for (int d = 1; d < 64; d <<= 1) {
+        const int u = __shfl_up(v, d, 64);
+        if (l >= d) v += u;
+    }
+    if (l == 63) part[w] = v;
+    __syncthreads();
+    for (int u = 0; u < w; ++u) v += part[u];
+    return v;
+}
+
+// counts[chunk][e]
+__global__ __launch_bounds__(kDispThreads) void dispatch_count_kernel(DispatchArgs a) {
+    __shared__ int count[kRouteMaxExperts];
+    const int i = threadIdx.x, p0 = (int)blockIdx.x * kDispChunk;
+    int e[kDispPer];
+#pragma unroll
+    for (int u = 0; u < kDispPer; ++u) e[u] = expert_at(a, p0 + u * kDispThreads + i);
     count[i] = 0;
     __syncthreads();
-    for (int p = i; p < a.n; p += kDispThreads) {
-        const int e = a.ids[p];
-        if (e >= 0 && e < a.nexperts) atomicAdd(&count[e], 1);
+#pragma unroll
+    for (int u = 0; u < kDispPer; ++u)
+        if (e[u] >= 0) atomicAdd(&count[e[u]], 1);
+    __syncthreads();
+    if (i < a.nexperts) a.counts[(int64_t)blockIdx.x * a.nexperts + i] = count[i];
+}
+
+// Workgroup of 64 experts: 16 runs of chunks each, counts replaced by the entries before the chunk.
+__global__ __launch_bounds__(kDispThreads) void dispatch_sum_kernel(DispatchArgs a) {
+    __shared__ int part[kDispWaves][64];
+    const int l = threadIdx.x & 63, w = threadIdx.x >> 6, e = (int)blockIdx.x * 64 + l;
+    const int per = (a.chunks + kDispWaves - 1) / kDispWaves;
+    const int c0 = w * per, c1 = c0 + per < a.chunks ? c0 + per : a.chunks;
+    int s = 0;
+    if (e < a.nexperts)
+        for (int c = c0; c < c1; ++c) s += a.counts[(int64_t)c * a.nexperts + e];
+    part[w][l] = s;
+    __syncthreads();
+    int before = 0;
+    for (int u = 0; u < w; ++u) before += part[u][l];
+    if (e >= a.nexperts) return;
+    for (int c = c0; c < c1; ++c) {
+        int32_t* p = a.counts + (int64_t)c * a.nexperts + e;
+        const int v = *p;
+        *p = before;
+        before += v;
     }
-    __syncthreads();
-    const int c = count[i];
-    scan[i] = c;
-    live[i] = c > 0;
-    __syncthreads();
-    for (int d = 1; d < kDispThreads; d <<= 1) {
-        const int u = i >= d ? scan[i - d] : 0, v = i >= d ? live[i - d] : 0;
-        __syncthreads();
-        scan[i] += u;
-        live[i] += v;
-        __syncthreads();
-    }
-    const int total = scan[kDispThreads - 1], nlive = live[kDispThreads - 1], first = scan[i] - c;
-    if (i < a.nexperts) a.expert_off[i] = first;
-    if (i == 0) a.expert_off[a.nexperts] = total;
-    if (a.group_off) {
-        if (c > 0) {
-            a.group_expert[live[i] - 1] = i;
-            a.group_off[live[i] - 1] = first;
-        }
-        for (int g = nlive + i; g <= a.ngroups; g += kDispThreads) {
-            if (g < a.ngroups) a.group_expert[g] = -1;
-            a.group_off[g] = total;
-        }
-    }
-    for (int p = total + i; p < a.n; p += kDispThreads) a.sorted_tok[p] = -1;
-    __syncthreads();
-    count[i] = first;
-    __syncthreads();
-    if (i < 64) {
-        for (int p0 = 0; p0 < a.n; p0 += 64) {
-            const int p = p0 + i;
-            int e = p < a.n ? a.ids[p] : -1;
-            if (e < 0 || e >= a.nexperts) e = -1;
-            unsigned long long same = ~0ull;
-            for (int b = 0; b < 11; ++b) {
-                const unsigned long long m = __ballot((e >> b) & 1);
-                same &= ((e >> b) & 1) ? m : ~m;
+    if (w == kDispWaves - 1) a.totals[e] = before;
+}
+
+enum { kDispOne, kDispAdd, kDispSummed };
+
+// Workgroup = chunk.  MODE: how the entries of the other chunks are known.
+template <int MODE>
+__global__ __launch_bounds__(kDispThreads) void dispatch_place_kernel(DispatchArgs a) {
+    extern __shared__ uint16_t seen[];  // [wave][expert]: entries of the waves before, then of the wave so far
+    __shared__ int first[kRouteMaxExperts], part[kDispWaves], part2[kDispWaves];
+    const int i = threadIdx.x, l = i & 63, w = i >> 6, E = a.nexperts;
+    // entries per wave: whole runs of 64, as even as they go
+    const int per = MODE == kDispOne ? (a.n + kDispThreads - 1) / kDispThreads : kDispPer;
+    const int p0 = (int)blockIdx.x * kDispChunk + w * per * 64 + l;
+    int e[kDispPer], place[kDispPer];
+#pragma unroll
+    for (int u = 0; u < kDispPer; ++u) e[u] = u < per ? expert_at(a, p0 + 64 * u) : -1;
+
+    int total = 0, before = 0;  // of expert i: all its entries, and those of earlier chunks
+    if (i < E) {
+        if constexpr (MODE == kDispAdd) {
+#pragma unroll 8
+            for (int c = 0; c < a.chunks; ++c) {
+                const int v = a.counts[(int64_t)c * E + i];
+                total += v;
+                before += c < (int)blockIdx.x ? v : 0;
             }
-            const int rank = __popcll(same & ((1ull << i) - 1ull));
-            const int at = e >= 0 ? count[e] + rank : -1;
-            __builtin_amdgcn_wave_barrier();
-            if (e >= 0 && rank == 0) count[e] += __popcll(same);
-            __builtin_amdgcn_wave_barrier();
-            if (p < a.n) a.row_idx[p] = at;
-            if (at >= 0) a.sorted_tok[at] = p / a.topk;
+        } else if constexpr (MODE == kDispSummed) {
+            total = a.totals[i];
+            before = a.counts[(int64_t)blockIdx.x * E + i];
+        }
+    }
+    uint16_t* mine = seen + w * E;
+    for (int k = l; k < E; k += 64) mine[k] = 0;
+    wave_sync();
+#pragma unroll
+    for (int u = 0; u < kDispPer; ++u) {
+        if (u >= per) break;
+        uint64_t same = __ballot(e[u] >= 0);
+        for (int b = 0; b < a.bits; ++b) {
+            const uint64_t m = __ballot((e[u] >> b) & 1);
+            same &= (e[u] >> b) & 1 ? m : ~m;
+        }
+        const int rank = __popcll(same & ((1ull << l) - 1ull));
+        place[u] = e[u] >= 0 ? mine[e[u]] + rank : 0;
+        wave_sync();
+        if (e[u] >= 0 && rank == 0) mine[e[u]] = (uint16_t)(place[u] + __popcll(same));
+        wave_sync();
+    }
+    __syncthreads();
+    if (i < E) {
+        int run = 0;
+        for (int u = 0; u < kDispWaves; ++u) {
+            const int v = seen[u * E + i];
+            seen[u * E + i] = (uint16_t)run;
+            run += v;
+        }
+        if constexpr (MODE == kDispOne) total = run;
+    }
+    const int end = workgroup_scan(total, part);
+    if (i < E) first[i] = end - total + before;
+    const int live = workgroup_scan(total > 0, part2);
+    if (i == kDispThreads - 1) part[0] = end;  // all entries (its reads ended before part2's barrier)
+    __syncthreads();
+    const int all = part[0];
+#pragma unroll
+    for (int u = 0; u < kDispPer; ++u) {
+        const int p = p0 + 64 * u;
+        if (u >= per || p >= a.n) continue;
+        const int at = e[u] >= 0 ? first[e[u]] + mine[e[u]] + place[u] : -1;
+        a.row_idx[p] = at;
+        if (at >= 0) a.sorted_tok[at] = p / a.topk;
+    }
+    for (int p = (int)blockIdx.x * kDispChunk + i; p < a.n && p < ((int)blockIdx.x + 1) * kDispChunk; p += kDispThreads)
+        if (p >= all) a.sorted_tok[p] = -1;
+    if (blockIdx.x == 0) {
+        if (i < E) a.expert_off[i] = end - total;
+        if (i == 0) a.expert_off[E] = all;
+        if (a.group_off) {
+            if (total > 0) {
+                a.group_expert[live - 1] = i;
+                a.group_off[live - 1] = end - total;
+            }
+            if (i == kDispThreads - 1) part[1] = live;
+            __syncthreads();
+            for (int g = part[1] + i; g <= a.ngroups; g += kDispThreads) {
+                if (g < a.ngroups) a.group_expert[g] = -1;
+                a.group_off[g] = all;
+            }
         }
     }
 }
@@ -186,6 +371,8 @@ __global__ __launch_bounds__(kDispThreads) void dispatch_kernel(DispatchArgs a) 
 
 using namespace qmm;
 
+constexpr int64_t kRouteMaxTokens = (1 << 25) - 1;  // 64 lanes a token, below 2^32 threads
+
 extern "C" int qmm_moe_route(int ltype, const void* logits, int64_t ldl, const float* bias, int64_t ntok, int nexperts, int score,
                              int ngroups, int topk_groups, int group_top, int topk, float scale, int32_t* ids, float* weights,
                              unsigned flags, void* stream) {
@@ -193,25 +380,41 @@ extern "C" int qmm_moe_route(int ltype, const void* logits, int64_t ldl, const f
         return QMM_EINVAL;
     if (ntok < 0 || nexperts < 1 || ldl < nexperts || ngroups < 1 || topk_groups < 1 || topk_groups > ngroups || topk < 1)
         return QMM_EINVAL;
-    if (nexperts > kRouteMaxExperts || ngroups > kRouteMaxGroups || topk > kRouteMaxTopk || ntok > 0x7FFFFFFF) return QMM_EUNSUPPORTED;
+    if (nexperts > kRouteMaxExperts || ngroups > kRouteMaxGroups || topk > kRouteMaxTopk || ntok > kRouteMaxTokens) return QMM_EUNSUPPORTED;
     if (nexperts % ngroups || topk > topk_groups * (nexperts / ngroups)) return QMM_EINVAL;
     if (group_top < 1 || group_top > 2 || group_top > nexperts / ngroups) return QMM_EINVAL;
     if (ntok == 0) return QMM_OK;
     if (!logits || !ids || !weights) return QMM_EINVAL;
     if (!aligned(logits, type_bytes(ltype)) || !aligned(bias, 4) || !aligned(ids, 4) || !aligned(weights, 4)) return QMM_EALIGN;
-    RouteArgs a{logits, bias, ldl, ltype, nexperts, score == QMM_SCORE_SOFTMAX, ngroups, topk_groups, group_top, topk,
-                (flags & QMM_ROUTE_RENORM) != 0, scale, ids, weights};
-    hipLaunchKernelGGL(route_kernel, dim3((unsigned)ntok), dim3(64), 0, as_stream(stream), a);
+    const RouteArgs a{logits, bias, ldl, ntok, ltype, nexperts, score == QMM_SCORE_SOFTMAX, ngroups, topk_groups, group_top, topk,
+                      (flags & QMM_ROUTE_RENORM) != 0, scale, ids, weights};
+    const bool vec = nexperts % 8 == 0 && aligned(logits, 16) && ldl * (int64_t)type_bytes(ltype) % 16 == 0;
+    const hipStream_t st = as_stream(stream);
+    const auto grid = [&](int lanes) { return dim3((unsigned)((ntok * lanes + 255) / 256)); };
+    const dim3 block(256);
+    if (nexperts <= 32) hipLaunchKernelGGL((route_kernel<16, 2, false>), grid(16), block, 0, st, a);
+    else if (nexperts <= 64) hipLaunchKernelGGL((route_kernel<16, 4, false>), grid(16), block, 0, st, a);
+    else if (nexperts <= 128 && vec) hipLaunchKernelGGL((route_kernel<16, 8, true>), grid(16), block, 0, st, a);
+    else if (nexperts <= 128) hipLaunchKernelGGL((route_kernel<16, 8, false>), grid(16), block, 0, st, a);
+    else if (nexperts <= 256 && vec) hipLaunchKernelGGL((route_kernel<32, 8, true>), grid(32), block, 0, st, a);
+    else if (nexperts <= 256) hipLaunchKernelGGL((route_kernel<32, 8, false>), grid(32), block, 0, st, a);
+    else if (nexperts <= 512 && vec) hipLaunchKernelGGL((route_kernel<64, 8, true>), grid(64), block, 0, st, a);
+    else if (nexperts <= 512) hipLaunchKernelGGL((route_kernel<64, 8, false>), grid(64), block, 0, st, a);
+    else if (vec) hipLaunchKernelGGL((route_kernel<64, 16, true>), grid(64), block, 0, st, a);
+    else hipLaunchKernelGGL((route_kernel<64, 16, false>), grid(64), block, 0, st, a);
     return launch_status();
 }
 
+static int64_t dispatch_chunks(int64_t n) { return n <= kDispChunk ? 1 : (n + kDispChunk - 1) / kDispChunk; }
+
 static bool dispatch_takes(int64_t ntok, int topk, int nexperts) {
-    return ntok <= 0x7FFFFFFF && topk <= kRouteMaxTopk && nexperts <= kRouteMaxExperts && ntok * topk <= 0x7FFFFFFF;
+    return ntok <= 0x7FFFFFFF && topk <= kRouteMaxTopk && nexperts <= kRouteMaxExperts && ntok * topk <= (int64_t)1 << 30;
 }
 
 extern "C" size_t qmm_moe_dispatch_workspace(int64_t ntok, int topk, int nexperts) {
     if (ntok < 0 || topk < 1 || nexperts < 1 || !dispatch_takes(ntok, topk, nexperts)) return 0;
-    return 16;
+    const int64_t chunks = dispatch_chunks(ntok * topk);
+    return chunks == 1 ? 16 : (size_t)(chunks + 1) * nexperts * 4;
 }
 
 extern "C" int qmm_moe_dispatch(const int32_t* ids, int64_t ntok, int topk, int nexperts, int32_t* sorted_tok, int32_t* row_idx,
@@ -225,7 +428,25 @@ extern "C" int qmm_moe_dispatch(const int32_t* ids, int64_t ntok, int topk, int 
         return QMM_EALIGN;
     if (ntok && ws_bytes < qmm_moe_dispatch_workspace(ntok, topk, nexperts)) return QMM_ESPACE;
     const int n = (int)(ntok * topk);
-    DispatchArgs a{ids, n, topk, nexperts, n < nexperts ? n : nexperts, sorted_tok, row_idx, expert_off, group_expert, group_off};
-    hipLaunchKernelGGL(dispatch_kernel, dim3(1), dim3(kDispThreads), 0, as_stream(stream), a);
+    const int chunks = (int)dispatch_chunks(n);
+    int bits = 0;
+    while ((1 << bits) < nexperts) ++bits;
+    int32_t* const counts = (int32_t*)ws;
+    const DispatchArgs a{ids, sorted_tok, row_idx, expert_off, group_expert, group_off, counts, counts + (int64_t)chunks * nexperts,
+                         n, topk, nexperts, n < nexperts ? n : nexperts, chunks, bits};
+    const hipStream_t st = as_stream(stream);
+    const size_t lds = (size_t)kDispWaves * nexperts * 2;
+    const dim3 block(kDispThreads);
+    if (chunks == 1) {
+        hipLaunchKernelGGL(dispatch_place_kernel<kDispOne>, dim3(1), block, lds, st, a);
+        return launch_status();
+    }
+    hipLaunchKernelGGL(dispatch_count_kernel, dim3((unsigned)chunks), block, 0, st, a);
+    if (chunks <= kDispDirect) {
+        hipLaunchKernelGGL(dispatch_place_kernel<kDispAdd>, dim3((unsigned)chunks), block, lds, st, a);
+    } else {
+        hipLaunchKernelGGL(dispatch_sum_kernel, dim3((unsigned)((nexperts + 63) / 64)), block, 0, st, a);
+        hipLaunchKernelGGL(dispatch_place_kernel<kDispSummed>, dim3((unsigned)chunks), block, lds, st, a);
+    }
     return launch_status();
 }
