@@ -542,50 +542,75 @@ def qgemm_prefill_experts_q8(wtype_gu, w_gate, w_up, wtype_down, w_down, nexpert
 # ------------------------------------------------------------------ between the products
 #
 # These entry points launch kernels of a few microseconds, so their checks read each tensor's
-# attributes once.
+# attributes once, in the order of cost.
 
-_TYPE_OF = None
+_TYPE_OF = {}
 
 
-def _type_of(dtype):
-    """QMM_TYPE_* of a torch dtype, 0 if the kernels do not take it."""
-    global _TYPE_OF
-    if _TYPE_OF is None:
+def _types():
+    """QMM_TYPE_* by torch dtype."""
+    if not _TYPE_OF:
         import torch
-        _TYPE_OF = {torch.float32: QMM_TYPE_F32, torch.float16: QMM_TYPE_F16, torch.bfloat16: QMM_TYPE_BF16}
-    return _TYPE_OF.get(dtype, 0)
+        _TYPE_OF.update({torch.float32: QMM_TYPE_F32, torch.float16: QMM_TYPE_F16, torch.bfloat16: QMM_TYPE_BF16})
+    return _TYPE_OF
 
 
-def _rows(t, name, ntok, ncols, device, types=(QMM_TYPE_F32, QMM_TYPE_F16, QMM_TYPE_BF16)):
-    """t must be a [ntok, ncols] GPU tensor of one of `types` whose rows are contiguous and do not
-    overlap (any row stride of at least ncols); returns (type code, row stride)."""
+def _matrix(t, name, what):
+    """The shape of a two-dimensional GPU tensor."""
+    shape = getattr(t, "shape", ())
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be {what}")
     if not getattr(t, "is_cuda", False):
         raise ValueError(f"{name} must be a GPU tensor")
-    if t.shape != (ntok, ncols):
-        raise ValueError(f"{name} must be [{ntok}, {ncols}], not {list(t.shape)}")
-    code = _type_of(t.dtype)
-    if code not in types:
+    return shape
+
+
+def _rows(t, name, shape, device, bf16=True):
+    """t must be a GPU tensor of `shape` and of float32, float16 or (bf16) bfloat16 on `device`, whose
+    rows are contiguous and do not overlap (any row stride from the width on); returns its type code
+    and row stride."""
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
+    code = (_TYPE_OF or _types()).get(t.dtype, 0)
+    if not code or (code == QMM_TYPE_BF16 and not bf16):
         raise ValueError(f"{name} has dtype {t.dtype}, which this call does not take")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, the call runs on {device}")
+    if t.is_contiguous():
+        return code, shape[1]
     ld, step = t.stride()
-    if ntok <= 1:
-        ld = ncols  # the one row's stride says nothing
-    if (step != 1 and ncols > 1) or ld < ncols:
+    if shape[0] <= 1:
+        ld = shape[1]  # the one row's stride says nothing
+    if (step != 1 and shape[1] > 1) or ld < shape[1]:
         raise ValueError(f"{name} must have contiguous rows that do not overlap")
     return code, ld
 
 
+_CURRENT = None
+
+
+def _current():
+    """(current device index, current stream handle of a device index): torch's direct functions, as
+    the Stream object that the public call builds costs as much as a launch; the public calls where
+    they are missing."""
+    global _CURRENT
+    if _CURRENT is None:
+        import torch
+        torch.cuda.init()
+        _CURRENT = (getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device),
+                    getattr(torch._C, "_cuda_getCurrentRawStream", lambda i: torch.cuda.current_stream(i).cuda_stream))
+    return _CURRENT
+
+
 def _call(fn, device, stream, *args):
     """Call a library function on `device`'s current stream (or the one given)."""
-    import torch
-    here = torch.cuda.current_device()
+    device_of, stream_of = _CURRENT or _current()
+    here = device_of()
     at = here if device.index is None else device.index
     if stream is None:
-        # the current stream's handle without the Stream object (2 us) where torch has it
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        stream = raw(at) if raw else torch.cuda.current_stream(device).cuda_stream
+        stream = stream_of(at)
     if at != here:
+        import torch
         with torch.cuda.device(at):
             rc = getattr(lib(), fn)(*args, stream)
     else:
@@ -614,28 +639,26 @@ def qmm_rmsnorm(x, w, eps, res=None, res_out=None, y=None, yq=None, stream=None)
     res_out, a tensor of res' dtype (of any dtype without res) that takes r, res itself for an
     update in place.  Returns (y, yq, res_out), None for those not asked for."""
     import torch
-    if getattr(x, "dim", lambda: 0)() != 2:
-        raise ValueError("x must be [ntok, hidden]")
-    ntok, hidden = x.shape
+    shape = ntok, hidden = _matrix(x, "x", "[ntok, hidden]")
     dev = x.device
     if hidden < 1:
         raise ValueError("hidden must be positive")
     if y is None and yq is None and res_out is None:
         raise ValueError("no output asked for")
-    xt, ldx = _rows(x, "x", ntok, hidden, dev)
+    xt, ldx = _rows(x, "x", shape, dev)
     _need(w, "w", "f32", hidden * 4, dev)
     rt = ldr = ldro = yt = ldy = 0
     if res is not None:
-        rt, ldr = _rows(res, "res", ntok, hidden, dev)
+        rt, ldr = _rows(res, "res", shape, dev)
     if res_out is not None:
-        ot, ldro = _rows(res_out, "res_out", ntok, hidden, dev)
+        ot, ldro = _rows(res_out, "res_out", shape, dev)
         if rt and ot != rt:
             raise ValueError("res_out must have res' dtype")
         rt = ot
     if y is not None:
         if isinstance(y, torch.dtype):
-            y = torch.empty((ntok, hidden), dtype=y, device=dev)
-        yt, ldy = _rows(y, "y", ntok, hidden, dev)
+            y = torch.empty(shape, dtype=y, device=dev)
+        yt, ldy = _rows(y, "y", shape, dev)
     if yq is not None:
         if hidden % 32:
             raise ValueError(f"hidden={hidden} is not a multiple of 32")
@@ -665,7 +688,7 @@ def qmm_dequantize_q8_1(xq, k, out=None, stream=None):
     ncols, dev = _nbytes(xq) // col, xq.device
     if out is None or isinstance(out, torch.dtype):
         out = torch.empty((ncols, k), dtype=out or torch.float32, device=dev)
-    ot, ldo = _rows(out, "out", ncols, k, dev, (QMM_TYPE_F32, QMM_TYPE_F16))
+    ot, ldo = _rows(out, "out", (ncols, k), dev, bf16=False)
     _call("qmm_dequantize_q8_1", dev, stream, xq.data_ptr(), k, ncols, ot, out.data_ptr(), ldo)
     return out
 
@@ -680,11 +703,9 @@ def qmm_moe_route(logits, topk, score=QMM_SCORE_SOFTMAX, bias=None, ngroups=1, t
     group_top best; weights are the chosen scores, divided by their sum if renorm, times scale.
     Experts whose logit is -inf or NaN are never chosen; missing choices are id -1, weight 0."""
     import torch
-    if getattr(logits, "dim", lambda: 0)() != 2:
-        raise ValueError("logits must be [ntok, nexperts]")
-    ntok, nexperts = logits.shape
+    shape = ntok, nexperts = _matrix(logits, "logits", "[ntok, nexperts]")
     dev = logits.device
-    lt, ldl = _rows(logits, "logits", ntok, nexperts, dev)
+    lt, ldl = _rows(logits, "logits", shape, dev)
     if topk < 1 or max(topk, ngroups, topk_groups, group_top) > 0x7FFFFFFF:
         raise ValueError("topk must be positive, and every count an int32")
     if bias is not None:
@@ -710,9 +731,7 @@ def qmm_moe_dispatch(ids, nexperts, sorted_tok=None, row_idx=None, expert_off=No
     group_off and sorted_tok (as entry_col), qmm_moe_combine row_idx.  Entries are ordered by expert,
     then token, then k; sorted_tok is -1 past the last entry, row_idx -1 where there is none."""
     import torch
-    if getattr(ids, "dim", lambda: 0)() != 2:
-        raise ValueError("ids must be [ntok, topk]")
-    ntok, topk = ids.shape
+    ntok, topk = _matrix(ids, "ids", "[ntok, topk]")
     dev = ids.device
     n = ntok * topk
     g = min(nexperts, n)
@@ -746,30 +765,30 @@ def qmm_lora(x, a, b, ranks, scales, seg_off, seg_adapter, y, base=None, ws=None
     float16 [nadapters, nrows, max_rank], of which the first ranks[i] (int32) rows / columns are
     used; scales: float32 [nadapters]; seg_off: int32 [nseg+1]; seg_adapter: int32 [nseg]; y, base:
     float32 [ntok, nrows] with any row stride.  Returns y."""
-    if getattr(x, "dim", lambda: 0)() != 2 or getattr(a, "dim", lambda: 0)() != 3 or getattr(b, "dim", lambda: 0)() != 3:
-        raise ValueError("x must be [ntok, k], a [nadapters, max_rank, k], b [nadapters, nrows, max_rank]")
-    ntok, k = x.shape
+    shape = ntok, k = _matrix(x, "x", "[ntok, k]")
+    if len(getattr(a, "shape", ())) != 3 or len(getattr(b, "shape", ())) != 3:
+        raise ValueError("a must be [nadapters, max_rank, k], b [nadapters, nrows, max_rank]")
     na, max_rank, ka = a.shape
-    nrows = b.shape[1]
+    nb, nrows, rb = b.shape
     dev = x.device
-    if ka != k or tuple(b.shape) != (na, nrows, max_rank):
-        raise ValueError("a must be [nadapters, max_rank, k] and b [nadapters, nrows, max_rank]")
-    xt, ldx = _rows(x, "x", ntok, k, dev, (QMM_TYPE_F16, QMM_TYPE_F32))
+    if ka != k or nb != na or rb != max_rank:
+        raise ValueError("a must be [nadapters, max_rank, k], b [nadapters, nrows, max_rank]")
+    xt, ldx = _rows(x, "x", shape, dev, bf16=False)
     for t, name in ((a, "a"), (b, "b")):
-        _need(t, name, "f16", na * max_rank * 2, dev)
-        if _type_of(t.dtype) != QMM_TYPE_F16:
+        _need(t, name, "f16", 0, dev)
+        if _TYPE_OF.get(t.dtype) != QMM_TYPE_F16:
             raise ValueError(f"{name} must be float16")
     _need(ranks, "ranks", "i32", na * 4, dev)
     _need(scales, "scales", "f32", na * 4, dev)
     nseg = int(seg_adapter.numel())
     _need(seg_adapter, "seg_adapter", "i32", nseg * 4, dev)
     _need(seg_off, "seg_off", "i32", (nseg + 1) * 4, dev)
-    _, ldy = _rows(y, "y", ntok, nrows, dev, (QMM_TYPE_F32,))
-    ldb = ldy
-    if base is None:
-        base = y
-    else:
-        _, ldb = _rows(base, "base", ntok, nrows, dev, (QMM_TYPE_F32,))
+    shape = (ntok, nrows)
+    yt, ldy = _rows(y, "y", shape, dev)
+    bt, ldb = (yt, ldy) if base is None else _rows(base, "base", shape, dev)
+    if yt != QMM_TYPE_F32 or bt != QMM_TYPE_F32:
+        raise ValueError("y and base must be float32")
+    base = y if base is None else base
     ws = _scratch(ws, qmm_lora_workspace(ntok, max_rank), dev, stream)
     _call("qmm_lora", dev, stream, xt, x.data_ptr(), ldx, ntok, k, a.data_ptr(), b.data_ptr(), ranks.data_ptr(),
           scales.data_ptr(), na, max_rank, seg_off.data_ptr(), seg_adapter.data_ptr(), nseg, base.data_ptr(), ldb,
