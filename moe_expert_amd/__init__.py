@@ -586,6 +586,13 @@ def _rows(t, name, shape, device, bf16=True):
     return code, ld
 
 
+def _flat(t, name, dtype, count, device):
+    """t must be a contiguous tensor of `dtype` on `device` (a GPU) with at least `count` elements."""
+    if t.dtype != dtype or t.numel() < count or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of at least {count} elements on {device}")
+    return t
+
+
 _CURRENT = None
 
 
@@ -623,7 +630,7 @@ def _scratch(ws, nbytes, device, stream):
     """A caller's workspace (checked), or a new one that stays reserved for the stream it is used on."""
     import torch
     if ws is not None:
-        return _need(ws, "ws", "u8", nbytes, device)
+        return _flat(ws, "ws", torch.uint8, nbytes, device)
     ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
     if stream is not None:
         ws.record_stream(torch.cuda.ExternalStream(stream, device=device))
@@ -646,7 +653,7 @@ def qmm_rmsnorm(x, w, eps, res=None, res_out=None, y=None, yq=None, stream=None)
     if y is None and yq is None and res_out is None:
         raise ValueError("no output asked for")
     xt, ldx = _rows(x, "x", shape, dev)
-    _need(w, "w", "f32", hidden * 4, dev)
+    _flat(w, "w", torch.float32, hidden, dev)
     rt = ldr = ldro = yt = ldy = 0
     if res is not None:
         rt, ldr = _rows(res, "res", shape, dev)
@@ -665,7 +672,7 @@ def qmm_rmsnorm(x, w, eps, res=None, res_out=None, y=None, yq=None, stream=None)
         nbytes = ntok * (hidden // 32) * Q8_1_BYTES
         if yq is True:
             yq = torch.empty((ntok, (hidden // 32) * Q8_1_BYTES), dtype=torch.uint8, device=dev)
-        _need(yq, "yq", "u8", nbytes, dev)
+        _flat(yq, "yq", torch.uint8, nbytes, dev)
     _call("qmm_rmsnorm", dev, stream, xt, x.data_ptr(), ldx, rt, _addr(res), ldr, _addr(res_out), ldro, w.data_ptr(), eps,
           ntok, hidden, yt, _addr(y), ldy, _addr(yq))
     return y, yq, res_out
@@ -709,9 +716,13 @@ def qmm_moe_route(logits, topk, score=QMM_SCORE_SOFTMAX, bias=None, ngroups=1, t
     if topk < 1 or max(topk, ngroups, topk_groups, group_top) > 0x7FFFFFFF:
         raise ValueError("topk must be positive, and every count an int32")
     if bias is not None:
-        _need(bias, "bias", "f32", nexperts * 4, dev)
-    ids = _out(ids, "ids", "i32", ntok * topk * 4, dev, (ntok, topk), torch.int32)
-    weights = _out(weights, "weights", "f32", ntok * topk * 4, dev, (ntok, topk), torch.float32)
+        _flat(bias, "bias", torch.float32, nexperts, dev)
+    if ids is not None:
+        _flat(ids, "ids", torch.int32, ntok * topk, dev)
+    if weights is not None:
+        _flat(weights, "weights", torch.float32, ntok * topk, dev)
+    ids = torch.empty((ntok, topk), dtype=torch.int32, device=dev) if ids is None else ids
+    weights = torch.empty((ntok, topk), dtype=torch.float32, device=dev) if weights is None else weights
     _call("qmm_moe_route", dev, stream, lt, logits.data_ptr(), ldl, _addr(bias), ntok, nexperts, score, ngroups, topk_groups,
           group_top, topk, scale, ids.data_ptr(), weights.data_ptr(), QMM_ROUTE_RENORM if renorm else 0)
     return ids, weights
@@ -735,20 +746,24 @@ def qmm_moe_dispatch(ids, nexperts, sorted_tok=None, row_idx=None, expert_off=No
     dev = ids.device
     n = ntok * topk
     g = min(nexperts, n)
-    _need(ids, "ids", "i32", n * 4)
     if not 0 < nexperts <= 0x7FFFFFFF or topk < 1:
         raise ValueError("nexperts and topk must be positive, nexperts an int32")
     if (group_expert is None) != (group_off is None):
         raise ValueError("group_expert and group_off go together")
     i32 = torch.int32
-    sorted_tok = _out(sorted_tok, "sorted_tok", "i32", n * 4, dev, (n,), i32)
-    row_idx = _out(row_idx, "row_idx", "i32", n * 4, dev, (ntok, topk), i32)
-    expert_off = _out(expert_off, "expert_off", "i32", (nexperts + 1) * 4, dev, (nexperts + 1,), i32)
-    group_expert = _out(group_expert, "group_expert", "i32", g * 4, dev, (g,), i32)
-    group_off = _out(group_off, "group_off", "i32", (g + 1) * 4, dev, (g + 1,), i32)
+    _flat(ids, "ids", i32, n, dev)
+    sorted_tok = torch.empty(n, dtype=i32, device=dev) if sorted_tok is None else _flat(sorted_tok, "sorted_tok", i32, n, dev)
+    row_idx = torch.empty((ntok, topk), dtype=i32, device=dev) if row_idx is None else _flat(row_idx, "row_idx", i32, n, dev)
+    if expert_off is None:
+        expert_off = torch.empty(nexperts + 1, dtype=i32, device=dev)
+    if group_expert is None:
+        group_expert, group_off = torch.empty(g, dtype=i32, device=dev), torch.empty(g + 1, dtype=i32, device=dev)
+    _flat(expert_off, "expert_off", i32, nexperts + 1, dev)
+    _flat(group_expert, "group_expert", i32, g, dev)
+    _flat(group_off, "group_off", i32, g + 1, dev)
     ws = _scratch(ws, qmm_moe_dispatch_workspace(ntok, topk, nexperts), dev, stream)
     _call("qmm_moe_dispatch", dev, stream, ids.data_ptr(), ntok, topk, nexperts, sorted_tok.data_ptr(), row_idx.data_ptr(),
-          expert_off.data_ptr(), group_expert.data_ptr(), group_off.data_ptr(), ws.data_ptr(), _nbytes(ws))
+          expert_off.data_ptr(), group_expert.data_ptr(), group_off.data_ptr(), ws.data_ptr(), ws.numel())
     return sorted_tok, row_idx, expert_off, group_expert, group_off
 
 
@@ -765,6 +780,7 @@ def qmm_lora(x, a, b, ranks, scales, seg_off, seg_adapter, y, base=None, ws=None
     float16 [nadapters, nrows, max_rank], of which the first ranks[i] (int32) rows / columns are
     used; scales: float32 [nadapters]; seg_off: int32 [nseg+1]; seg_adapter: int32 [nseg]; y, base:
     float32 [ntok, nrows] with any row stride.  Returns y."""
+    import torch
     shape = ntok, k = _matrix(x, "x", "[ntok, k]")
     if len(getattr(a, "shape", ())) != 3 or len(getattr(b, "shape", ())) != 3:
         raise ValueError("a must be [nadapters, max_rank, k], b [nadapters, nrows, max_rank]")
@@ -774,15 +790,13 @@ def qmm_lora(x, a, b, ranks, scales, seg_off, seg_adapter, y, base=None, ws=None
     if ka != k or nb != na or rb != max_rank:
         raise ValueError("a must be [nadapters, max_rank, k], b [nadapters, nrows, max_rank]")
     xt, ldx = _rows(x, "x", shape, dev, bf16=False)
-    for t, name in ((a, "a"), (b, "b")):
-        _need(t, name, "f16", 0, dev)
-        if _TYPE_OF.get(t.dtype) != QMM_TYPE_F16:
-            raise ValueError(f"{name} must be float16")
-    _need(ranks, "ranks", "i32", na * 4, dev)
-    _need(scales, "scales", "f32", na * 4, dev)
-    nseg = int(seg_adapter.numel())
-    _need(seg_adapter, "seg_adapter", "i32", nseg * 4, dev)
-    _need(seg_off, "seg_off", "i32", (nseg + 1) * 4, dev)
+    _flat(a, "a", torch.float16, 0, dev)
+    _flat(b, "b", torch.float16, 0, dev)
+    _flat(ranks, "ranks", torch.int32, na, dev)
+    _flat(scales, "scales", torch.float32, na, dev)
+    nseg = seg_adapter.numel()
+    _flat(seg_adapter, "seg_adapter", torch.int32, nseg, dev)
+    _flat(seg_off, "seg_off", torch.int32, nseg + 1, dev)
     shape = (ntok, nrows)
     yt, ldy = _rows(y, "y", shape, dev)
     bt, ldb = (yt, ldy) if base is None else _rows(base, "base", shape, dev)
@@ -792,5 +806,5 @@ def qmm_lora(x, a, b, ranks, scales, seg_off, seg_adapter, y, base=None, ws=None
     ws = _scratch(ws, qmm_lora_workspace(ntok, max_rank), dev, stream)
     _call("qmm_lora", dev, stream, xt, x.data_ptr(), ldx, ntok, k, a.data_ptr(), b.data_ptr(), ranks.data_ptr(),
           scales.data_ptr(), na, max_rank, seg_off.data_ptr(), seg_adapter.data_ptr(), nseg, base.data_ptr(), ldb,
-          y.data_ptr(), ldy, nrows, ws.data_ptr(), _nbytes(ws))
+          y.data_ptr(), ldy, nrows, ws.data_ptr(), ws.numel())
     return y
