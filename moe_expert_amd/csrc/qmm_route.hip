@@ -23,25 +23,34 @@ struct RouteArgs {
 
 constexpr float kNever = -__builtin_inff();
 
-// Maximum and sum over aligned groups of L lanes (16, 32, 64), in every lane.
+// Maximum (of integers) and sum over aligned groups of L lanes (16, 32, 64), in every lane.
 template <int L>
-__device__ __forceinline__ float lanes_max(float v) {
-    v = fmaxf(v, dpp<0xB1>(v));
-    v = fmaxf(v, dpp<0x4E>(v));
-    v = fmaxf(v, dpp<0x141>(v));
-    v = fmaxf(v, dpp<0x140>(v));
+__device__ __forceinline__ int lanes_max(int v) {
+    const auto larger = [](int a, int b) { return a > b ? a : b; };
+    v = larger(v, __builtin_amdgcn_mov_dpp(v, 0xB1, 0xF, 0xF, true));
+    v = larger(v, __builtin_amdgcn_mov_dpp(v, 0x4E, 0xF, 0xF, true));
+    v = larger(v, __builtin_amdgcn_mov_dpp(v, 0x141, 0xF, 0xF, true));
+    v = larger(v, __builtin_amdgcn_mov_dpp(v, 0x140, 0xF, 0xF, true));
     if constexpr (L >= 32) {
-        const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false, false);
-        const uint32_t r0 = r[0], r1 = r[1];
-        v = fmaxf(__builtin_bit_cast(float, r0), __builtin_bit_cast(float, r1));
+        const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+        v = larger((int)r[0], (int)r[1]);
     }
     if constexpr (L >= 64) {
-        const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false, false);
-        const uint32_t r0 = r[0], r1 = r[1];
-        v = fmaxf(__builtin_bit_cast(float, r0), __builtin_bit_cast(float, r1));
+        const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        v = larger((int)r[0], (int)r[1]);
     }
     return v;
 }
+
+// Binary32 values (no NaN) as integers of the same order, -0 and +0 the same: maxima of integers need
+// none of the canonicalising moves that float maxima do.
+constexpr int kNeverKey = (int)0x80000000;  // below every value's
+__device__ __forceinline__ int key_of(float v) {
+    const int b = __builtin_bit_cast(int, v + 0.0f);
+    return b ^ ((b >> 31) & 0x7FFFFFFF);
+}
+__device__ __forceinline__ float value_of(int k) { return __builtin_bit_cast(float, k ^ ((k >> 31) & 0x7FFFFFFF)); }
+
 template <int L>
 __device__ __forceinline__ float lanes_sum(float v) {
     v += dpp<0xB1>(v);
@@ -91,7 +100,7 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
     // s: a factor of the score (softmax: over the sum, known for the whole row) or the score
     float sum = 1.0f;
     if (a.softmax) {
-        top = lanes_max<L>(top);
+        top = value_of(lanes_max<L>(key_of(top)));
         sum = 0.0f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -118,6 +127,7 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
         // a run's score: by its lanes where it is a power of two of whole lanes, else from LDS
         const int per = E / a.ngroups, lanes = per / V;
         __shared__ float members[T][L * V];
+        __shared__ int beaten[T][kRouteMaxGroups];
         float m0 = kNever, m1 = kNever;
         if (lanes * V == per && (lanes & (lanes - 1)) == 0) {
 #pragma unroll
@@ -147,36 +157,50 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
         }
         wave_sync();
         // experts of a run that at least topk_groups others beat are out
-        int last = -1;
-        bool out = false;
+        for (int r = q; r < a.ngroups; r += L) {
+            const float mine = runs[g][r];
+            int better = 0;
+            for (int o = 0; o < a.ngroups; ++o) {
+                const float x = runs[g][o];
+                better += (int)(x > mine) | ((int)(x == mine) & (int)(o < r));
+            }
+            beaten[g][r] = better >= a.topk_groups;
+        }
+        wave_sync();
+        int r = (e0 < E ? e0 : E - 1) / per, left = (r + 1) * per - e0;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int r = (e0 + v) / per;
-            if (e0 + v < E && r != last) {
-                const float mine = runs[g][r];
-                int better = 0;
-                for (int o = 0; o < a.ngroups; ++o) better += runs[g][o] > mine || (runs[g][o] == mine && o < r);
-                out = better >= a.topk_groups;
-                last = r;
+            if (v == left) {
+                r = r + 1 < a.ngroups ? r + 1 : r;
+                left += per;
             }
-            if (out) c[v] = kNever;
+            c[v] = beaten[g][r] ? kNever : c[v];
         }
     }
-    const int base = (threadIdx.x & 63) / L * L;  // this token's lanes in the ballot
-    for (int k = 0; k < a.topk; ++k) {
-        float m = c[0];
+    int key[V];
 #pragma unroll
-        for (int v = 1; v < V; ++v) m = fmaxf(m, c[v]);
-        const float best = lanes_max<L>(m);
-        const uint64_t hold = __ballot(m == best) >> base;
-        const bool own = (int)__builtin_ctzll(hold) == q;
-        if (own) {
+    for (int v = 0; v < V; ++v) key[v] = c[v] == kNever ? kNeverKey : key_of(c[v]);
+    for (int k = 0; k < a.topk; ++k) {
+        int m = key[0];
+#pragma unroll
+        for (int v = 1; v < V; ++v) m = key[v] > m ? key[v] : m;
+        const int best = lanes_max<L>(m);
+        // the lowest of this token's lanes that holds it
+        const uint64_t hold = __ballot(m == best);
+        int holder;
+        if constexpr (L == 64) {
+            holder = (int)__builtin_ctzll(hold);
+        } else {
+            const uint32_t half = threadIdx.x & 32 ? (uint32_t)(hold >> 32) : (uint32_t)hold;
+            holder = (int)__builtin_ctz(L == 32 ? half : half >> (threadIdx.x & 16));
+        }
+        if (holder == q) {
             int at = 0;
 #pragma unroll
-            for (int v = V - 1; v >= 0; --v) at = c[v] == best ? v : at;
+            for (int v = V - 1; v >= 0; --v) at = key[v] == best ? v : at;
 #pragma unroll
-            for (int v = 0; v < V; ++v) c[v] = v == at ? kNever : c[v];
-            chosen[g][k] = best == kNever ? -1 : e0 + at;
+            for (int v = 0; v < V; ++v) key[v] = v == at ? kNeverKey : key[v];
+            chosen[g][k] = best == kNeverKey ? -1 : e0 + at;
         }
     }
     wave_sync();
@@ -198,16 +222,16 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
 
 // ------------------------------------------------------------------ dispatch
 
-// A stable counting sort of the entries by expert.  One chunk (4096 entries): one workgroup counts,
-// scans and places.  More: one launch counts each chunk's experts, a second places every chunk from
+// A stable counting sort of the entries by expert.  Up to 4096 entries: one workgroup counts, scans
+// and places.  More: one launch counts each chunk's experts, a second places every chunk from
 // the counts of the chunks before it; beyond 64 chunks a launch between them sums the counts over the
 // chunks, so that no workgroup reads them all.  Within a chunk a wave takes consecutive entries, 64
 // at a time; an entry's place among its wave's entries of the same expert comes from ballots over
 // the expert's bits, so the order needs no atomics.  Bound: launches and dependent loads (8192 tokens
 // of top-8, 128 experts: 0.8 MB).
 
-constexpr int kDispThreads = 1024, kDispWaves = 16, kDispPer = 4;
-constexpr int kDispChunk = kDispThreads * kDispPer;
+constexpr int kDispThreads = 1024, kDispWaves = 16;
+constexpr int kDispOnePer = 4;   // entries a thread of a call of one chunk (4096 entries)
 constexpr int kDispDirect = 64;  // chunks whose counts a placing workgroup adds up itself
 
 struct DispatchArgs {
@@ -223,30 +247,34 @@ __device__ __forceinline__ int expert_at(const DispatchArgs& a, int p) {
     return e >= 0 && e < a.nexperts ? e : -1;
 }
 
-// Inclusive scan over the workgroup (16 waves), each wave by lane exchanges, the waves through LDS.
+// Inclusive scan over the workgroup (16 waves): rows of 16 lanes by DPP shifts, the rows of a wave by
+// the broadcasts of each row's (then each half's) last lane, the waves through LDS.
 __device__ __forceinline__ int workgroup_scan(int v, int* part) {
     const int l = threadIdx.x & 63, w = threadIdx.x >> 6;
-    for (int d = 1; d < 64; d <<= 1) {
-        const int u = __shfl_up(v, d, 64);
-        if (l >= d) v += u;
-    }
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);  // row_shr 1, 2, 4, 8
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // row_bcast 15 into rows 1, 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // row_bcast 31 into rows 2, 3
     if (l == 63) part[w] = v;
     __syncthreads();
     for (int u = 0; u < w; ++u) v += part[u];
     return v;
 }
 
-// counts[chunk][e]
+// counts[chunk][e], chunks of 1024 PER entries
+template <int PER>
 __global__ __launch_bounds__(kDispThreads) void dispatch_count_kernel(DispatchArgs a) {
     __shared__ int count[kRouteMaxExperts];
-    const int i = threadIdx.x, p0 = (int)blockIdx.x * kDispChunk;
-    int e[kDispPer];
+    const int i = threadIdx.x, p0 = (int)blockIdx.x * (PER * kDispThreads);
+    int e[PER];
 #pragma unroll
-    for (int u = 0; u < kDispPer; ++u) e[u] = expert_at(a, p0 + u * kDispThreads + i);
+    for (int u = 0; u < PER; ++u) e[u] = expert_at(a, p0 + u * kDispThreads + i);
     count[i] = 0;
     __syncthreads();
 #pragma unroll
-    for (int u = 0; u < kDispPer; ++u)
+    for (int u = 0; u < PER; ++u)
         if (e[u] >= 0) atomicAdd(&count[e[u]], 1);
     __syncthreads();
     if (i < a.nexperts) a.counts[(int64_t)blockIdx.x * a.nexperts + i] = count[i];
@@ -277,18 +305,19 @@ __global__ __launch_bounds__(kDispThreads) void dispatch_sum_kernel(DispatchArgs
 
 enum { kDispOne, kDispAdd, kDispSummed };
 
-// Workgroup = chunk.  MODE: how the entries of the other chunks are known.
-template <int MODE>
+// Workgroup = chunk of 1024 PER entries (kDispOne: all of them).  MODE: how the entries of the other
+// chunks are known.
+template <int MODE, int PER>
 __global__ __launch_bounds__(kDispThreads) void dispatch_place_kernel(DispatchArgs a) {
     extern __shared__ uint16_t seen[];  // [wave][expert]: entries of the waves before, then of the wave so far
-    __shared__ int first[kRouteMaxExperts], part[kDispWaves], part2[kDispWaves];
+    __shared__ int first[kRouteMaxExperts], part[kDispWaves], every;
     const int i = threadIdx.x, l = i & 63, w = i >> 6, E = a.nexperts;
     // entries per wave: whole runs of 64, as even as they go
-    const int per = MODE == kDispOne ? (a.n + kDispThreads - 1) / kDispThreads : kDispPer;
-    const int p0 = (int)blockIdx.x * kDispChunk + w * per * 64 + l;
-    int e[kDispPer], place[kDispPer];
+    const int per = MODE == kDispOne ? (a.n + kDispThreads - 1) / kDispThreads : PER;
+    const int begin = (int)blockIdx.x * (PER * kDispThreads), p0 = begin + w * per * 64 + l;
+    int e[PER], place[PER];
 #pragma unroll
-    for (int u = 0; u < kDispPer; ++u) e[u] = u < per ? expert_at(a, p0 + 64 * u) : -1;
+    for (int u = 0; u < PER; ++u) e[u] = u < per ? expert_at(a, p0 + 64 * u) : -1;
 
     int total = 0, before = 0;  // of expert i: all its entries, and those of earlier chunks
     if (i < E) {
@@ -308,7 +337,7 @@ __global__ __launch_bounds__(kDispThreads) void dispatch_place_kernel(DispatchAr
     for (int k = l; k < E; k += 64) mine[k] = 0;
     wave_sync();
 #pragma unroll
-    for (int u = 0; u < kDispPer; ++u) {
+    for (int u = 0; u < PER; ++u) {
         if (u >= per) break;
         uint64_t same = __ballot(e[u] >= 0);
         for (int b = 0; b < a.bits; ++b) {
@@ -333,31 +362,33 @@ __global__ __launch_bounds__(kDispThreads) void dispatch_place_kernel(DispatchAr
     }
     const int end = workgroup_scan(total, part);
     if (i < E) first[i] = end - total + before;
-    const int live = workgroup_scan(total > 0, part2);
-    if (i == kDispThreads - 1) part[0] = end;  // all entries (its reads ended before part2's barrier)
+    if (i == kDispThreads - 1) every = end;  // all entries
     __syncthreads();
-    const int all = part[0];
+    const int all = every;
 #pragma unroll
-    for (int u = 0; u < kDispPer; ++u) {
+    for (int u = 0; u < PER; ++u) {
         const int p = p0 + 64 * u;
         if (u >= per || p >= a.n) continue;
         const int at = e[u] >= 0 ? first[e[u]] + mine[e[u]] + place[u] : -1;
         a.row_idx[p] = at;
         if (at >= 0) a.sorted_tok[at] = p / a.topk;
     }
-    for (int p = (int)blockIdx.x * kDispChunk + i; p < a.n && p < ((int)blockIdx.x + 1) * kDispChunk; p += kDispThreads)
-        if (p >= all) a.sorted_tok[p] = -1;
+    for (int u = 0; u < PER; ++u) {
+        const int p = begin + u * kDispThreads + i;
+        if (p >= all && p < a.n) a.sorted_tok[p] = -1;
+    }
     if (blockIdx.x == 0) {
         if (i < E) a.expert_off[i] = end - total;
         if (i == 0) a.expert_off[E] = all;
         if (a.group_off) {
+            const int live = workgroup_scan(total > 0, part);
             if (total > 0) {
                 a.group_expert[live - 1] = i;
                 a.group_off[live - 1] = end - total;
             }
-            if (i == kDispThreads - 1) part[1] = live;
+            if (i == kDispThreads - 1) every = live;
             __syncthreads();
-            for (int g = part[1] + i; g <= a.ngroups; g += kDispThreads) {
+            for (int g = every + i; g <= a.ngroups; g += kDispThreads) {
                 if (g < a.ngroups) a.group_expert[g] = -1;
                 a.group_off[g] = all;
             }
@@ -405,7 +436,13 @@ extern "C" int qmm_moe_route(int ltype, const void* logits, int64_t ldl, const f
     return launch_status();
 }
 
-static int64_t dispatch_chunks(int64_t n) { return n <= kDispChunk ? 1 : (n + kDispChunk - 1) / kDispChunk; }
+// Entries a thread of a chunked call: 2 while a placing workgroup can add up all counts (65536 entries
+// 8.0 us; 9.2 with 4), else 8 (2M entries 29 us; 46 with 2).
+static int dispatch_per(int64_t n) { return n <= kDispDirect * 2 * kDispThreads ? 2 : 8; }
+static int64_t dispatch_chunks(int64_t n) {
+    const int64_t chunk = dispatch_per(n) * kDispThreads;
+    return n <= kDispOnePer * kDispThreads ? 1 : (n + chunk - 1) / chunk;
+}
 
 static bool dispatch_takes(int64_t ntok, int topk, int nexperts) {
     return ntok <= 0x7FFFFFFF && topk <= kRouteMaxTopk && nexperts <= kRouteMaxExperts && ntok * topk <= (int64_t)1 << 30;
@@ -438,15 +475,17 @@ extern "C" int qmm_moe_dispatch(const int32_t* ids, int64_t ntok, int topk, int 
     const size_t lds = (size_t)kDispWaves * nexperts * 2;
     const dim3 block(kDispThreads);
     if (chunks == 1) {
-        hipLaunchKernelGGL(dispatch_place_kernel<kDispOne>, dim3(1), block, lds, st, a);
-        return launch_status();
-    }
-    hipLaunchKernelGGL(dispatch_count_kernel, dim3((unsigned)chunks), block, 0, st, a);
-    if (chunks <= kDispDirect) {
-        hipLaunchKernelGGL(dispatch_place_kernel<kDispAdd>, dim3((unsigned)chunks), block, lds, st, a);
+        hipLaunchKernelGGL((dispatch_place_kernel<kDispOne, kDispOnePer>), dim3(1), block, lds, st, a);
+    } else if (dispatch_per(n) == 2) {
+        hipLaunchKernelGGL(dispatch_count_kernel<2>, dim3((unsigned)chunks), block, 0, st, a);
+        hipLaunchKernelGGL((dispatch_place_kernel<kDispAdd, 2>), dim3((unsigned)chunks), block, lds, st, a);
+    } else if (chunks <= kDispDirect) {
+        hipLaunchKernelGGL(dispatch_count_kernel<8>, dim3((unsigned)chunks), block, 0, st, a);
+        hipLaunchKernelGGL((dispatch_place_kernel<kDispAdd, 8>), dim3((unsigned)chunks), block, lds, st, a);
     } else {
+        hipLaunchKernelGGL(dispatch_count_kernel<8>, dim3((unsigned)chunks), block, 0, st, a);
         hipLaunchKernelGGL(dispatch_sum_kernel, dim3((unsigned)((nexperts + 63) / 64)), block, 0, st, a);
-        hipLaunchKernelGGL(dispatch_place_kernel<kDispSummed>, dim3((unsigned)chunks), block, lds, st, a);
+        hipLaunchKernelGGL((dispatch_place_kernel<kDispSummed, 8>), dim3((unsigned)chunks), block, lds, st, a);
     }
     return launch_status();
 }
