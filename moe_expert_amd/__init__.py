@@ -626,15 +626,22 @@ def _call(fn, device, stream, *args):
         raise QmmError(fn, rc)
 
 
+def _empty(shape, dtype, device, stream):
+    """A new tensor of the memory of the stream it is used on (the current one, or the one given): memory
+    that another stream's pending work has given back would still be written by it."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device)):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _scratch(ws, nbytes, device, stream):
-    """A caller's workspace (checked), or a new one that stays reserved for the stream it is used on."""
+    """A caller's workspace (checked), or a new one."""
     import torch
     if ws is not None:
         return _flat(ws, "ws", torch.uint8, nbytes, device)
-    ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
-    if stream is not None:
-        ws.record_stream(torch.cuda.ExternalStream(stream, device=device))
-    return ws
+    return _empty(max(nbytes, 16), torch.uint8, device, stream)
 
 
 def qmm_rmsnorm(x, w, eps, res=None, res_out=None, y=None, yq=None, stream=None):
@@ -664,14 +671,14 @@ def qmm_rmsnorm(x, w, eps, res=None, res_out=None, y=None, yq=None, stream=None)
         rt = ot
     if y is not None:
         if isinstance(y, torch.dtype):
-            y = torch.empty(shape, dtype=y, device=dev)
+            y = _empty(shape, y, dev, stream)
         yt, ldy = _rows(y, "y", shape, dev)
     if yq is not None:
         if hidden % 32:
             raise ValueError(f"hidden={hidden} is not a multiple of 32")
         nbytes = ntok * (hidden // 32) * Q8_1_BYTES
         if yq is True:
-            yq = torch.empty((ntok, (hidden // 32) * Q8_1_BYTES), dtype=torch.uint8, device=dev)
+            yq = _empty((ntok, (hidden // 32) * Q8_1_BYTES), torch.uint8, dev, stream)
         _flat(yq, "yq", torch.uint8, nbytes, dev)
     _call("qmm_rmsnorm", dev, stream, xt, x.data_ptr(), ldx, rt, _addr(res), ldr, _addr(res_out), ldro, w.data_ptr(), eps,
           ntok, hidden, yt, _addr(y), ldy, _addr(yq))
@@ -694,7 +701,7 @@ def qmm_dequantize_q8_1(xq, k, out=None, stream=None):
         raise ValueError("xq must hold whole q8_1 columns of width k")
     ncols, dev = _nbytes(xq) // col, xq.device
     if out is None or isinstance(out, torch.dtype):
-        out = torch.empty((ncols, k), dtype=out or torch.float32, device=dev)
+        out = _empty((ncols, k), out or torch.float32, dev, stream)
     ot, ldo = _rows(out, "out", (ncols, k), dev, bf16=False)
     _call("qmm_dequantize_q8_1", dev, stream, xq.data_ptr(), k, ncols, ot, out.data_ptr(), ldo)
     return out
@@ -721,8 +728,8 @@ def qmm_moe_route(logits, topk, score=QMM_SCORE_SOFTMAX, bias=None, ngroups=1, t
         _flat(ids, "ids", torch.int32, ntok * topk, dev)
     if weights is not None:
         _flat(weights, "weights", torch.float32, ntok * topk, dev)
-    ids = torch.empty((ntok, topk), dtype=torch.int32, device=dev) if ids is None else ids
-    weights = torch.empty((ntok, topk), dtype=torch.float32, device=dev) if weights is None else weights
+    ids = _empty((ntok, topk), torch.int32, dev, stream) if ids is None else ids
+    weights = _empty((ntok, topk), torch.float32, dev, stream) if weights is None else weights
     _call("qmm_moe_route", dev, stream, lt, logits.data_ptr(), ldl, _addr(bias), ntok, nexperts, score, ngroups, topk_groups,
           group_top, topk, scale, ids.data_ptr(), weights.data_ptr(), QMM_ROUTE_RENORM if renorm else 0)
     return ids, weights
@@ -752,12 +759,12 @@ def qmm_moe_dispatch(ids, nexperts, sorted_tok=None, row_idx=None, expert_off=No
         raise ValueError("group_expert and group_off go together")
     i32 = torch.int32
     _flat(ids, "ids", i32, n, dev)
-    sorted_tok = torch.empty(n, dtype=i32, device=dev) if sorted_tok is None else _flat(sorted_tok, "sorted_tok", i32, n, dev)
-    row_idx = torch.empty((ntok, topk), dtype=i32, device=dev) if row_idx is None else _flat(row_idx, "row_idx", i32, n, dev)
+    sorted_tok = _empty(n, i32, dev, stream) if sorted_tok is None else _flat(sorted_tok, "sorted_tok", i32, n, dev)
+    row_idx = _empty((ntok, topk), i32, dev, stream) if row_idx is None else _flat(row_idx, "row_idx", i32, n, dev)
     if expert_off is None:
-        expert_off = torch.empty(nexperts + 1, dtype=i32, device=dev)
+        expert_off = _empty(nexperts + 1, i32, dev, stream)
     if group_expert is None:
-        group_expert, group_off = torch.empty(g, dtype=i32, device=dev), torch.empty(g + 1, dtype=i32, device=dev)
+        group_expert, group_off = _empty(g, i32, dev, stream), _empty(g + 1, i32, dev, stream)
     _flat(expert_off, "expert_off", i32, nexperts + 1, dev)
     _flat(group_expert, "group_expert", i32, g, dev)
     _flat(group_off, "group_off", i32, g + 1, dev)

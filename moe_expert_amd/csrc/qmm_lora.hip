@@ -7,8 +7,8 @@
 // values for itself, measured slower: 9.4 against 8.0 us for 8 requests of one token at rank 16,
 // k 2560, 8192 rows; 40 against 13 us at rank 64, k 6144, 2560 rows.)
 //
-// Bound: the base and y.  8192 tokens x (2560 -> 8192), rank 16: 130 us for the 582 MB that cannot be
-// avoided (4.5 TB/s, a large copy reaches 5.0), of which the inner values 18 us; short calls are
+// Bound: the base and y.  8192 tokens x (2560 -> 8192), rank 16: 129 us for the 582 MB that cannot be
+// avoided (4.5 TB/s, a large copy reaches 5.0), of which the inner values 17 us; short calls are
 // bound by the chain of dependent loads segment -> adapter -> A, x -> inner values -> y.
 #include "qmm_values.h"
 
@@ -36,10 +36,29 @@ struct LoraTile {
 };
 
 // Tile `tile` of the segments' tiles of T tokens each (the last of a segment holds what is left):
-// its tokens [t0, t0 + nt) and their adapter, -1 for none.  Every lane of the wave calls it.
+// its tokens [t0, t0 + nt) and their adapter, -1 for none.  A scan of the segments' tile counts, 64 a
+// step; MANY, for more than 64 segments: four steps are skipped by their sum where the tile lies
+// beyond them (4096 segments 223 us against 407).  Every wave does its own, all lanes call it.
+template <bool MANY>
 __device__ __forceinline__ LoraTile find_tile(const LoraArgs& a, int T, int tile) {
     const int l = threadIdx.x & 63;
     for (int s0 = 0; s0 < a.nseg; s0 += 64) {
+        if constexpr (MANY) {
+            while (s0 + 256 <= a.nseg) {
+                int total = 0;
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    int o0 = a.seg_off[s0 + 64 * u + l], o1 = a.seg_off[s0 + 64 * u + l + 1];
+                    o0 = o0 < 0 ? 0 : o0 > a.ntok ? a.ntok : o0;
+                    o1 = o1 < o0 ? o0 : o1 > a.ntok ? a.ntok : o1;
+                    total += (o1 - o0 + T - 1) / T;
+                }
+                total = __builtin_amdgcn_readlane(wave_scan(total), 63);
+                if (total > tile) break;
+                tile -= total;
+                s0 += 256;
+            }
+        }
         const int s = s0 + l;
         int o0 = 0, o1 = 0, i = -1;
         if (s < a.nseg) {
@@ -57,17 +76,13 @@ __device__ __forceinline__ LoraTile find_tile(const LoraArgs& a, int T, int tile
         }
         o0 = o0 < 0 ? 0 : o0 > a.ntok ? a.ntok : o0;
         o1 = o1 < o0 ? o0 : o1 > a.ntok ? a.ntok : o1;
-        int end = (o1 - o0 + T - 1) / T;
-        const int n = end;
-        for (int d = 1; d < 64; d <<= 1) {
-            const int u = __shfl_up(end, d, 64);
-            if (l >= d) end += u;
-        }
-        const uint64_t past = __ballot(end > tile);
+        const int n = (o1 - o0 + T - 1) / T;
+        const int upto = wave_scan(n);
+        const uint64_t past = __ballot(upto > tile);
         if (past) {
             const int src = (int)__builtin_ctzll(past);
             LoraTile r;
-            r.t0 = __builtin_amdgcn_readlane(o0, src) + (tile - __builtin_amdgcn_readlane(end - n, src)) * T;
+            r.t0 = __builtin_amdgcn_readlane(o0, src) + (tile - __builtin_amdgcn_readlane(upto - n, src)) * T;
             const int left = __builtin_amdgcn_readlane(o1, src) - r.t0;
             r.nt = left < T ? left : T;
             r.adapter = __builtin_amdgcn_readlane(i, src);
@@ -76,7 +91,7 @@ __device__ __forceinline__ LoraTile find_tile(const LoraArgs& a, int T, int tile
             r.scale = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, scale), src));
             return r;
         }
-        tile -= __builtin_amdgcn_readlane(end, 63);
+        tile -= __builtin_amdgcn_readlane(upto, 63);
     }
     return {0, 0, -1, 0, 0.0f};
 }
@@ -160,11 +175,11 @@ __device__ __forceinline__ void down_tile_ranks(const LoraArgs& a, const LoraTil
 }
 
 // Workgroup (tile, split): the waves' sums joined in wave order into the split's inner values.
-template <int XT, int NR, int W>
+template <int XT, int NR, int W, bool MANY>
 __global__ __launch_bounds__(64 * W) void lora_down_kernel(LoraArgs a) {
     constexpr int T = 16, R = 16 * NR;
     __shared__ float part[W][T][R + 1];
-    const LoraTile tile = find_tile(a, T, blockIdx.x);
+    const LoraTile tile = find_tile<MANY>(a, T, blockIdx.x);
     if (tile.nt == 0 || tile.rank == 0) return;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     down_tile_ranks<XT, NR, R + 1>(a, tile, (int)blockIdx.y * W + w, W * a.split, part[w]);
@@ -243,7 +258,9 @@ typedef float f32x2 __attribute__((ext_vector_type(2)));
 // of product c takes row 2 (l % 32) + c, so a lane holds two neighbouring values of each token:
 // register r is token 8 (r / 4) + 4 (l / 32) + r % 4.  Every load is unconditional, at a clamped place
 // where the block ends inside the tile or the rows (with a branch around each load the wave waited
-// for one before the next: 8192 x 8192 took 190 us against 123).  VEC: an even number of rows, aligned.
+// for one before the next: 8192 x 8192 took 190 us against 123).  y is stored past the caches (129 us
+// against 144), the base is not read past them (517 tokens 23.2 us against 27.2): the projection has
+// just written it.  VEC: an even number of rows, aligned.
 template <bool VEC>
 struct UpBlock {
     static constexpr int CT = 2;
@@ -275,7 +292,7 @@ struct UpBlock {
             const int t = token(r);
             const float* p = base + (uint64_t)(uint32_t)(t < tile.nt ? t : tile.nt - 1) * (uint32_t)a.ldbase;
             if constexpr (VEC) {
-                in[r] = __builtin_nontemporal_load((const f32x2*)(p + (j < rows ? j : 0)));
+                in[r] = *((const f32x2*)(p + (j < rows ? j : 0)));
             } else {
 #pragma unroll
                 for (int c = 0; c < CT; ++c) in[r][c] = p[j + c < rows ? j + c : rows - 1];
@@ -348,13 +365,13 @@ __device__ __forceinline__ void copy_base(const LoraArgs& a, const LoraTile& til
 
 // Workgroup (row block, tile): 32 tokens by 256 rows of y, one UpBlock a wave, on the SPLIT parts of
 // the inner values that lora_down_kernel left.
-template <int SPLIT, bool VEC>
+template <int SPLIT, bool VEC, bool MANY>
 __global__ __launch_bounds__(256, SPLIT > 2 ? 2 : 4) void lora_up_kernel(LoraArgs a) {
     constexpr int T = kUpTokens, ROWS = kUpRows;
     extern __shared__ u32x4 frag[];
     __shared__ uint32_t largest[T];
     __shared__ float factor[T];
-    const LoraTile tile = find_tile(a, T, blockIdx.y);
+    const LoraTile tile = find_tile<MANY>(a, T, blockIdx.y);
     if (tile.nt == 0) return;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r0 = (int)blockIdx.x * ROWS;
     const float* base = a.base + (int64_t)tile.t0 * a.ldbase + r0;
@@ -390,8 +407,9 @@ constexpr int64_t kLoraMaxTokens = 1 << 20;
 constexpr int kLoraMaxSegments = 1 << 14;
 
 // How many workgroups share the columns of one token tile, so that few tiles still fill the GPU; the
-// outer product reads that many parts.  517 ragged tokens, rank 64: 27.5 us with 2, 29.8 with 4, 35
-// with 1; 8 tokens of 8 requests, rank 16: 8.0 us with 8.
+// outer product reads that many parts.  517 ragged tokens, ranks to 64: 27.5 us with 2, 29.8 with 4,
+// 35 with 1 (before the base was read through the caches: 23.2 now); 8 requests of one token, rank 16:
+// 7.5 us with 8.
 static int lora_split(int64_t ntok) { return ntok <= 64 ? 8 : ntok <= 1024 ? 2 : 1; }
 
 extern "C" size_t qmm_lora_workspace(int64_t ntok, int max_rank) {
@@ -399,23 +417,23 @@ extern "C" size_t qmm_lora_workspace(int64_t ntok, int max_rank) {
     return (size_t)lora_split(ntok) * ntok * max_rank * 4 + 16;
 }
 
-template <int XT>
+template <int XT, bool MANY>
 static void launch_down(const LoraArgs& p, hipStream_t st) {
     const dim3 grid((unsigned)(p.ntok / 16 + p.nseg), (unsigned)p.split);
-    if (p.max_rank <= 16) hipLaunchKernelGGL((lora_down_kernel<XT, 1, 8>), grid, dim3(512), 0, st, p);
-    else if (p.max_rank <= 32) hipLaunchKernelGGL((lora_down_kernel<XT, 2, 8>), grid, dim3(512), 0, st, p);
-    else if (p.max_rank <= 64) hipLaunchKernelGGL((lora_down_kernel<XT, 4, 8>), grid, dim3(512), 0, st, p);
-    else if (p.max_rank <= 128) hipLaunchKernelGGL((lora_down_kernel<XT, 8, 4>), grid, dim3(256), 0, st, p);
-    else hipLaunchKernelGGL((lora_down_kernel<XT, 16, 2>), grid, dim3(128), 0, st, p);
+    if (p.max_rank <= 16) hipLaunchKernelGGL((lora_down_kernel<XT, 1, 8, MANY>), grid, dim3(512), 0, st, p);
+    else if (p.max_rank <= 32) hipLaunchKernelGGL((lora_down_kernel<XT, 2, 8, MANY>), grid, dim3(512), 0, st, p);
+    else if (p.max_rank <= 64) hipLaunchKernelGGL((lora_down_kernel<XT, 4, 8, MANY>), grid, dim3(512), 0, st, p);
+    else if (p.max_rank <= 128) hipLaunchKernelGGL((lora_down_kernel<XT, 8, 4, MANY>), grid, dim3(256), 0, st, p);
+    else hipLaunchKernelGGL((lora_down_kernel<XT, 16, 2, MANY>), grid, dim3(128), 0, st, p);
 }
 
-template <bool VEC>
+template <bool VEC, bool MANY>
 static void launch_up(const LoraArgs& p, hipStream_t st) {
     const dim3 grid((unsigned)((p.nrows + kUpRows - 1) / kUpRows), (unsigned)(p.ntok / kUpTokens + p.nseg));
     const size_t lds = (size_t)((p.max_rank + 15) / 16) * 64 * kUpTokens;  // hi and lo fragments of every token
-    if (p.split == 8) hipLaunchKernelGGL((lora_up_kernel<8, VEC>), grid, dim3(256), lds, st, p);
-    else if (p.split == 2) hipLaunchKernelGGL((lora_up_kernel<2, VEC>), grid, dim3(256), lds, st, p);
-    else hipLaunchKernelGGL((lora_up_kernel<1, VEC>), grid, dim3(256), lds, st, p);
+    if (p.split == 8) hipLaunchKernelGGL((lora_up_kernel<8, VEC, MANY>), grid, dim3(256), lds, st, p);
+    else if (p.split == 2) hipLaunchKernelGGL((lora_up_kernel<2, VEC, MANY>), grid, dim3(256), lds, st, p);
+    else hipLaunchKernelGGL((lora_up_kernel<1, VEC, MANY>), grid, dim3(256), lds, st, p);
 }
 
 extern "C" int qmm_lora(int xtype, const void* x, int64_t ldx, int64_t ntok, int64_t k, const uint16_t* a, const uint16_t* b,
@@ -437,10 +455,13 @@ extern "C" int qmm_lora(int xtype, const void* x, int64_t ldx, int64_t ntok, int
     LoraArgs p{x, a, b, ranks, seg_off, seg_adapter, scales, base, y, (float*)ws, ldx, ldbase, ldy, (int)ntok, (int)k,
                nadapters, max_rank, nseg, (int)nrows, lora_split(ntok)};
     const hipStream_t st = as_stream(stream);
-    if (xtype == QMM_TYPE_F32) launch_down<kF32>(p, st);
-    else launch_down<kBin16>(p, st);
+    const bool many = nseg > 64;
+    if (xtype == QMM_TYPE_F32) many ? launch_down<kF32, true>(p, st) : launch_down<kF32, false>(p, st);
+    else many ? launch_down<kBin16, true>(p, st) : launch_down<kBin16, false>(p, st);
     // y and base 8 bytes at a time
-    if (aligned(base, 8) && aligned(y, 8) && ldbase % 2 == 0 && ldy % 2 == 0 && nrows % 2 == 0) launch_up<true>(p, st);
-    else launch_up<false>(p, st);
+    if (aligned(base, 8) && aligned(y, 8) && ldbase % 2 == 0 && ldy % 2 == 0 && nrows % 2 == 0)
+        many ? launch_up<true, true>(p, st) : launch_up<true, false>(p, st);
+    else
+        many ? launch_up<false, true>(p, st) : launch_up<false, false>(p, st);
     return launch_status();
 }

@@ -247,16 +247,10 @@ __device__ __forceinline__ int expert_at(const DispatchArgs& a, int p) {
     return e >= 0 && e < a.nexperts ? e : -1;
 }
 
-// Inclusive scan over the workgroup (16 waves): rows of 16 lanes by DPP shifts, the rows of a wave by
-// the broadcasts of each row's (then each half's) last lane, the waves through LDS.
+// Inclusive scan over the workgroup (16 waves), the waves' sums through LDS.
 __device__ __forceinline__ int workgroup_scan(int v, int* part) {
     const int l = threadIdx.x & 63, w = threadIdx.x >> 6;
-    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);  // row_shr 1, 2, 4, 8
-    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
-    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
-    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
-    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // row_bcast 15 into rows 1, 3
-    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // row_bcast 31 into rows 2, 3
+    v = wave_scan(v);
     if (l == 63) part[w] = v;
     __syncthreads();
     for (int u = 0; u < w; ++u) v += part[u];

@@ -26,6 +26,18 @@ __device__ __forceinline__ void store_value(void* p, int64_t i, int type, float 
     else ((uint16_t*)p)[i] = (uint16_t)(type == kBin16 ? f2h(v) : f2bf(v));
 }
 
+// Inclusive scan over the wave: rows of 16 lanes by DPP shifts, the rows by the broadcasts of each
+// row's (then each half's) last lane.
+__device__ __forceinline__ int wave_scan(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);  // row_shr 1, 2, 4, 8
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // row_bcast 15 into rows 1, 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // row_bcast 31 into rows 2, 3
+    return v;
+}
+
 // Eight consecutive values as loaded: 16 bytes of a 16-bit type, 32 of binary32.
 struct Raw8 {
     u32x4 a, b;

@@ -173,3 +173,33 @@ def test_lora_offsets_past_32_bits():
     M.qmm_lora(dev(x1), big, bb, rk, sc, dev(np.array([0, 20], np.int32)), dev(np.array([na - 1], np.int32)), y1, base=dev(base1))
     one = (x1, last[None], b1[None], np.array([r]), np.ones(1), np.array([0, 20]), np.array([0]), base1)
     check(one, host(y1))
+
+
+@pytest.mark.parametrize("nseg", [64, 65, 256, 700])
+def test_lora_many_segments(nseg):
+    """More segments than one step, or one round, of the kernels' scan takes; empty ones among them."""
+    rng = np.random.default_rng(nseg)
+    lens = rng.integers(0, 4, nseg)
+    arrays = inputs(nseg, int(lens.sum()), 128, 200, 16, lens, rng.integers(-1, 6, nseg), 6)
+    check(arrays, run(arrays))
+
+
+def test_lora_given_stream_allocates_there():
+    """A call on a given stream takes its workspace and nothing else from the caller's stream: memory
+    that pending work of the caller's stream has given back is not touched."""
+    import torch
+    arrays = inputs(21, 300, 512, 640, 16, [300], [0], 1)
+    x, a, b, ranks, scales, seg_off, adapters, base = [dev(v) for v in arrays]
+    want = M.qmm_lora(x, a, b, ranks, scales, seg_off, adapters, torch.empty_like(base), base=base)
+    side = torch.cuda.Stream()
+    y = torch.empty_like(base)
+    torch.cuda.synchronize()
+    n = M.qmm_lora_workspace(300, 16)
+    for _ in range(20):
+        junk = torch.empty(n, dtype=torch.uint8, device="cuda")
+        for _ in range(4):
+            junk.fill_(255)  # still running when its memory is given back
+        del junk
+        M.qmm_lora(x, a, b, ranks, scales, seg_off, adapters, y, base=base, stream=side.cuda_stream)
+    torch.cuda.synchronize()
+    assert torch.equal(y, want)
