@@ -260,8 +260,9 @@ typedef float f32x2 __attribute__((ext_vector_type(2)));
 // where the block ends inside the tile or the rows (with a branch around each load the wave waited
 // for one before the next: 8192 x 8192 took 190 us against 123).  y is stored past the caches (129 us
 // against 144), the base is not read past them (517 tokens 23.2 us against 27.2): the projection has
-// just written it.  VEC: an even number of rows, aligned.
-template <bool VEC>
+// just written it.  FEW: tiles of up to 8 tokens skip the registers of the others (64 requests of one
+// token 16.0 us against 19.2; the prompt 131 against 129 with it).  VEC: an even number of rows, aligned.
+template <bool VEC, bool FEW>
 struct UpBlock {
     static constexpr int CT = 2;
     f32x2 in[16];
@@ -289,6 +290,7 @@ struct UpBlock {
     __device__ __forceinline__ void load(const LoraArgs& a, const LoraTile& tile, int r0, const float* base) {
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
+            if (FEW && r == 4 && tile.nt <= 8) break;  // registers 4 and on are tokens 8 and on
             const int t = token(r);
             const float* p = base + (uint64_t)(uint32_t)(t < tile.nt ? t : tile.nt - 1) * (uint32_t)a.ldbase;
             if constexpr (VEC) {
@@ -339,6 +341,7 @@ struct UpBlock {
         }
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
+            if (FEW && r == 4 && tile.nt <= 8) break;
             const int t = token(r);
             const float f = factor[t];
             f32x2 o;
@@ -365,7 +368,7 @@ __device__ __forceinline__ void copy_base(const LoraArgs& a, const LoraTile& til
 
 // Workgroup (row block, tile): 32 tokens by 256 rows of y, one UpBlock a wave, on the SPLIT parts of
 // the inner values that lora_down_kernel left.
-template <int SPLIT, bool VEC, bool MANY>
+template <int SPLIT, bool VEC, bool MANY, bool FEW>
 __global__ __launch_bounds__(256, SPLIT > 2 ? 2 : 4) void lora_up_kernel(LoraArgs a) {
     constexpr int T = kUpTokens, ROWS = kUpRows;
     extern __shared__ u32x4 frag[];
@@ -378,7 +381,7 @@ __global__ __launch_bounds__(256, SPLIT > 2 ? 2 : 4) void lora_up_kernel(LoraArg
     float* y = a.y + (int64_t)tile.t0 * a.ldy + r0;
     const int rows = a.nrows - r0 < ROWS ? a.nrows - r0 : ROWS;
     if (tile.rank == 0) return copy_base(a, tile, base, y, rows);
-    UpBlock<VEC> blk(64 * w, rows);
+    UpBlock<VEC, FEW> blk(64 * w, rows);
     blk.load(a, tile, r0, base);
     make_fragments(tile, frag, largest, factor, [&](int tok, int j, float* v) {
         const float* p = a.v + ((int64_t)tile.t0 + tok) * a.max_rank + j;
@@ -409,7 +412,7 @@ constexpr int kLoraMaxSegments = 1 << 14;
 // How many workgroups share the columns of one token tile, so that few tiles still fill the GPU; the
 // outer product reads that many parts.  517 ragged tokens, ranks to 64: 27.5 us with 2, 29.8 with 4,
 // 35 with 1 (before the base was read through the caches: 23.2 now); 8 requests of one token, rank 16:
-// 7.5 us with 8.
+// 7.0 us with 8.
 static int lora_split(int64_t ntok) { return ntok <= 64 ? 8 : ntok <= 1024 ? 2 : 1; }
 
 extern "C" size_t qmm_lora_workspace(int64_t ntok, int max_rank) {
@@ -427,13 +430,13 @@ static void launch_down(const LoraArgs& p, hipStream_t st) {
     else hipLaunchKernelGGL((lora_down_kernel<XT, 16, 2, MANY>), grid, dim3(128), 0, st, p);
 }
 
-template <bool VEC, bool MANY>
+template <bool VEC, bool MANY, bool FEW>
 static void launch_up(const LoraArgs& p, hipStream_t st) {
     const dim3 grid((unsigned)((p.nrows + kUpRows - 1) / kUpRows), (unsigned)(p.ntok / kUpTokens + p.nseg));
     const size_t lds = (size_t)((p.max_rank + 15) / 16) * 64 * kUpTokens;  // hi and lo fragments of every token
-    if (p.split == 8) hipLaunchKernelGGL((lora_up_kernel<8, VEC, MANY>), grid, dim3(256), lds, st, p);
-    else if (p.split == 2) hipLaunchKernelGGL((lora_up_kernel<2, VEC, MANY>), grid, dim3(256), lds, st, p);
-    else hipLaunchKernelGGL((lora_up_kernel<1, VEC, MANY>), grid, dim3(256), lds, st, p);
+    if (p.split == 8) hipLaunchKernelGGL((lora_up_kernel<8, VEC, MANY, FEW>), grid, dim3(256), lds, st, p);
+    else if (p.split == 2) hipLaunchKernelGGL((lora_up_kernel<2, VEC, MANY, FEW>), grid, dim3(256), lds, st, p);
+    else hipLaunchKernelGGL((lora_up_kernel<1, VEC, MANY, FEW>), grid, dim3(256), lds, st, p);
 }
 
 extern "C" int qmm_lora(int xtype, const void* x, int64_t ldx, int64_t ntok, int64_t k, const uint16_t* a, const uint16_t* b,
@@ -459,9 +462,11 @@ extern "C" int qmm_lora(int xtype, const void* x, int64_t ldx, int64_t ntok, int
     if (xtype == QMM_TYPE_F32) many ? launch_down<kF32, true>(p, st) : launch_down<kF32, false>(p, st);
     else many ? launch_down<kBin16, true>(p, st) : launch_down<kBin16, false>(p, st);
     // y and base 8 bytes at a time
-    if (aligned(base, 8) && aligned(y, 8) && ldbase % 2 == 0 && ldy % 2 == 0 && nrows % 2 == 0)
-        many ? launch_up<true, true>(p, st) : launch_up<true, false>(p, st);
-    else
-        many ? launch_up<false, true>(p, st) : launch_up<false, false>(p, st);
+    const bool vec = aligned(base, 8) && aligned(y, 8) && ldbase % 2 == 0 && ldy % 2 == 0 && nrows % 2 == 0;
+    const bool few = ntok <= 8 * (int64_t)nseg;  // tiles of up to 8 tokens on average
+    if (vec && many) few ? launch_up<true, true, true>(p, st) : launch_up<true, true, false>(p, st);
+    else if (vec) few ? launch_up<true, false, true>(p, st) : launch_up<true, false, false>(p, st);
+    else if (many) few ? launch_up<false, true, true>(p, st) : launch_up<false, true, false>(p, st);
+    else few ? launch_up<false, false, true>(p, st) : launch_up<false, false, false>(p, st);
     return launch_status();
 }
