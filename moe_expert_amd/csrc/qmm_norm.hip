@@ -171,7 +171,8 @@ __device__ __forceinline__ void store_lane_block(const NormArgs& a, int64_t t, i
 }
 
 // The same for rows of any width and alignment: thread i holds the values i, i + blockDim.x, ... (NE
-// of them), read and written one at a time; 32 consecutive lanes hold one q8_1 block.
+// of them), read and written one at a time, neighbouring lanes at neighbouring values; 32 consecutive
+// lanes hold one q8_1 block.  517 x 1001 bfloat16: 3.4 us.
 template <int NE>
 __global__ __launch_bounds__(1024) void rmsnorm_any_kernel(NormArgs a) {
     const int threads = (int)blockDim.x, tid = (int)threadIdx.x;
@@ -252,7 +253,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_long_kernel(NormArgs a) {
     }
 }
 
-// One thread per 4 values of a block.
+// One thread per 4 values of a block (a dword of the block).  Bound: bytes; 1 x 2560: 2.0 us, a launch.
 __global__ __launch_bounds__(256) void dequantize_q8_1_kernel(const uint8_t* __restrict__ xq, int nb, int64_t nblk, int otype,
                                                               void* __restrict__ out, int64_t ldo) {
     const int64_t g = (int64_t)blockIdx.x * 256 + threadIdx.x;
