@@ -225,8 +225,9 @@ size_t qgemm_prefill_experts_workspace(int nexperts, int64_t inter, int64_t nent
  *                                                        y 16-byte aligned)
  *   x_f16      : binary16 [ntok][hidden], 16-byte aligned.
  *   sorted_tok : int32 [nentries]; a token outside [0, ntok) reads zeros.  expert_off: int32
- *                [nexperts+1], non-decreasing, expert_off[nexperts] == nentries (offsets are
- *                clamped to [0, nentries]; rows of no expert are not written).
+ *                [nexperts+1], non-decreasing, expert_off[nexperts] <= nentries (offsets are
+ *                clamped to [0, nentries]; rows of no expert, as those past a qmm_moe_dispatch's
+ *                last entry, are not written).
  *   w_gate, w_up (format wtype_gu, inter rows of width hidden) and w_down (wtype_down, hidden
  *   rows of width inter) at e * stride; Q8_0 or IQ4_NL (CB3: QMM_EUNSUPPORTED); 4-byte
  *   aligned, strides multiples of 4.

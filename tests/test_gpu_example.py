@@ -90,3 +90,38 @@ def test_block_decode_in_a_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want) and torch.equal(kept, mine)
+
+
+@pytest.mark.parametrize("path", ["decode", "prompt"])
+def test_tokens_without_experts(path):
+    """Tokens whose logits are all masked get ids of -1: the dispatch drops them, the products do not
+    touch their rows, the combine gives zeros, and the other tokens' results keep their bits."""
+    import torch
+    from examples import moe_block as E
+    b = E.Block(seed=5, hidden=512, inter=256, nexperts=16, topk=4)
+    n = 12 if path == "decode" else 200
+    g = torch.Generator(device="cuda").manual_seed(2)
+    h = torch.randn(n, b.hidden, generator=g, device="cuda")
+    logits = torch.randn(n, b.nexperts, generator=g, device="cuda")
+    gone = torch.zeros(n, dtype=torch.bool, device="cuda")
+    gone[::3] = True
+
+    def experts(z):
+        ids, w = M.qmm_moe_route(z, b.topk)
+        tok, row, off, ge, go = M.qmm_moe_dispatch(ids, b.nexperts)
+        if path == "decode":
+            y, _ = M.qgemv_grouped_experts(M.QMM_IQ4_NL, b.gate, b.up, M.QMM_Q8_0, b.down, b.hidden, b.inter,
+                                           M.qmm_quantize_q8_1(h), ge, go, tok, y=torch.zeros(n * b.topk, b.hidden, device="cuda"))
+        else:
+            y, _ = M.qgemm_prefill_experts(M.QMM_IQ4_NL, b.gate, b.up, M.QMM_Q8_0, b.down, b.nexperts, b.hidden, b.inter, h.half(),
+                                           tok, off, y=torch.zeros(n * b.topk, b.hidden, device="cuda"))
+        return M.qmm_moe_combine(y, row, w), ids
+
+    full, _ = experts(logits)
+    masked = logits.clone()
+    masked[gone] = float("-inf")
+    some, ids = experts(masked)
+    assert (ids[gone] == -1).all() and (some[gone] == 0).all()
+    assert torch.equal(some[~gone], full[~gone])
+    none, _ = experts(torch.full_like(logits, float("-inf")))
+    assert (none == 0).all()
