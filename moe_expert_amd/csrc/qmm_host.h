@@ -15,10 +15,6 @@ inline int64_t row_bytes_of(int wtype, int64_t k) { return qmm_row_bytes(wtype, 
 
 inline bool valid_wtype(int wtype) { return wtype == QMM_Q8_0 || wtype == QMM_IQ4_NL || wtype == QMM_CB3; }
 
-// QMM_TYPE_*: known, and bytes of one value
-inline bool valid_type(int t) { return t == QMM_TYPE_F32 || t == QMM_TYPE_F16 || t == QMM_TYPE_BF16; }
-inline uintptr_t type_bytes(int t) { return t == QMM_TYPE_F32 ? 4 : 2; }
-
 // Status after a launch: QMM_EHIP if the runtime recorded a launch error.
 inline int launch_status() {
     const hipError_t e = hipGetLastError();

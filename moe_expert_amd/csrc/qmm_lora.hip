@@ -406,7 +406,7 @@ __global__ __launch_bounds__(256, SPLIT > 2 ? 2 : 4) void lora_up_kernel(LoraArg
 
 }  // namespace qmm
 
-#include "qmm_host.h"
+#include "qmm_types.h"
 
 using namespace qmm;
 

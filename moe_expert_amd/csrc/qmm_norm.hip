@@ -270,7 +270,7 @@ __global__ __launch_bounds__(256) void dequantize_q8_1_kernel(const uint8_t* __r
 
 }  // namespace qmm
 
-#include "qmm_host.h"
+#include "qmm_types.h"
 
 using namespace qmm;
 

@@ -402,7 +402,7 @@ __global__ __launch_bounds__(kDispThreads) void dispatch_place_kernel(DispatchAr
 
 }  // namespace qmm
 
-#include "qmm_host.h"
+#include "qmm_types.h"
 
 using namespace qmm;
 
