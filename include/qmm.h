@@ -412,8 +412,8 @@ size_t qmm_lora_workspace(int64_t ntok, int max_rank);
 /* Low-rank adapters of many requests beside a shared projection (qgemv_dense*, qgemm_dense): tokens
  * seg_off[s] .. seg_off[s+1]-1 belong to request s and use adapter i = seg_adapter[s]:
  *   y[t][r] = base[t][r] + scales[i] * sum_j B[i][r][j] * (sum_c A[i][j][c] * x[t][c]),  j < ranks[i]
- * with binary32 sums; the inner sums enter the outer product with at least 20 bits below the
- * token's largest one.  A segment whose adapter is outside [0, nadapters) gives y = base.
+ * with binary32 sums, of the inner product and, from those sums as they are, of the outer one.  A
+ * segment whose adapter is outside [0, nadapters) gives y = base.
  *   x    : QMM_TYPE_F16 or QMM_TYPE_F32 [ntok][ldx], 16-byte aligned, ldx * element size a
  *          multiple of 16.
  *   a    : binary16 [nadapters][max_rank][k];  b : binary16 [nadapters][nrows][max_rank]; 16-byte

@@ -27,6 +27,7 @@ struct LoraArgs {
 };
 
 typedef _Float16 half8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
@@ -201,54 +202,46 @@ __global__ __launch_bounds__(64 * W) void lora_down_kernel(LoraArgs a) {
 
 constexpr int kUpTokens = 32, kUpRows = 256;  // of y per workgroup: one block of 64 rows a wave
 
-// The inner values of a tile as binary16 fragments in LDS.  Each token's are scaled by the power of
-// two that puts the largest into [512, 1024) and cut into high and low parts, v = hi + lo to 2^-24
-// of the largest, so that the product with B runs on binary16 MFMA with nothing lost to its range:
-// acc = hi B + lo B, y = base + acc * factor, factor = scale 2^e.  frag: [hi, lo][step][half][token],
-// 8 consecutive ranks each.  fetch(token, j, v) adds the values j .. j+7 of a token to v.
-template <class F>
-__device__ __forceinline__ void make_fragments(const LoraTile& tile, u32x4* frag, uint32_t* largest, float* factor, F fetch) {
-    constexpr int T = kUpTokens, G = 256 / T;  // G threads per token
-    constexpr int MAXG = kLoraMaxRank / 8 / G;
-    const int tid = threadIdx.x, tok = tid % T, g0 = tid / T, steps = (tile.rank + 15) / 16;
-    if (tid < T) largest[tid] = 0;
-    float v[MAXG][8];
-    uint32_t big = 0;
-#pragma unroll
-    for (int i = 0; i < MAXG; ++i) {
-        const int j = 8 * (g0 + G * i);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[i][e] = 0.0f;
-        if (tok < tile.nt && j < tile.rank) {
-            fetch(tok, j, v[i]);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                if (j + e >= tile.rank) v[i][e] = 0.0f;
-                const uint32_t b = __builtin_bit_cast(uint32_t, v[i][e]) & 0x7FFFFFFFu;
-                if (b < 0x7F800000u && b > big) big = b;  // infinities and NaN keep to themselves
-            }
-        }
+// A binary32 value as three bfloat16 parts, v = v1 + v2 + v3 exactly (8 bits each, cut, not rounded, so
+// none overflows); an infinity or NaN is the first part alone.  Parts are the high halves of words.
+__device__ __forceinline__ void split3(float v, uint32_t* p) {
+    p[0] = __builtin_bit_cast(uint32_t, v) & 0xFFFF0000u;
+    p[1] = p[2] = 0;
+    if (v != v) p[0] = 0x7FC00000u;
+    if (__builtin_isfinite(v)) {
+        const float r = v - __builtin_bit_cast(float, p[0]);
+        p[1] = __builtin_bit_cast(uint32_t, r) & 0xFFFF0000u;
+        p[2] = __builtin_bit_cast(uint32_t, r - __builtin_bit_cast(float, p[1]));
     }
-    __syncthreads();
-    if (big) atomicMax(&largest[tok], big);
-    __syncthreads();
-    // the largest is in [2^ex, 2^(ex+1)) or subnormal; no scaling where there is no finite one but 0
-    const int ex = largest[tok] ? (int)(largest[tok] >> 23) - 127 : 9;
-    if (tid < T) factor[tid] = ldexpf(tile.scale, ex - 9);
-    const int part = steps * 2 * T;
+}
+
+// The high halves of two words as one.
+__device__ __forceinline__ uint32_t high_halves(uint32_t lo, uint32_t hi) { return __builtin_amdgcn_perm(hi, lo, 0x07060302u); }
+
+// The inner values of a tile in LDS, each as its three parts, in the order the outer product's A operand
+// takes them.  frag: [part][step of 16 ranks][half][token], 8 consecutive ranks each; zeros past the
+// rank and past the tile's tokens.  fetch(token, j, v) adds the values j .. j+7 of a token to v.
+template <class F>
+__device__ __forceinline__ void make_fragments(const LoraTile& tile, u32x4* frag, F fetch) {
+    constexpr int T = kUpTokens, G = 256 / T;  // G threads per token
+    const int tok = threadIdx.x % T, steps = (tile.rank + 15) / 16, part = steps * 2 * T;
+#pragma unroll 1
+    for (int g = threadIdx.x / T; g < 2 * steps; g += G) {
+        float v[8];
 #pragma unroll
-    for (int i = 0; i < MAXG; ++i) {
-        const int g = g0 + G * i;
-        if (g < 2 * steps) {
-            half8 hi, lo;
+        for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+        if (tok < tile.nt && 8 * g < tile.rank) fetch(tok, 8 * g, v);
+        uint32_t p[8][3];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float s = ldexpf(v[i][e], 9 - ex);
-                hi[e] = (_Float16)s;
-                lo[e] = __builtin_isfinite(s) ? (_Float16)(s - (float)hi[e]) : (_Float16)0.0f;
-            }
-            frag[g * T + tok] = __builtin_bit_cast(u32x4, hi);
-            frag[part + g * T + tok] = __builtin_bit_cast(u32x4, lo);
+        for (int e = 0; e < 8; ++e) split3(8 * g + e < tile.rank ? v[e] : 0.0f, p[e]);
+#pragma unroll
+        for (int n = 0; n < 3; ++n) {
+            u32x4 w;
+            w.x = high_halves(p[0][n], p[1][n]);
+            w.y = high_halves(p[2][n], p[3][n]);
+            w.z = high_halves(p[4][n], p[5][n]);
+            w.w = high_halves(p[6][n], p[7][n]);
+            frag[n * part + g * T + tok] = w;
         }
     }
     __syncthreads();
@@ -262,8 +255,11 @@ typedef float f32x2 __attribute__((ext_vector_type(2)));
 // where the block ends inside the tile or the rows (with a branch around each load the wave waited
 // for one before the next: 8192 x 8192 took 190 us against 123).  y is stored past the caches (129 us
 // against 144), the base is not read past them (517 tokens 23.2 us against 27.2): the projection has
-// just written it.  FEW: tiles of up to 8 tokens skip the registers of the others (64 requests of one
-// token 16.0 us against 19.2; the prompt 131 against 129 with it).  VEC: an even number of rows, aligned.
+// just written it.  The product is binary32's on bfloat16 MFMA: the three parts of a value times the two
+// of B (11 bits), six exact products into the binary32 sum.  The binary32 MFMA instead has a sixteenth
+// of the rate (517 tokens 25.2 us against 23.8; 64 requests of one token 18.5 against 14.6; 8192 tokens
+// at rank 256 336 against 306).  FEW: tiles of up to 8 tokens skip the registers of the others.
+// VEC: an even number of rows, aligned.
 template <bool VEC, bool FEW>
 struct UpBlock {
     static constexpr int CT = 2;
@@ -279,15 +275,11 @@ struct UpBlock {
         j = rb + CT * col;
     }
     __device__ __forceinline__ int token(int r) const { return 8 * (r / 4) + 4 * h + r % 4; }
-    // steps s and s + 1 (those there are) of B, as they lie there
-    __device__ __forceinline__ void load_b(const LoraArgs& a, int s, int steps) {
+    // 16-rank step s of B, as it lies there
+    __device__ __forceinline__ void load_b(half8* w, const LoraArgs& a, int s) const {
+        const int k = 16 * s + 8 * h;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            if (s + u >= steps) break;
-            const int k = 16 * (s + u) + 8 * h;
-#pragma unroll
-            for (int c = 0; c < CT; ++c) b[u][c] = *(const half8*)(br[c] + (k < a.max_rank ? k : 0));
-        }
+        for (int c = 0; c < CT; ++c) w[c] = *(const half8*)(br[c] + (k < a.max_rank ? k : 0));
     }
     __device__ __forceinline__ void load(const LoraArgs& a, const LoraTile& tile, int r0, const float* base) {
 #pragma unroll
@@ -305,58 +297,112 @@ struct UpBlock {
 #pragma unroll
         for (int c = 0; c < CT; ++c)
             br[c] = a.b + ((int64_t)tile.adapter * a.nrows + r0 + (j + c < rows ? j + c : rows - 1)) * a.max_rank;
-        load_b(a, 0, (tile.rank + 15) / 16);
+        load_b(b[0], a, 0);
+        if (tile.rank > 16) load_b(b[1], a, 1);
     }
-    __device__ __forceinline__ void multiply_store(const LoraArgs& a, const LoraTile& tile, const u32x4* frag,
-                                                   const float* factor, float* y) {
+    // Columns of B past the rank may hold anything: zeros there.
+    __device__ __forceinline__ void mask_b(half8& w, int s, int rank) const {
+        if (16 * s + 16 > rank) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = 16 * s + 8 * h + e < rank ? w[e] : (_Float16)0.0f;
+        }
+    }
+    __device__ __forceinline__ void multiply_store(const LoraArgs& a, const LoraTile& tile, const u32x4* frag, float* y) {
         constexpr int T = kUpTokens;
         const int steps = (tile.rank + 15) / 16, part = steps * 2 * T;
         f32x16 acc[CT];
 #pragma unroll
         for (int c = 0; c < CT; ++c) acc[c] = f32x16{};
         for (int s = 0; s < steps; s += 2) {
-            half8 cur[2][CT];
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int c = 0; c < CT; ++c) cur[u][c] = b[u][c];
-            if (s + 2 < steps) load_b(a, s + 2, steps);
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                if (s + u < steps) {
-                    const int k = 16 * (s + u) + 8 * h;
-                    if (16 * (s + u) + 16 > tile.rank) {  // columns past the rank may hold anything
+                if (s + u >= steps) break;
+                const u32x4* f = frag + (2 * (s + u) + h) * T + col;
 #pragma unroll
-                        for (int c = 0; c < CT; ++c)
+                for (int c = 0; c < CT; ++c) {
+                    mask_b(b[u][c], s + u, tile.rank);
+                    u32x4 w1, w2;  // w = w1 + w2 exactly: 8 and 3 bits
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) cur[u][c][e] = k + e < tile.rank ? cur[u][c][e] : (_Float16)0.0f;
+                    for (int i = 0; i < 4; ++i) {
+                        const float lo = (float)b[u][c][2 * i], hi = (float)b[u][c][2 * i + 1];
+                        const uint32_t lu = __builtin_bit_cast(uint32_t, lo), hu = __builtin_bit_cast(uint32_t, hi);
+                        w1[i] = high_halves(lu, hu);
+                        w2[i] = high_halves(__builtin_bit_cast(uint32_t, lo - __builtin_bit_cast(float, lu & 0xFFFF0000u)),
+                                            __builtin_bit_cast(uint32_t, hi - __builtin_bit_cast(float, hu & 0xFFFF0000u)));
                     }
-                    const half8 hi = __builtin_bit_cast(half8, frag[(2 * (s + u) + h) * T + col]);
-                    const half8 lo = __builtin_bit_cast(half8, frag[part + (2 * (s + u) + h) * T + col]);
 #pragma unroll
-                    for (int c = 0; c < CT; ++c) {
-                        acc[c] = __builtin_amdgcn_mfma_f32_32x32x16_f16(lo, cur[u][c], acc[c], 0, 0, 0);
-                        acc[c] = __builtin_amdgcn_mfma_f32_32x32x16_f16(hi, cur[u][c], acc[c], 0, 0, 0);
+                    for (int n = 2; n >= 0; --n) {
+                        const bf8 v = __builtin_bit_cast(bf8, f[n * part]);
+                        acc[c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, __builtin_bit_cast(bf8, w2), acc[c], 0, 0, 0);
+                        acc[c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, __builtin_bit_cast(bf8, w1), acc[c], 0, 0, 0);
                     }
+                    __builtin_amdgcn_sched_barrier(0);  // what is in flight across it did not fit the registers
                 }
+                if (s + u + 2 < steps) load_b(b[u], a, s + u + 2);
             }
+        }
+        // An infinity times the parts of a value is not the infinity times the value (a part may be 0 or of
+        // the other sign): sums that are not finite are formed once more in binary32, the others stay.
+        float odd = 0.0f;
+#pragma unroll
+        for (int c = 0; c < CT; ++c)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) odd = __builtin_fmaf(acc[c][r], 0.0f, odd);
+        uint32_t redo = 0;
+        if (odd != odd) {
+#pragma unroll
+            for (int c = 0; c < CT; ++c)
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    if (!__builtin_isfinite(acc[c][r])) {
+                        acc[c][r] = 0.0f;
+                        redo |= 1u << (16 * c + r);
+                    }
         }
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
             if (FEW && r == 4 && tile.nt <= 8) break;
-            const int t = token(r);
-            const float f = factor[t];
-            f32x2 o;
 #pragma unroll
-            for (int c = 0; c < CT; ++c) o[c] = in[r][c] + acc[c][r] * f;
+            for (int c = 0; c < CT; ++c) in[r][c] = in[r][c] + acc[c][r] * tile.scale;
+        }
+        if (__ballot(redo != 0)) add_in_binary32(a, tile, frag, redo);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            if (FEW && r == 4 && tile.nt <= 8) break;
+            const int t = token(r);
             float* p = y + (uint64_t)(uint32_t)t * (uint32_t)a.ldy + j;
             if constexpr (VEC) {
-                if (t < tile.nt && j < rows) __builtin_nontemporal_store(o, (f32x2*)p);
+                if (t < tile.nt && j < rows) __builtin_nontemporal_store(in[r], (f32x2*)p);
             } else if (t < tile.nt) {
 #pragma unroll
                 for (int c = 0; c < CT; ++c)
-                    if (j + c < rows) p[c] = o[c];
+                    if (j + c < rows) p[c] = in[r][c];
             }
+        }
+    }
+    __device__ __forceinline__ void add_in_binary32(const LoraArgs& a, const LoraTile& tile, const u32x4* frag, uint32_t redo) {
+        constexpr int T = kUpTokens;
+        const int steps = (tile.rank + 15) / 16, part = steps * 2 * T;
+#pragma unroll
+        for (int c = 0; c < CT; ++c) {
+            f32x16 sum = f32x16{};
+#pragma unroll 1
+            for (int s = 0; s < steps; ++s) {
+                const u32x4* f = frag + (2 * s + h) * T + col;
+                load_b(b[0], a, s);
+                mask_b(b[0][c], s, tile.rank);
+                const u32x4 v1 = f[0], v2 = f[part], v3 = f[2 * part];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const auto value = [&](const u32x4& p) {
+                        return __builtin_bit_cast(float, e & 1 ? p[e / 2] & 0xFFFF0000u : p[e / 2] << 16);
+                    };
+                    sum = __builtin_amdgcn_mfma_f32_32x32x2f32(value(v1) + (value(v2) + value(v3)), (float)b[0][c][e], sum, 0, 0, 0);
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                if (redo >> (16 * c + r) & 1) in[r][c] += sum[r] * tile.scale;
         }
     }
 };
@@ -376,8 +422,6 @@ template <int SPLIT, bool VEC, bool MANY, bool FEW>
 __global__ __launch_bounds__(256, SPLIT > 2 ? 2 : 4) void lora_up_kernel(LoraArgs a) {
     constexpr int T = kUpTokens, ROWS = kUpRows;
     extern __shared__ u32x4 frag[];
-    __shared__ uint32_t largest[T];
-    __shared__ float factor[T];
     const LoraTile tile = find_tile<MANY>(a, T, blockIdx.y);
     if (tile.nt == 0) return;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r0 = (int)blockIdx.x * ROWS;
@@ -387,7 +431,7 @@ __global__ __launch_bounds__(256, SPLIT > 2 ? 2 : 4) void lora_up_kernel(LoraArg
     if (tile.rank == 0) return copy_base(a, tile, base, y, rows);
     UpBlock<VEC, FEW> blk(64 * w, rows);
     blk.load(a, tile, r0, base);
-    make_fragments(tile, frag, largest, factor, [&](int tok, int j, float* v) {
+    make_fragments(tile, frag, [&](int tok, int j, float* v) {
         const float* p = a.v + ((int64_t)tile.t0 + tok) * a.max_rank + j;
         f32x4 u[SPLIT][2];
 #pragma unroll
@@ -401,7 +445,7 @@ __global__ __launch_bounds__(256, SPLIT > 2 ? 2 : 4) void lora_up_kernel(LoraArg
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] += u[s][e / 4][e % 4];
     });
-    blk.multiply_store(a, tile, frag, factor, y);
+    blk.multiply_store(a, tile, frag, y);
 }
 
 }  // namespace qmm
@@ -437,7 +481,7 @@ static void launch_down(const LoraArgs& p, hipStream_t st) {
 template <bool VEC, bool MANY, bool FEW>
 static void launch_up(const LoraArgs& p, hipStream_t st) {
     const dim3 grid((unsigned)((p.nrows + kUpRows - 1) / kUpRows), (unsigned)(p.ntok / kUpTokens + p.nseg));
-    const size_t lds = (size_t)((p.max_rank + 15) / 16) * 64 * kUpTokens;  // hi and lo fragments of every token
+    const size_t lds = (size_t)((p.max_rank + 15) / 16) * 96 * kUpTokens;  // three parts of every token's inner values
     if (p.split == 8) hipLaunchKernelGGL((lora_up_kernel<8, VEC, MANY, FEW>), grid, dim3(256), lds, st, p);
     else if (p.split == 2) hipLaunchKernelGGL((lora_up_kernel<2, VEC, MANY, FEW>), grid, dim3(256), lds, st, p);
     else hipLaunchKernelGGL((lora_up_kernel<1, VEC, MANY, FEW>), grid, dim3(256), lds, st, p);
