@@ -630,9 +630,10 @@ def _empty(shape, dtype, device, stream):
     """A new tensor of the memory of the stream it is used on (the current one, or the one given): memory
     that another stream's pending work has given back would still be written by it."""
     import torch
-    if stream is None:
+    if stream is None or stream == _current()[1](device.index):
         return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device)):
+    # an ExternalStream of handle 0 is some stream of torch's pool, not the default one
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
