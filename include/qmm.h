@@ -358,7 +358,7 @@ int qmm_rmsnorm(int xtype, const void* x, int64_t ldx, int rtype, const void* re
  * once to the output type.
  *   xq   : q8_1 [ncols][k/32][36], 4-byte aligned.   k : a multiple of 32, > 0.
  *   out  : otype (QMM_TYPE_F32 or QMM_TYPE_F16) [ncols][ldo], ldo >= k.
- * Errors: QMM_EINVAL, QMM_EALIGN, QMM_EUNSUPPORTED (2^29 blocks or more). */
+ * Errors: QMM_EINVAL, QMM_EALIGN, QMM_EUNSUPPORTED (more than 2^29 - 32 blocks). */
 int qmm_dequantize_q8_1(const void* xq, int64_t k, int64_t ncols, int otype, void* out, int64_t ldo,
                         void* stream);
 

@@ -275,6 +275,7 @@ __global__ __launch_bounds__(256) void dequantize_q8_1_kernel(const uint8_t* __r
 using namespace qmm;
 
 constexpr int64_t kNormMaxRows = (1 << 22) - 1;  // a workgroup of 1024 threads a row, below 2^32 threads
+constexpr int64_t kValuesMaxBlocks = ((int64_t)1 << 29) - 32;  // 8 threads a block, whole workgroups of 256, below 2^32 threads
 
 extern "C" int qmm_rmsnorm(int xtype, const void* x, int64_t ldx, int rtype, const void* res, int64_t ldr, void* res_out,
                            int64_t ldro, const float* w, float eps, int64_t ntok, int64_t hidden, int ytype, void* y,
@@ -324,7 +325,7 @@ extern "C" int qmm_rmsnorm(int xtype, const void* x, int64_t ldx, int rtype, con
 
 extern "C" int qmm_dequantize_q8_1(const void* xq, int64_t k, int64_t ncols, int otype, void* out, int64_t ldo, void* stream) {
     if (k < 32 || k % 32 || ncols < 0 || ldo < k || (otype != QMM_TYPE_F32 && otype != QMM_TYPE_F16)) return QMM_EINVAL;
-    if (k > (int64_t)1 << 30 || ncols > (int64_t)1 << 31 || ncols * (k / 32) >= (int64_t)1 << 29) return QMM_EUNSUPPORTED;
+    if (k > (int64_t)1 << 30 || ncols > (int64_t)1 << 31 || ncols * (k / 32) > kValuesMaxBlocks) return QMM_EUNSUPPORTED;
     if (ncols == 0) return QMM_OK;
     if (!xq || !out) return QMM_EINVAL;
     if (!aligned(xq, 4) || !aligned(out, type_bytes(otype))) return QMM_EALIGN;
