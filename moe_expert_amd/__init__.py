@@ -593,6 +593,13 @@ def _flat(t, name, dtype, count, device):
     return t
 
 
+def _vector(t, name, dtype, count, device):
+    """The same for a vector of weights, of exactly `count` elements: a longer one is another model's."""
+    if t.dtype != dtype or t.numel() != count or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {count} elements on {device}")
+    return t
+
+
 _CURRENT = None
 
 
@@ -661,7 +668,7 @@ def qmm_rmsnorm(x, w, eps, res=None, res_out=None, y=None, yq=None, stream=None)
     if y is None and yq is None and res_out is None:
         raise ValueError("no output asked for")
     xt, ldx = _rows(x, "x", shape, dev)
-    _flat(w, "w", torch.float32, hidden, dev)
+    _vector(w, "w", torch.float32, hidden, dev)
     rt = ldr = ldro = yt = ldy = 0
     if res is not None:
         rt, ldr = _rows(res, "res", shape, dev)
@@ -724,7 +731,7 @@ def qmm_moe_route(logits, topk, score=QMM_SCORE_SOFTMAX, bias=None, ngroups=1, t
     if topk < 1 or max(topk, ngroups, topk_groups, group_top) > 0x7FFFFFFF:
         raise ValueError("topk must be positive, and every count an int32")
     if bias is not None:
-        _flat(bias, "bias", torch.float32, nexperts, dev)
+        _vector(bias, "bias", torch.float32, nexperts, dev)
     if ids is not None:
         _flat(ids, "ids", torch.int32, ntok * topk, dev)
     if weights is not None:
@@ -800,8 +807,8 @@ def qmm_lora(x, a, b, ranks, scales, seg_off, seg_adapter, y, base=None, ws=None
     xt, ldx = _rows(x, "x", shape, dev, bf16=False)
     _flat(a, "a", torch.float16, 0, dev)
     _flat(b, "b", torch.float16, 0, dev)
-    _flat(ranks, "ranks", torch.int32, na, dev)
-    _flat(scales, "scales", torch.float32, na, dev)
+    _vector(ranks, "ranks", torch.int32, na, dev)
+    _vector(scales, "scales", torch.float32, na, dev)
     nseg = seg_adapter.numel()
     _flat(seg_adapter, "seg_adapter", torch.int32, nseg, dev)
     _flat(seg_off, "seg_off", torch.int32, nseg + 1, dev)
