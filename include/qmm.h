@@ -366,7 +366,8 @@ int qmm_dequantize_q8_1(const void* xq, int64_t k, int64_t ncols, int otype, voi
  *   s[e] = softmax(l)[e]  or  1 / (1 + exp(-l[e]))                        (score)
  *   c[e] = s[e] + bias[e]   (bias NULL: s[e]; a softmax without bias whose groups, if any, go by
  *          their best member is compared by l[e] itself, the same order without its rounding)
- *   an expert whose l[e] or c[e] is -inf or NaN is never chosen (nor counted in the softmax);
+ *   an expert whose l[e] is -inf or NaN is never chosen nor counted in the softmax; one whose c[e]
+ *     is, by its bias, is never chosen but its s[e] counts in the softmax;
  *   ngroups > 1: the experts form ngroups equal runs; a run's score is the sum of its group_top
  *     (1 or 2) largest c (-inf where it has fewer), the topk_groups best runs stay, the experts of
  *     the others are not chosen;

@@ -723,7 +723,8 @@ def qmm_moe_route(logits, topk, score=QMM_SCORE_SOFTMAX, bias=None, ngroups=1, t
     Scores are the softmax or the sigmoid of the logits; experts are chosen by score + bias (float32
     [nexperts]) among the topk_groups best of ngroups runs of experts, a run rated by the sum of its
     group_top best; weights are the chosen scores, divided by their sum if renorm, times scale.
-    Experts whose logit is -inf or NaN are never chosen; missing choices are id -1, weight 0."""
+    Experts whose logit or score + bias is -inf or NaN are never chosen (those that only the bias takes
+    out count in the softmax); missing choices are id -1, weight 0."""
     import torch
     shape = ntok, nexperts = _matrix(logits, "logits", "[ntok, nexperts]")
     dev = logits.device
