@@ -108,6 +108,10 @@ def main():
     off, ad = segments([1] * 8, [0, 1, 2, 3, -1, 0, 1, 2])
     step = lambda: block.decode(x, res.clone(), off, ad)  # noqa: E731
     print(f"decode, 8 requests: {timed(step):.1f} us eager", flush=True)
+    _, mid = step()
+    h = M.qmm_dequantize_q8_1(mid["hq"], block.hidden)  # what the experts read
+    y, _, _ = M.qmm_rmsnorm(mid["proj"], block.norm, EPS, res=res, y=torch.float32)
+    print(f"decode, q8_1 activations against the binary32 norm: {float((h - y).norm() / y.norm()):.2%}", flush=True)
     graph = torch.cuda.CUDAGraph()
     kept = res.clone()
     with torch.cuda.graph(graph):
