@@ -7,9 +7,11 @@
 // values for itself, measured slower: 9.4 against 8.0 us for 8 requests of one token at rank 16,
 // k 2560, 8192 rows; 40 against 13 us at rank 64, k 6144, 2560 rows.)
 //
-// Bound: the base and y.  8192 tokens x (2560 -> 8192), rank 16: 129 us for the 582 MB that cannot be
-// avoided (4.5 TB/s, a large copy reaches 5.0), of which the inner values 17 us; short calls are
-// bound by the chain of dependent loads segment -> adapter -> A, x -> inner values -> y.
+// Bound: the base and y.  8192 tokens x (2560 -> 8192), rank 16: 130 us for the 580 MB that cannot be
+// avoided (4.5 TB/s, a large copy reaches 5.0), of which the inner values 18 us; short calls are
+// bound by the chain of dependent loads segment -> adapter -> A, x -> inner values -> y.  Many requests
+// of one token are far from their bytes (64: 14.7 us for 9 MB; 512, 2560 -> 2560: 42 us; 4096,
+// 1024 -> 1024: 209 us): a tile of 32 tokens each, found by a scan of the segments in each workgroup.
 #include "qmm_values.h"
 
 namespace qmm {
@@ -39,7 +41,7 @@ struct LoraTile {
 // Tile `tile` of the segments' tiles of T tokens each (the last of a segment holds what is left):
 // its tokens [t0, t0 + nt) and their adapter, -1 for none.  A scan of the segments' tile counts, 64 a
 // step; MANY, for more than 64 segments: four steps are skipped by their sum where the tile lies
-// beyond them (4096 segments 223 us against 407).  Every wave does its own, all lanes call it.
+// beyond them (4096 segments 223 us against 407 when it was tried).  Every wave does its own, all lanes call it.
 template <bool MANY>
 __device__ __forceinline__ LoraTile find_tile(const LoraArgs& a, int T, int tile) {
     const int l = threadIdx.x & 63;
@@ -177,7 +179,7 @@ __device__ __forceinline__ void down_tile_ranks(const LoraArgs& a, const LoraTil
 
 // Workgroup (tile, split): the waves' sums joined in wave order into the split's inner values.  16
 // tokens a tile (32 measured the same on prompts and leave half as many workgroups in short calls);
-// 8192 tokens, k 2560, rank 16: 17 us for the 42 MB of x; 517 tokens, ranks to 64: 9 us.
+// 8192 tokens, k 2560, rank 16: 17.6 us for the 42 MB of x; 517 tokens, ranks to 64: 9.3 us.
 template <int XT, int NR, int W, bool MANY>
 __global__ __launch_bounds__(64 * W) void lora_down_kernel(LoraArgs a) {
     constexpr int T = 16, R = 16 * NR;
@@ -407,7 +409,8 @@ struct UpBlock {
     }
 };
 
-// A workgroup's part of a tile without an adapter: y = base.
+// A workgroup's part of a tile without an adapter: y = base, one value a thread and token.  8192 x 8192
+// without adapters: 202 us (537 MB, 2.7 TB/s).
 __device__ __forceinline__ void copy_base(const LoraArgs& a, const LoraTile& tile, const float* base, float* y, int rows) {
     if (a.base == a.y) return;
     for (int t = 0; t < tile.nt; ++t)
@@ -416,8 +419,8 @@ __device__ __forceinline__ void copy_base(const LoraArgs& a, const LoraTile& til
 
 // Workgroup (row block, tile): 32 tokens by 256 rows of y, one UpBlock a wave, on the SPLIT parts of
 // the inner values that lora_down_kernel left.  4 waves per SIMD (at 3 the prompt took 149 us against
-// 138, at 5 the registers spill).  8192 x 8192, rank 16: 106 us for 537 MB; 517 x 12288, ranks to 64:
-// 13.6 us for 63 MB.
+// 138, at 5 the registers spill).  8192 x 8192, rank 16: 108 us for 537 MB; 517 x 12288, ranks to 64:
+// 14.2 us for 63 MB.
 template <int SPLIT, bool VEC, bool MANY, bool FEW>
 __global__ __launch_bounds__(256, SPLIT > 2 ? 2 : 4) void lora_up_kernel(LoraArgs a) {
     constexpr int T = kUpTokens, ROWS = kUpRows;
@@ -458,9 +461,11 @@ constexpr int64_t kLoraMaxTokens = 1 << 20;
 constexpr int kLoraMaxSegments = 1 << 14;
 
 // How many workgroups share the columns of one token tile, so that few tiles still fill the GPU; the
-// outer product reads that many parts.  517 ragged tokens, ranks to 64: 27.5 us with 2, 29.8 with 4,
-// 35 with 1 (before the base was read through the caches: 23.2 now); 8 requests of one token, rank 16:
-// 7.0 us with 8.
+// outer product reads that many parts.  With 1 / 2 / 8: 8 requests of one token at rank 16 10.9 / 8.6 /
+// 7.3 us; one request (2560 -> 8192, rank 16) of 64 tokens 11.2 / 9.3 / 8.3, 256 tokens 13.2 / 11.2 / 10.3,
+// 1024 tokens 20.2 / 18.2 / 19.7, 1100 tokens 21.0 / 19.2 / 20.3, 2048 tokens 29.6 / 28.9 / 31.9; 517
+// ragged tokens, ranks to 64, 30.4 / 25.2 / 25.0.  The steps at 64 and 1024 tokens lie where the work per
+// token still differs by 1 us (65 tokens 9.4 against 8.4) and 2 us (1100 tokens 21.1 against 19.2).
 static int lora_split(int64_t ntok) { return ntok <= 64 ? 8 : ntok <= 1024 ? 2 : 1; }
 
 extern "C" size_t qmm_lora_workspace(int64_t ntok, int max_rank) {

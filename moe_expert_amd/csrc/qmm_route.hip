@@ -77,9 +77,12 @@ __device__ __forceinline__ float run_score(const RouteArgs& a, float best, float
 // 128 experts 5.2 us against 6.1 with 4 experts a lane (8 tokens: 4.4 against 3.9), of 256 7.3
 // against 9.4 with 4 and 7.6 with 16.  VEC: rows in
 // aligned pieces of 8 (V = 8 or 16).
-// Bound: VALU, about 35 instructions a choice; few tokens: that chain's latency.  8192 tokens, top-8
-// of 128: 5.2 us (4.7 MB; one token a wave with exchanges through lanes 17.4); 8 tokens 4.3 us; 4099
-// tokens of 256 experts in 8 runs 9.3 us; 8192 tokens, top-10 of 512 14 us.
+// Bound: VALU and what a choice waits for: with 8 experts a lane 14 vector instructions find the best, 34
+// locate and remove it, and some 25 scalar ones and no-ops stand between them; few tokens: that chain's
+// latency.  8192 tokens, top-8 of 128: 5.2 us (4.7 MB; one token a wave with exchanges through lanes
+// 17.4); 8 tokens 4.3 us; 8192 tokens, top-10 of 512 14 us; 4099 tokens of 256 experts in 8 runs with
+// sigmoid and bias 9.3 us, in which each bias value is a load behind its own branch, waited for before
+// the next, and scores are divided by a sum of 1.
 template <int L, int V, bool VEC>
 __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
     constexpr int T = 256 / L;
