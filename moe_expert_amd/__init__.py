@@ -13,7 +13,9 @@ Names follow the C ABI: ``qmm_quantize_q8_1``, ``qmm_dequant_f16``, ``qgemv_dens
 ``qgemm_prefill_experts`` (and the measurement hooks ``qmm_debug_stream_read``,
 ``qmm_debug_mfma_loop``); between the products ``qmm_rmsnorm``, ``qmm_dequantize_q8_1``,
 ``qmm_moe_route``, ``qmm_moe_dispatch`` and ``qmm_lora``, which also take row-strided views of
-float32, float16 or bfloat16 tensors where their docstrings say so.
+float32, float16 or bfloat16 tensors where their docstrings say so.  What these make anew on a given
+stream is that stream's memory: as with torch's own tensors, ``record_stream`` it where work of another
+stream may outlive it.
 """
 from __future__ import annotations
 
