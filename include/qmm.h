@@ -57,7 +57,7 @@ extern "C" {
 #define QMM_EHIP (-4)         /* the HIP runtime reported an error at launch */
 #define QMM_ESPACE (-5)       /* workspace smaller than the *_workspace() query returned */
 
-/* value types of the tensors of qmm_rmsnorm, qmm_dequantize_q8_1, qmm_moe_route and qmm_lora */
+/* value types of the tensors of qmm_rmsnorm, qmm_dequantize_q8_1, qmm_moe_route, qmm_lora and qmm_kv_* */
 #define QMM_TYPE_F32 1
 #define QMM_TYPE_F16 2  /* binary16 */
 #define QMM_TYPE_BF16 3 /* bfloat16 */
@@ -433,6 +433,85 @@ int qmm_lora(int xtype, const void* x, int64_t ldx, int64_t ntok, int64_t k, con
              int max_rank, const int32_t* seg_off, const int32_t* seg_adapter, int nseg,
              const float* base, int64_t ldbase, float* y, int64_t ldy, int64_t nrows, void* ws,
              size_t ws_bytes, void* stream);
+
+/* A paged key-value cache (host struct; k and v are device pointers).  Each of k and v is an array
+ * of npages pages, kstride / vstride bytes apart; a page holds, for each of its nheads heads, a chunk of
+ * page_size positions of head_dim values, page_size * qmm_row_bytes(type, head_dim) bytes:
+ *   QMM_F16    : binary16 [page_size][head_dim];
+ *   QMM_Q8_0, QMM_IQ4_NL : two planes, the blocks' factors [page_size][head_dim / 32 * 32 or 16 bytes],
+ *                then their binary16 scales [page_size][head_dim / 32].  With nb = head_dim / 32, value
+ *                16 i + n of block b (i = 0, 1; n = 0 .. 15) is int8 (n*nb + b)*2 + i of its position's
+ *                factors, or the low (i = 0) or high (i = 1) half of byte n*nb + b: what one lane of a
+ *                matrix instruction takes of every block is contiguous.  Values as in the weight formats,
+ *                d * q and d * level.
+ *   ktype, vtype : QMM_F16, QMM_Q8_0 or QMM_IQ4_NL.   k, v : 16-byte aligned; strides multiples of 16.
+ *   page_size : a multiple of 16, at most 4096.   head_dim : 64, 96, 128, 192 or 256.
+ *   nheads : 1 .. 1024.   npages : 1 .. 2^31 - 1.
+ *
+ * Sequence s of nseq has lens[s] positions in the cache, the new tokens of the call among them; position p
+ * is place p % page_size of page pages[s*ldpages + p / page_size].  Its new tokens are seg_off[s] ..
+ * seg_off[s+1]-1 of the call's ntok (NULL: nseq = ntok, token s alone); they are its last positions, token
+ * t the position lens[s] - (seg_off[s+1] - t).  What the host cannot check is bounded on the device: offsets
+ * are clamped to [0, ntok] and have to be non-decreasing, a position below 0, past max_pages or
+ * on a page outside [0, npages) does not exist, and tokens of no sequence are left alone.
+ *   pages : int32 [nseq][ldpages], ldpages >= max_pages; entries past a sequence's pages are not read.
+ *   lens : int32 [nseq].   seg_off : int32 [nseq + 1] or NULL.   (4-byte aligned.)
+ *   ntok at most 2^20, ntok * nheads at most 2^27, nseq at most 2^14, max_pages * page_size below 2^31. */
+typedef struct {
+    int ktype, vtype;
+    void *k, *v;
+    int64_t kstride, vstride; /* bytes from a page to the next */
+    int64_t npages;
+    int page_size, nheads, head_dim;
+} qmm_kv_cache;
+
+/* Writes new tokens' keys and values to their positions, quantized per 32 values x_j of a head's row:
+ *   QMM_Q8_0   : d = max |x| / 127, q_j = x_j / d rounded half away from zero;
+ *   QMM_IQ4_NL : d = x_m / -127, x_m the value of largest magnitude (the first of them); the index of x_j
+ *                the level nearest to x_j / d, ties to the lower one;
+ *   in binary32 with IEEE divisions; d is stored as binary16.  Where d is 0 every value is 0 (scale +0, indices 8).
+ *   QMM_F16    : x_j rounded to nearest even.
+ * A block of a block format that holds an infinity or NaN does not read back as what it held; its
+ * neighbours do.  A token whose position does not exist is not written.  The positions of one call
+ * must be distinct.
+ *   xtype : type of k and v, QMM_TYPE_*.   k, v : [ntok][ldk], [ntok][ldv], rows of nheads * head_dim
+ *   values; one of them may be NULL: that cache is left alone.   cache : host pointer.
+ * Errors: QMM_EINVAL, QMM_EALIGN, QMM_EUNSUPPORTED. */
+int qmm_kv_write(const qmm_kv_cache* cache, const int32_t* pages, int64_t ldpages, int64_t max_pages,
+                 const int32_t* lens, const int32_t* seg_off, int nseq, int xtype, const void* k,
+                 int64_t ldk, const void* v, int64_t ldv, int64_t ntok, void* stream);
+
+/* Reads keys and values back, each value exact and rounded once to the output type: the last
+ * seg_off[s+1] - seg_off[s] positions of each sequence (all of it where that is lens[s]); rows of zeros
+ * where a position does not exist.  Arguments as qmm_kv_write; rows of k and v must not overlap. */
+int qmm_kv_read(const qmm_kv_cache* cache, const int32_t* pages, int64_t ldpages, int64_t max_pages,
+                const int32_t* lens, const int32_t* seg_off, int nseq, int otype, void* k, int64_t ldk,
+                void* v, int64_t ldv, int64_t ntok, void* stream);
+
+/* Workspace bytes qmm_kv_attend needs (host); 0 for sizes it does not take. */
+size_t qmm_kv_attend_workspace(const qmm_kv_cache* cache, int64_t ntok, int nheads, int nseq,
+                               int64_t max_pages);
+
+/* Attention of new tokens over the cache, their own keys and values among it (qmm_kv_write first).  For
+ * token t of sequence s at position p, head h, and the cache's head h / (nheads / cache->nheads):
+ *   z_j = scale * sum_c q[t][h][c] * key_j[c],   j <= p, j > p - window if window > 0, j existing
+ *   out[t][h] = sum_j exp(z_j - max z) * value_j / sum_j exp(z_j - max z),   lse[t][h] = log sum_j exp(z_j)
+ * with binary32 scores, statistics and sums.  No j (a token before position 0, an empty sequence, missing
+ * pages): out 0, lse -inf.  Positions a token does not see have no effect on it, whatever they hold.  A
+ * row of q that is not finite gives NaN in its own outputs.  Meant for up to some tens of tokens a sequence
+ * (any count is right: each 16 or 32 rows of queries read the cache once).
+ *   q    : qtype [ntok][ldq], rows of nheads * head_dim values.   nheads : a multiple of cache->nheads, at
+ *          most 1024.   scale : finite.   window : >= 0.
+ *   out  : otype [ntok][ldo], must not overlap q.   lse : float [ntok][nheads] or NULL.
+ *   cache->vtype holds at most as many bits as cache->ktype (an error of a key enters the exponent).
+ *   ws   : qmm_kv_attend_workspace() bytes, 16-byte aligned; nothing in it is kept between calls, and
+ *          calls that may overlap in time need one each.
+ * Results do not depend on scheduling.
+ * Errors: QMM_EINVAL, QMM_EALIGN, QMM_EUNSUPPORTED, QMM_ESPACE. */
+int qmm_kv_attend(const qmm_kv_cache* cache, const int32_t* pages, int64_t ldpages, int64_t max_pages,
+                  const int32_t* lens, const int32_t* seg_off, int nseq, int qtype, const void* q,
+                  int64_t ldq, int64_t ntok, int nheads, float scale, int64_t window, int otype,
+                  void* out, int64_t ldo, float* lse, void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -12,7 +12,8 @@ Names follow the C ABI: ``qmm_quantize_q8_1``, ``qmm_dequant_f16``, ``qgemv_dens
 ``qgemv_dense_f32``, ``qmm_debug_block_sums``, ``qgemv_grouped_experts``,
 ``qgemm_prefill_experts`` (and the measurement hooks ``qmm_debug_stream_read``,
 ``qmm_debug_mfma_loop``); between the products ``qmm_rmsnorm``, ``qmm_dequantize_q8_1``,
-``qmm_moe_route``, ``qmm_moe_dispatch`` and ``qmm_lora``, which also take row-strided views of
+``qmm_moe_route``, ``qmm_moe_dispatch`` and ``qmm_lora``, and over a paged key-value cache (``KvCache``)
+``qmm_kv_write``, ``qmm_kv_read`` and ``qmm_kv_attend``, which also take row-strided views of
 float32, float16 or bfloat16 tensors where their docstrings say so.  What these make anew on a given
 stream is that stream's memory: as with torch's own tensors, ``record_stream`` it where work of another
 stream may outlive it.
@@ -74,6 +75,11 @@ SIGNATURES = {
     "qmm_lora_workspace": (_SZ, [_I64, _I32]),
     "qmm_lora": (_I32, [_I32, _P, _I64, _I64, _I64, _P, _P, _P, _P, _I32, _I32, _P, _P, _I32, _P, _I64, _P, _I64, _I64,
                         _P, _SZ, _P]),
+    "qmm_kv_write": (_I32, [_P, _P, _I64, _I64, _P, _P, _I32, _I32, _P, _I64, _P, _I64, _I64, _P]),
+    "qmm_kv_read": (_I32, [_P, _P, _I64, _I64, _P, _P, _I32, _I32, _P, _I64, _P, _I64, _I64, _P]),
+    "qmm_kv_attend_workspace": (_SZ, [_P, _I64, _I32, _I32, _I64]),
+    "qmm_kv_attend": (_I32, [_P, _P, _I64, _I64, _P, _P, _I32, _I32, _P, _I64, _I64, _I32, _F32, _I64, _I32, _P, _I64, _P,
+                             _P, _SZ, _P]),
 }
 
 _lib = None
@@ -826,3 +832,201 @@ def qmm_lora(x, a, b, ranks, scales, seg_off, seg_adapter, y, base=None, ws=None
           scales.data_ptr(), na, max_rank, seg_off.data_ptr(), seg_adapter.data_ptr(), nseg, base.data_ptr(), ldb,
           y.data_ptr(), ldy, nrows, ws.data_ptr(), ws.numel())
     return y
+
+
+# ------------------------------------------------------------------ the key-value cache
+
+KV_DIMS = (64, 96, 128, 192, 256)
+
+
+class _KvStruct(C.Structure):
+    """qmm_kv_cache of include/qmm.h."""
+    _fields_ = [("ktype", _I32), ("vtype", _I32), ("k", _P), ("v", _P), ("kstride", _I64), ("vstride", _I64), ("npages", _I64),
+                ("page_size", _I32), ("nheads", _I32), ("head_dim", _I32)]
+
+
+class KvCache:
+    """A paged key-value cache over two caller-owned tensors, checked once: k of format ktype, v of vtype
+    (QMM_F16, QMM_Q8_0 or QMM_IQ4_NL), each [npages, nheads, page_size, row]: float16 with row = head_dim,
+    or uint8 with row = row_bytes(type, head_dim) (a page and head's planes of factors and scales; the
+    layout is in include/qmm.h).  Pages may lie apart (a view into a larger allocation: the first
+    dimension's stride), what is in a page is contiguous.  page_size is a multiple of 16, head_dim 64,
+    96, 128, 192 or 256.  The object keeps the tensors; it must not outlive a change of their storage."""
+
+    __slots__ = ("ktype", "vtype", "k", "v", "device", "npages", "nheads", "page_size", "head_dim", "width", "_struct", "_ref")
+
+    def __init__(self, ktype, vtype, k, v):
+        dims = [self._side(t, kind, name) for t, kind, name in ((k, ktype, "k"), (v, vtype, "v"))]
+        if dims[0] != dims[1] or k.device != v.device:
+            raise ValueError(f"k and v must hold the same pages, heads and head_dim on one device: {dims[0]}, {dims[1]}")
+        self.npages, self.nheads, self.page_size, self.head_dim = dims[0]
+        self.ktype, self.vtype, self.k, self.v, self.device = ktype, vtype, k, v, k.device
+        self.width = self.nheads * self.head_dim
+        self._struct = _KvStruct(ktype, vtype, k.data_ptr(), v.data_ptr(), *(t.stride(0) * t.element_size() if t.shape[0] > 1 else
+                                 t[0].numel() * t.element_size() for t in (k, v)), self.npages, self.page_size, self.nheads, self.head_dim)
+        self._ref = C.addressof(self._struct)
+
+    @staticmethod
+    def _side(t, kind, name):
+        import torch
+        if kind not in (QMM_F16, QMM_Q8_0, QMM_IQ4_NL):
+            raise ValueError(f"{name}: caches are QMM_F16, QMM_Q8_0 or QMM_IQ4_NL")
+        shape = getattr(t, "shape", ())
+        if len(shape) != 4 or min(shape) < 1:
+            raise ValueError(f"{name} must be [npages, nheads, page_size, row]")
+        if not getattr(t, "is_cuda", False):
+            raise ValueError(f"{name} must be a GPU tensor")
+        want = torch.float16 if kind == QMM_F16 else torch.uint8
+        if t.dtype != want:
+            raise ValueError(f"{name} must have dtype {want}, not {t.dtype}")
+        npages, nheads, page_size, row = shape
+        if page_size % 16 or page_size > 4096 or nheads > 1024 or npages > 0x7FFFFFFF:
+            raise ValueError(f"{name}: page_size must be a multiple of 16 up to 4096, nheads at most 1024")
+        dim = row if kind == QMM_F16 else row * 32 // BLOCK_BYTES[kind]
+        if dim not in KV_DIMS or (kind != QMM_F16 and row != dim // 32 * BLOCK_BYTES[kind]):
+            raise ValueError(f"{name}: rows of {row} are not rows of head_dim in {KV_DIMS}")
+        st = t.stride()
+        inner = (page_size * row, row, 1)
+        if any(n > 1 and s != w for n, s, w in zip(shape[1:], st[1:], inner)) or (npages > 1 and st[0] < nheads * page_size * row):
+            raise ValueError(f"{name}: what is in a page must be contiguous, and pages must not overlap")
+        return npages, nheads, page_size, dim
+
+    @classmethod
+    def empty(cls, ktype, vtype, npages, nheads, head_dim, page_size=64, device="cuda"):
+        """A new cache of zeros."""
+        import torch
+        new = [torch.zeros((npages, nheads, page_size, head_dim if kind == QMM_F16 else row_bytes(kind, head_dim)),
+                           dtype=torch.float16 if kind == QMM_F16 else torch.uint8, device=device) for kind in (ktype, vtype)]
+        return cls(ktype, vtype, *new)
+
+
+def _kv_sequences(cache, pages, lens, seg_off, ntok):
+    """The checks of a call's sequences: (nseq, max_pages, ldpages)."""
+    import torch
+    i32, dev = torch.int32, cache.device
+    if len(getattr(pages, "shape", ())) != 2:
+        raise ValueError("pages must be [nseq, max_pages]")
+    nseq, width = pages.shape
+    if pages.dtype != i32 or pages.device != dev:
+        raise ValueError(f"pages must be int32 on {dev}")
+    ld = width
+    if not pages.is_contiguous():
+        ld, step = pages.stride()
+        if nseq <= 1:
+            ld = width
+        if (step != 1 and width > 1) or ld < width:
+            raise ValueError("pages must have contiguous rows that do not overlap")
+    if width < 1:
+        raise ValueError("pages must have a column")
+    _vector(lens, "lens", i32, nseq, dev)
+    if seg_off is not None:
+        _vector(seg_off, "seg_off", i32, nseq + 1, dev)
+    elif nseq != ntok:
+        raise ValueError(f"{ntok} tokens of {nseq} sequences need seg_off")
+    return nseq, width, ld
+
+
+def qmm_kv_write(cache, pages, lens, k=None, v=None, seg_off=None, stream=None):
+    """Writes new tokens' keys and values (either may be None) to a KvCache, quantized per 32 values of a
+    head as the cache's format says.
+
+    k, v: [ntok, nheads * head_dim] float32, float16 or bfloat16 (the same), any row stride.  pages: int32
+    [nseq, max_pages], each sequence's pages in order (entries it does not need may hold anything); lens:
+    int32 [nseq], its length with the new tokens; seg_off: int32 [nseq+1], sequence s has the tokens
+    seg_off[s] .. seg_off[s+1]-1, its last positions (None: token s is sequence s's).  A token whose
+    position is negative, past the table or on a page outside the cache is not written."""
+    x = v if k is None else k
+    if x is None:
+        raise ValueError("k or v is required")
+    ntok = _matrix(x, "k" if k is not None else "v", "[ntok, nheads * head_dim]")[0]
+    dev = cache.device
+    nseq, width, ldp = _kv_sequences(cache, pages, lens, seg_off, ntok)
+    kt = vt = ldk = ldv = 0
+    if k is not None:
+        kt, ldk = _rows(k, "k", (ntok, cache.width), dev)
+    if v is not None:
+        vt, ldv = _rows(v, "v", (ntok, cache.width), dev)
+        if kt and vt != kt:
+            raise ValueError("k and v must have the same dtype")
+    _call("qmm_kv_write", dev, stream, cache._ref, pages.data_ptr(), ldp, width, lens.data_ptr(), _addr(seg_off), nseq, kt or vt,
+          _addr(k), ldk, _addr(v), ldv, ntok)
+
+
+def qmm_kv_read(cache, pages, lens, k=None, v=None, seg_off=None, ntok=None, stream=None):
+    """Reads positions of a KvCache back: the last seg_off[s+1] - seg_off[s] positions of each sequence
+    (None: the last one), in order, into k and v: [ntok, nheads * head_dim] tensors of one of float32,
+    float16 and bfloat16 with any row stride, or a dtype for a new one (ntok rows; by default nseq, one of
+    each sequence); None for what is not wanted.  Positions that do not exist give rows of zeros; rows of
+    no sequence are left alone.  Returns (k, v)."""
+    import torch
+    dev = cache.device
+    for t in (k, v):
+        if t is not None and not isinstance(t, torch.dtype):
+            ntok = _matrix(t, "k and v", "[ntok, nheads * head_dim] or a dtype")[0]
+    if ntok is None:
+        if seg_off is not None:
+            raise ValueError("ntok is required for new tensors of ragged sequences")
+        ntok = _matrix(pages, "pages", "[nseq, max_pages]")[0]
+    if ntok < 0:
+        raise ValueError("ntok must not be negative")
+    nseq, width, ldp = _kv_sequences(cache, pages, lens, seg_off, ntok)
+    shape, code, lds, outs = (ntok, cache.width), 0, [0, 0], [k, v]
+    if k is None and v is None:
+        raise ValueError("k or v is required")
+    for i, (t, name) in enumerate(((k, "k"), (v, "v"))):
+        if t is None:
+            continue
+        if isinstance(t, torch.dtype):
+            if t not in (_TYPE_OF or _types()):
+                raise ValueError(f"{name}: {t} is not a type that this call writes")
+            # rows of no sequence would be whatever the memory held
+            t = outs[i] = _empty(shape, t, dev, stream)
+        ct, lds[i] = _rows(t, name, shape, dev)
+        if code and ct != code:
+            raise ValueError("k and v must have the same dtype")
+        code = ct
+    _call("qmm_kv_read", dev, stream, cache._ref, pages.data_ptr(), ldp, width, lens.data_ptr(), _addr(seg_off), nseq, code,
+          _addr(outs[0]), lds[0], _addr(outs[1]), lds[1], ntok)
+    return tuple(outs)
+
+
+def qmm_kv_attend_workspace(cache, ntok, nheads, nseq, max_pages):
+    """Workspace bytes of qmm_kv_attend for up to these sizes; 0 for sizes it does not take."""
+    return int(lib().qmm_kv_attend_workspace(cache._ref, ntok, nheads, nseq, max_pages))
+
+
+def qmm_kv_attend(q, cache, pages, lens, seg_off=None, scale=None, window=0, out=None, lse=None, ws=None, stream=None):
+    """Attention of new tokens over a KvCache that holds their keys and values already (qmm_kv_write).
+
+    q: [ntok, nheads * head_dim] float32, float16 or bfloat16, any row stride, nheads a multiple of the
+    cache's; head h reads the cache's head h // (nheads / cache.nheads).  pages, lens, seg_off as
+    qmm_kv_write; a token at position p sees the positions j <= p, with window > 0 only j > p - window.
+    scale: of the products, 1 / sqrt(head_dim) by default.  out: a tensor like q, of any of the types, or
+    a dtype for a new one (default q's; rows of no sequence are left alone); must not be q.  lse: float32
+    [ntok, nheads] or True for a new one: the log of each row's sum of exponentials.  A row that sees no position
+    gives zeros and -inf.  ws: qmm_kv_attend_workspace bytes (a call makes its own by default).
+    Returns (out, lse)."""
+    import torch
+    shape = ntok, width = _matrix(q, "q", "[ntok, nheads * head_dim]")
+    dev, dim = cache.device, cache.head_dim
+    nheads = width // dim
+    if width < 1 or width % cache.width:
+        raise ValueError(f"q must have a multiple of {cache.width} columns")
+    nseq, maxp, ldp = _kv_sequences(cache, pages, lens, seg_off, ntok)
+    qt, ldq = _rows(q, "q", shape, dev)
+    if out is None or isinstance(out, torch.dtype):
+        if out is not None and out not in (_TYPE_OF or _types()):
+            raise ValueError(f"out: {out} is not a type that this call writes")
+        out = _empty(shape, out or q.dtype, dev, stream)
+    ot, ldo = _rows(out, "out", shape, dev)
+    if lse is True:
+        lse = _empty((ntok, nheads), torch.float32, dev, stream)
+    elif lse is not None:
+        _flat(lse, "lse", torch.float32, ntok * nheads, dev)
+    if not 0 <= window <= 0x7FFFFFFFFFFFFFFF:
+        raise ValueError("window must not be negative")
+    ws = _scratch(ws, qmm_kv_attend_workspace(cache, ntok, nheads, nseq, maxp), dev, stream)
+    _call("qmm_kv_attend", dev, stream, cache._ref, pages.data_ptr(), ldp, maxp, lens.data_ptr(), _addr(seg_off), nseq, qt,
+          q.data_ptr(), ldq, ntok, nheads, dim ** -0.5 if scale is None else scale, window, ot, out.data_ptr(), ldo, _addr(lse),
+          ws.data_ptr(), ws.numel())
+    return out, lse

@@ -11,7 +11,8 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libqmm.so")
 OBJ = os.path.join(HERE, "_build")
 SOURCES = ["qmm_api.hip", "qmm_quant.hip", "qmm_gemv.hip", "qmm_grouped.hip", "qmm_prefill.hip", "qmm_probe.hip",
-           "qmm_combine.hip", "qmm_norm.hip", "qmm_route.hip", "qmm_lora.hip"]
+           "qmm_combine.hip", "qmm_norm.hip", "qmm_route.hip", "qmm_lora.hip", "qmm_kv.hip",
+           "qmm_attend.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

@@ -1,7 +1,7 @@
 // qmm_api.hip -- format sizes, version and status strings of libqmm (host only).
 #include "qmm_host.h"
 
-extern "C" int qmm_version(void) { return 101; }
+extern "C" int qmm_version(void) { return 102; }
 
 extern "C" const char* qmm_status_str(int status) {
     switch (status) {
