@@ -862,8 +862,9 @@ class KvCache:
         self.npages, self.nheads, self.page_size, self.head_dim = dims[0]
         self.ktype, self.vtype, self.k, self.v, self.device = ktype, vtype, k, v, k.device
         self.width = self.nheads * self.head_dim
-        self._struct = _KvStruct(ktype, vtype, k.data_ptr(), v.data_ptr(), *(t.stride(0) * t.element_size() if t.shape[0] > 1 else
-                                 t[0].numel() * t.element_size() for t in (k, v)), self.npages, self.page_size, self.nheads, self.head_dim)
+        # (the stride of a single page says nothing)
+        strides = [(t.stride()[0] if self.npages > 1 else t.numel()) * t.element_size() for t in (k, v)]
+        self._struct = _KvStruct(ktype, vtype, k.data_ptr(), v.data_ptr(), *strides, self.npages, self.page_size, self.nheads, self.head_dim)
         self._ref = C.addressof(self._struct)
 
     @staticmethod
