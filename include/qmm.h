@@ -456,7 +456,7 @@ int qmm_lora(int xtype, const void* x, int64_t ldx, int64_t ntok, int64_t k, con
  * on a page outside [0, npages) does not exist, and tokens of no sequence are left alone.
  *   pages : int32 [nseq][ldpages], ldpages >= max_pages; entries past a sequence's pages are not read.
  *   lens : int32 [nseq].   seg_off : int32 [nseq + 1] or NULL.   (4-byte aligned.)
- *   ntok at most 2^20, ntok * nheads at most 2^27, nseq at most 2^14, max_pages * page_size below 2^31. */
+ *   ntok at most 2^20, ntok * nheads at most 2^27, nseq at most 2^14, max_pages * page_size at most 2^30. */
 typedef struct {
     int ktype, vtype;
     void *k, *v;

@@ -12,7 +12,7 @@ LIB = os.path.join(HERE, "libqmm.so")
 OBJ = os.path.join(HERE, "_build")
 SOURCES = ["qmm_api.hip", "qmm_quant.hip", "qmm_gemv.hip", "qmm_grouped.hip", "qmm_prefill.hip", "qmm_probe.hip",
            "qmm_combine.hip", "qmm_norm.hip", "qmm_route.hip", "qmm_lora.hip", "qmm_kv.hip",
-           "qmm_attend.hip"]
+           "qmm_attend.hip", "qmm_attend_f16.hip", "qmm_attend_q8.hip", "qmm_attend_iq4.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

@@ -1,130 +1,217 @@
-// qmm_attend.hip -- attention of new tokens over the paged key-value cache, for gfx950.
-//
-// For a row (token, head) at position p: z_j = scale q . k_j over the positions j it sees, out = sum_j
-// exp(z_j - m) v_j / sum_j exp(z_j - m) with the running maximum m and sum of one pass over the cache.
-#include "qmm_kv.h"
+// qmm_attend.hip -- attention of new tokens over the paged key-value cache: the split of many sequences, the
+// join of a split one and the entry point, for gfx950.  The pass itself is in qmm_attend.h.
+#include "qmm_attend.h"
 
 namespace qmm {
 
-struct AttendArgs {
-    const void* q;
-    void* out;
-    float* lse;
-    int64_t ldq, ldo;
-    KvSide k, v;
-    KvPlace p;
-    int nheads, qtype, otype;
-    float scale;
-    int64_t window;
-};
-
-__device__ __forceinline__ float kv_value(const char* chunk, int type, int place, int dim, int page_size, int c) {
-    if (type == kKvF16) return h2f(((const uint16_t*)chunk)[place * dim + c]);
-    const int nb = dim / 32, b = c / 32, i = c / 16 & 1, n = c & 15;
-    const float d = h2f(((const uint16_t*)(chunk + page_size * kv_factor_bytes(type, dim)))[place * nb + b]);
-    if (type == kKvQ8) return d * (float)((const int8_t*)chunk)[((place * 16 + n) * nb + b) * 2 + i];
-    return d * iq4nl_value(((const uint8_t*)chunk)[(place * 16 + n) * nb + b] >> (4 * i) & 15);
+// The split of more sequences than a wave's registers hold: items and slots before each sequence.
+__global__ __launch_bounds__(1024) void attend_plan_kernel(AttendArgs a, int rows, int32_t* plan) {
+    __shared__ int64_t work[16];
+    __shared__ int items[16], slots[16];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, nseq = a.p.nseq;
+    int64_t sum = 0;
+    for (int s = threadIdx.x; s - lane < nseq; s += 1024) {
+        int64_t mine = 0;
+        if (s < nseq) {
+            const SeqWork w = seq_work(a, s, rows);
+            mine = (int64_t)w.steps * w.tiles;
+        }
+        sum += ((int64_t)wave_total((int)(mine >> 24)) << 24) + wave_total((int)(mine & 0xFFFFFF));
+    }
+    if (lane == 0) work[wave] = sum;
+    __syncthreads();
+    sum = 0;
+    for (int i = 0; i < 16; ++i) sum += work[i];
+    const int c = part_steps(a, sum);
+    int before = 0, sbefore = 0;
+    for (int s0 = 0; s0 < nseq; s0 += 1024) {
+        const int s = s0 + threadIdx.x;
+        int mine = 0, slot = 0;
+        if (s < nseq) {
+            const SeqWork w = seq_work(a, s, rows);
+            const int parts = parts_of(w, c);
+            mine = parts * w.tiles;
+            slot = parts > 1 ? mine : 0;
+        }
+        const int upto = wave_scan(mine), sl = wave_scan(slot);
+        __syncthreads();
+        if (lane == 63) {
+            items[wave] = upto;
+            slots[wave] = sl;
+        }
+        __syncthreads();
+        int off = before, soff = sbefore;
+        for (int i = 0; i < 16; ++i) {
+            off += i < wave ? items[i] : 0;
+            soff += i < wave ? slots[i] : 0;
+            before += items[i];
+            sbefore += slots[i];
+        }
+        if (s < nseq) {
+            plan[1 + s] = off + upto - mine;
+            plan[2 + nseq + s] = soff + sl - slot;
+        }
+    }
+    if (threadIdx.x == 0) {
+        plan[0] = c;
+        plan[1 + nseq] = before;
+        plan[2 + 2 * nseq] = sbefore;
+    }
 }
 
-// One wave per row: 64 positions at a time, a lane a score, then a lane every 64th value of the output.
-__global__ __launch_bounds__(64) void attend_kernel(AttendArgs a) {
-    __shared__ float q[256], w[64];
-    __shared__ int at[64];
-    const int t = (int)(blockIdx.x / (uint32_t)a.nheads), h = (int)(blockIdx.x - (uint32_t)t * a.nheads), lane = threadIdx.x;
-    const int s = kv_sequence16(a.p, t);
-    if (s < 0) return;
-    const int dim = a.p.dim, head = h / (a.nheads / a.p.nheads), ps = a.p.page_size;
-    int first, end;
-    kv_segment(a.p, s, first, end);
-    const int64_t pos = (int64_t)a.p.lens[s] - (end - t);
-    for (int c = lane; c < dim; c += 64) q[c] = load_value(a.q, t * a.ldq + (int64_t)h * dim + c, a.qtype) * a.scale;
-    __syncthreads();
-    const int64_t hi = min(pos + 1, (int64_t)a.p.max_pages * ps);
-    float m = -INFINITY, l = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int64_t j0 = a.window > 0 ? max((int64_t)0, pos - a.window + 1) : 0; j0 < hi; j0 += 64) {
-        const int64_t j = j0 + lane;
-        const int pg = j < hi ? kv_page(a.p, s, j) : -1, place = (int)((uint32_t)j % (uint32_t)ps);
-        float z = -INFINITY;
-        if (pg >= 0) {
-            const char* chunk = kv_chunk(a.k, a.p, pg, head);
-            z = 0.0f;
-            for (int c = 0; c < dim; ++c) z += q[c] * kv_value(chunk, a.k.type, place, dim, ps, c);
-        }
-        float top = z;
-        for (int i = 1; i < 64; i <<= 1) top = fmaxf(top, __shfl_xor(top, i, 64));
-        const float now = fmaxf(m, top), base = now == -INFINITY ? 0.0f : now;
-        const float e = pg >= 0 ? expf(z - base) : 0.0f, shrink = expf(m - base);
-        float total = e;
-        for (int i = 1; i < 64; i <<= 1) total += __shfl_xor(total, i, 64);
-        l = l * shrink + total;
-        m = now;
-        w[lane] = e;
-        at[lane] = pg;
-        __syncthreads();
-        for (int i = 0; i < 4; ++i) {
-            const int c = lane + 64 * i;
-            o[i] *= shrink;
-            if (c >= dim) continue;
-            for (int x = 0; x < 64; ++x)
-                if (at[x] >= 0)
-                    o[i] += w[x] * kv_value(kv_chunk(a.v, a.p, at[x], head), a.v.type, (int)((uint32_t)(j0 + x) % (uint32_t)ps), dim, ps, c);
+// The parts of a tile joined, in the order of the parts: 32 dims of a row are a unit, the tile's workgroups share
+// the units.  Eight lanes hold a unit, 32 groups of them every 32nd part.
+template <int NB>
+__global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, int tile_rows) {
+    __shared__ float sm[32], sl[32], so[32][36];
+    const int head = (int)(blockIdx.x % (uint32_t)a.p.nheads);
+    Item it;
+    if (!find_item(a, (int)(blockIdx.x / (uint32_t)a.p.nheads), tile_rows, it) || it.parts == 1) return;
+    if (it.slot < 0 || it.slot + it.parts > a.slots) return;
+    const int row0 = it.tile * tile_rows, rows = min(tile_rows, it.w.n * a.group - row0);
+    const int run = threadIdx.x / 8, e = threadIdx.x & 7;
+    const int64_t size = part_floats(tile_rows, 32 * NB);
+    const float* part = a.parts + ((int64_t)it.slot * a.p.nheads + head) * size;
+    for (int u = it.part; u < rows * NB; u += it.parts) {
+        const int r = u / NB, d = 32 * (u - r * NB) + 4 * e;
+        float top = -INFINITY, sum = 0.0f;
+        float4_t f = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int i = run; i < it.parts; i += 32) {
+            const float* p = part + (int64_t)i * a.p.nheads * size;
+            const float m = p[r], l = p[tile_rows + r];
+            const float4_t o = *(const float4_t*)(p + 2 * tile_rows + r * (32 * NB) + d);
+            const float now = __builtin_fmaxf(top, m), old = beside(top, now), fresh = beside(m, now);
+            top = now;
+            sum = sum * old + l * fresh;
+            f = f * old + o * fresh;
         }
         __syncthreads();
+        if (e == 0) {
+            sm[run] = top;
+            sl[run] = sum;
+        }
+        *(float4_t*)&so[run][4 * e] = f;
+        __syncthreads();
+        if (threadIdx.x < 32) {
+            float most = -INFINITY, total = 0.0f, v = 0.0f;
+            for (int i = 0; i < 32; ++i) most = __builtin_fmaxf(most, sm[i]);
+            for (int i = 0; i < 32; ++i) {
+                const float x = beside(sm[i], most);
+                total += x * sl[i];
+                v += x * so[i][threadIdx.x];
+            }
+            const int tok = (row0 + r) / a.group, h = head * a.group + row0 + r - tok * a.group, dim = 32 * (u - r * NB) + (int)threadIdx.x;
+            store_value(a.out, (it.w.first + tok) * a.ldo + (int64_t)h * (32 * NB) + dim, a.otype, total != 0.0f ? v * (1.0f / total) : 0.0f);
+            if (dim == 0 && a.lse)
+                a.lse[(int64_t)(it.w.first + tok) * a.nheads + h] = total != 0.0f ? most * 0.693147180559945f + __logf(total) : -INFINITY;
+        }
     }
-    for (int i = 0; i < 4; ++i) {
-        const int c = lane + 64 * i;
-        if (c < dim) store_value(a.out, t * a.ldo + (int64_t)h * dim + c, a.otype, l != 0.0f ? o[i] / l : 0.0f);
-    }
-    if (a.lse && lane == 0) a.lse[(int64_t)t * a.nheads + h] = l != 0.0f ? m + logf(l) : -INFINITY;
 }
 
 }  // namespace qmm
+
+#include <algorithm>
 
 #include "qmm_kv_host.h"
 
 using namespace qmm;
 
-static int attend_place(KvPlace& p, const qmm_kv_cache* c, const int32_t* pages, int64_t ldpages, int64_t max_pages,
-                        const int32_t* lens, const int32_t* seg_off, int nseq, int64_t ntok, int nheads) {
-    const int rc = kv_place(p, c, pages, ldpages, max_pages, lens, seg_off, nseq, ntok);
+namespace {
+
+constexpr int64_t kAtTarget = 1024;  // workgroups to split the caches over
+constexpr int kAtLeast = 8;          // steps of the shortest part
+
+struct AttendShape {
+    KvPlace p;
+    int rt;          // 16-row tiles a workgroup
+    int target, least;
+    int64_t items;   // workgroups a head of keys, at most
+    int64_t slots;   // parts of tiles that have several, at most
+    size_t bytes;    // of the workspace: parts, then the plan
+    size_t plan;     // its offset
+};
+
+int attend_shape(AttendShape& s, const qmm_kv_cache* c, const int32_t* pages, int64_t ldpages, int64_t max_pages,
+                 const int32_t* lens, const int32_t* seg_off, int nseq, int64_t ntok, int nheads) {
+    const int rc = kv_place(s.p, c, pages, ldpages, max_pages, lens, seg_off, nseq, ntok);
     if (rc != QMM_OK) return rc;
     if (nheads < 1 || nheads % c->nheads) return QMM_EINVAL;
     if (nheads > 1024 || ntok * nheads > kKvMaxRows || kv_row_bytes(c->vtype, 64) > kv_row_bytes(c->ktype, 64)) return QMM_EUNSUPPORTED;
+    const int64_t group = nheads / c->nheads;
+    const bool wide = c->head_dim <= 128;  // two tiles of wider heads do not fit the registers
+    s.rt = wide && nseq && group * ((ntok + nseq - 1) / nseq) > 16 ? 2 : 1;
+    const int64_t rows = 16 * s.rt, tiles = std::min(nseq + ntok * group / rows, ntok * ((group + rows - 1) / rows));
+    s.target = (int)((kAtTarget + c->nheads - 1) / c->nheads);
+    s.least = kAtLeast;
+    const int64_t steps = (max_pages * c->page_size + kAtStep - 1) / kAtStep + 1, most = (steps + s.least - 1) / s.least;
+    s.items = std::min(s.target + tiles, tiles * most);
+    s.slots = most > 1 ? std::min((int64_t)2 * s.target, tiles * most) : 0;
+    if (s.items * c->nheads >= 1 << 24) return QMM_EUNSUPPORTED;  // below 2^32 threads
+    // (sized for 32 rows where a call of other proportions would take them)
+    s.plan = (size_t)(s.slots * c->nheads * part_floats(wide ? 32 : 16, c->head_dim) * 4 + 15) & ~(size_t)15;
+    s.bytes = s.plan + (nseq > kAtInline ? (size_t)(2 * nseq + 3) * 4 : 0);
+    s.bytes = s.bytes < 16 ? 16 : s.bytes;
     return QMM_OK;
 }
 
+}  // namespace
+
 extern "C" size_t qmm_kv_attend_workspace(const qmm_kv_cache* c, int64_t ntok, int nheads, int nseq, int64_t max_pages) {
-    KvPlace p;
+    AttendShape s;
     static const int32_t some = 0;
-    return attend_place(p, c, &some, max_pages, max_pages, &some, &some, nseq, ntok, nheads) == QMM_OK ? 16 : 0;
+    return attend_shape(s, c, &some, max_pages, max_pages, &some, &some, nseq, ntok, nheads) == QMM_OK ? s.bytes : 0;
 }
 
 extern "C" int qmm_kv_attend(const qmm_kv_cache* c, const int32_t* pages, int64_t ldpages, int64_t max_pages, const int32_t* lens,
                              const int32_t* seg_off, int nseq, int qtype, const void* q, int64_t ldq, int64_t ntok, int nheads,
                              float scale, int64_t window, int otype, void* out, int64_t ldo, float* lse, void* ws, size_t ws_bytes,
                              void* stream) {
-    AttendArgs a;
     if (!valid_type(qtype) || !valid_type(otype) || window < 0 || !(scale >= -3.4e38f) || !(scale <= 3.4e38f)) return QMM_EINVAL;
-    const int rc = attend_place(a.p, c, pages, ldpages, max_pages, lens, seg_off, nseq, ntok, nheads);
+    AttendShape s;
+    const int rc = attend_shape(s, c, pages, ldpages, max_pages, lens, seg_off, nseq, ntok, nheads);
     if (rc != QMM_OK) return rc;
     const int64_t width = (int64_t)nheads * c->head_dim;
     if (ldq < width || ldo < width) return QMM_EINVAL;
     if (ntok == 0 || nseq == 0) return QMM_OK;
     if (!q || !out || !ws) return QMM_EINVAL;
     if (!aligned(q, type_bytes(qtype)) || !aligned(out, type_bytes(otype)) || !aligned(lse, 4) || !aligned(ws, 16)) return QMM_EALIGN;
-    if (ws_bytes < qmm_kv_attend_workspace(c, ntok, nheads, nseq, max_pages)) return QMM_ESPACE;
+    if (ws_bytes < s.bytes) return QMM_ESPACE;
+    const auto fours = [](const void* p, int64_t ld, int type) { return aligned(p, 4 * type_bytes(type)) && ld % 4 == 0; };
+    AttendArgs a;
     a.q = q;
     a.out = out;
     a.lse = lse;
+    a.parts = (float*)ws;
+    a.plan = nseq > kAtInline ? (const int32_t*)((char*)ws + s.plan) : nullptr;
     a.ldq = ldq;
     a.ldo = ldo;
     a.k = KvSide{(char*)c->k, c->kstride, c->ktype};
     a.v = KvSide{(char*)c->v, c->vstride, c->vtype};
+    a.p = s.p;
     a.nheads = nheads;
+    a.group = nheads / c->nheads;
     a.qtype = qtype;
     a.otype = otype;
-    a.scale = scale;
-    a.window = window;
-    hipLaunchKernelGGL(attend_kernel, dim3((unsigned)(ntok * nheads)), dim3(64), 0, as_stream(stream), a);
+    a.scale = (float)((double)scale * 1.4426950408889634);
+    a.window = (int)std::min(window, (int64_t)0x7FFFFFFF);  // more than any position
+    a.target = s.target;
+    a.least = s.least;
+    a.slots = (int)s.slots;
+    a.vec = fours(q, ldq, qtype) && fours(out, ldo, otype);
+    const hipStream_t st = as_stream(stream);
+    if (a.plan) hipLaunchKernelGGL(attend_plan_kernel, dim3(1), dim3(1024), 0, st, a, 16 * s.rt, const_cast<int32_t*>(a.plan));
+    const unsigned grid = (unsigned)(s.items * c->nheads);
+    if (c->ktype == QMM_F16) attend_f16(a, grid, s.rt, st);
+    else if (c->ktype == QMM_Q8_0) attend_q8(a, grid, s.rt, st);
+    else attend_iq4(a, grid, s.rt, st);
+    if (s.slots) {
+        switch (c->head_dim / 32) {
+            case 2: hipLaunchKernelGGL(attend_join_kernel<2>, dim3(grid), dim3(256), 0, st, a, 16 * s.rt); break;
+            case 3: hipLaunchKernelGGL(attend_join_kernel<3>, dim3(grid), dim3(256), 0, st, a, 16 * s.rt); break;
+            case 4: hipLaunchKernelGGL(attend_join_kernel<4>, dim3(grid), dim3(256), 0, st, a, 16 * s.rt); break;
+            case 6: hipLaunchKernelGGL(attend_join_kernel<6>, dim3(grid), dim3(256), 0, st, a, 16 * s.rt); break;
+            default: hipLaunchKernelGGL(attend_join_kernel<8>, dim3(grid), dim3(256), 0, st, a, 16 * s.rt); break;
+        }
+    }
     return launch_status();
 }

@@ -8,6 +8,7 @@ namespace qmm {
 
 constexpr int64_t kKvMaxTokens = 1 << 20;
 constexpr int kKvMaxSeq = 1 << 14;
+constexpr int64_t kKvMaxLength = 0x40000000;  // positions of a sequence
 constexpr int64_t kKvMaxRows = 1 << 27;  // 16 lanes a row, below 2^32 threads
 
 inline bool kv_dim(int d) { return d == 64 || d == 96 || d == 128 || d == 192 || d == 256; }
@@ -33,7 +34,7 @@ inline int kv_place(KvPlace& p, const qmm_kv_cache* c, const int32_t* pages, int
     const int rc = kv_check(c);
     if (rc != QMM_OK) return rc;
     if (ntok < 0 || nseq < 0 || max_pages < 1 || ldpages < max_pages || (!seg_off && nseq != ntok)) return QMM_EINVAL;
-    if (ntok > kKvMaxTokens || nseq > kKvMaxSeq || max_pages > 0x7FFFFFFF / c->page_size) return QMM_EUNSUPPORTED;
+    if (ntok > kKvMaxTokens || nseq > kKvMaxSeq || max_pages > kKvMaxLength || max_pages * c->page_size > kKvMaxLength) return QMM_EUNSUPPORTED;
     if (ntok && nseq && (!pages || !lens)) return QMM_EINVAL;
     if (!aligned(pages, 4) || !aligned(lens, 4) || !aligned(seg_off, 4)) return QMM_EALIGN;
     p = KvPlace{pages, lens, seg_off, ldpages, c->npages, (int)max_pages, c->page_size, c->nheads, c->head_dim, nseq, (int)ntok};

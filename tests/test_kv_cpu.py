@@ -44,7 +44,7 @@ SHARED = [
     (dict(npages=1 << 31), -2), (dict(kstride=4 * 64 * 256 - 16), -1), (dict(vstride=4 * 64 * 136 - 16), -1), (dict(kstride=4 * 64 * 256 + 8), -3),
     (dict(vstride=4 * 64 * 136 + 2), -3), (dict(pages=None), -1), (dict(lens=None), -1), (dict(max_pages=0), -1), (dict(ldpages=4), -1),
     (dict(nseq=-1), -1), (dict(ntok=-1), -1), (dict(seg_off=None), -1), (dict(nseq=(1 << 14) + 1), -2), (dict(ntok=(1 << 20) + 1), -2),
-    (dict(max_pages=1 << 25, ldpages=1 << 25), -2), (dict(pages=TWO), -3), (dict(lens=TWO), -3), (dict(seg_off=TWO), -3), (dict(ntok=0), 0),
+    (dict(max_pages=(1 << 24) + 1, ldpages=1 << 25), -2), (dict(max_pages=1 << 40, ldpages=1 << 40), -2), (dict(pages=TWO), -3), (dict(lens=TWO), -3), (dict(seg_off=TWO), -3), (dict(ntok=0), 0),
     (dict(nseq=0, pages=None, lens=None), 0),
 ]
 
