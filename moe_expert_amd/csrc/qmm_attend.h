@@ -42,7 +42,7 @@ struct AttendArgs {
     float scale;                      // times log2(e)
     int window;                       // 0: none
     int target, least, slots;         // workgroups a head of keys to split the cache over, steps of the shortest part, places for parts
-    int vec;                          // q and out: groups of four values are aligned
+    int vec;                          // out: groups of four values are aligned
 };
 
 // ------------------------------------------------------------------ what a workgroup does
@@ -69,6 +69,10 @@ __device__ __forceinline__ SeqWork seq_work(const AttendArgs& a, int s, int rows
     w.steps = w.n > 0 && last > w.base ? (last - w.base + kAtStep - 1) / kAtStep : 0;
     w.tiles = (int)(((int64_t)w.n * a.group + rows - 1) / rows);
     return w;
+}
+
+__device__ __forceinline__ SeqWork lane_work(const AttendArgs& a, int s, int rows) {
+    return s < a.p.nseq ? seq_work(a, s, rows) : SeqWork{0, 0, 0, 0, 0, 0, 0};
 }
 
 // Steps of a part: the whole work over the target, at least `least`.
@@ -105,33 +109,29 @@ __device__ __forceinline__ bool find_item(const AttendArgs& a, int i, int rows, 
         it.slot = slots[s];
         i -= items[s];
     } else {
-        SeqWork w[kAtInline / 64];
+        SeqWork w;
         int64_t work = 0;
-#pragma unroll
-        for (int j = 0; j < kAtInline / 64; ++j) {
-            w[j] = SeqWork{0, 0, 0, 0, 0, 0, 0};
-            if (64 * j >= nseq) continue;
-            if (64 * j + lane < nseq) w[j] = seq_work(a, 64 * j + lane, rows);
-            const int64_t mine = (int64_t)w[j].steps * w[j].tiles;  // below 2^49 in all: two sums that fit 32 bits
+        for (int j = 0; j < nseq; j += 64) {
+            w = lane_work(a, j + lane, rows);
+            const int64_t mine = (int64_t)w.steps * w.tiles;  // below 2^49 in all: two sums that fit 32 bits
             work += ((int64_t)wave_total((int)(mine >> 24)) << 24) + wave_total((int)(mine & 0xFFFFFF));
         }
         it.c = part_steps(a, work);
         int before = 0, slots = 0;
         bool found = false;
-#pragma unroll
-        for (int j = 0; j < kAtInline / 64; ++j) {
-            if (64 * j >= nseq || found) continue;
-            const int parts = parts_of(w[j], it.c), mine = parts * w[j].tiles, slot = parts > 1 ? mine : 0;
+        for (int j = 0; j < nseq && !found; j += 64) {
+            if (nseq > 64) w = lane_work(a, j + lane, rows);
+            const int parts = parts_of(w, it.c), mine = parts * w.tiles, slot = parts > 1 ? mine : 0;
             const int upto = wave_scan(mine), sl = wave_scan(slot), total = lane_of(upto, 63);
             if (i < before + total) {
                 const int s = __popcll(__ballot(before + upto <= i));
-                it.w.first = lane_of(w[j].first, s);
-                it.w.n = lane_of(w[j].n, s);
-                it.w.len = lane_of(w[j].len, s);
-                it.w.base = lane_of(w[j].base, s);
-                it.w.steps = lane_of(w[j].steps, s);
-                it.w.tiles = lane_of(w[j].tiles, s);
-                it.w.seq = 64 * j + s;
+                it.w.first = lane_of(w.first, s);
+                it.w.n = lane_of(w.n, s);
+                it.w.len = lane_of(w.len, s);
+                it.w.base = lane_of(w.base, s);
+                it.w.steps = lane_of(w.steps, s);
+                it.w.tiles = lane_of(w.tiles, s);
+                it.w.seq = j + s;
                 it.parts = lane_of(parts, s);
                 it.slot = slots + lane_of(sl - slot, s);
                 i -= before + lane_of(upto - mine, s);
@@ -252,6 +252,24 @@ struct Values {
         const int i = (x & 3) * NB + b;
         return (float)__builtin_bit_cast(half2_t, d[x >> 2][i / 2])[i & 1];
     }
+    // The binary16 bits of the largest magnitude among the scales (of the positions seen, if any is not).
+    __device__ __forceinline__ int largest(const bool (&seen)[8], bool masked) const {
+        typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+        u16x2 most = {0, 0};
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 2 * NB; ++i) {
+                uint32_t v = d[h][i] & 0x7FFF7FFFu;
+                if (masked) {
+                    const int x = 4 * h + 2 * i / NB, y = 4 * h + (2 * i + 1) / NB;
+                    if (x == y) v = seen[x] ? v : 0u;
+                    else v = (seen[x] ? v & 0xFFFFu : 0u) | (seen[y] ? v & 0xFFFF0000u : 0u);
+                }
+                most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2, v));
+            }
+        return max((int)most.x, (int)most.y);
+    }
     // Biased bytes; of iq4_nl the levels, where two half dwords of neighbouring positions share a lookup.
     struct Ready {
         uint32_t a[8][kWords], b[TYPE == kKvIq4 ? 8 : 1][kWords];
@@ -317,24 +335,17 @@ __device__ __forceinline__ float rows_sum(float v) {
     return __builtin_bit_cast(float, (int)r[0]) + __builtin_bit_cast(float, (int)r[1]);
 }
 
+__device__ __forceinline__ bool not_finite(uint32_t half) { return (half & 0x7C00u) == 0x7C00u; }
+
+// Orders LDS accesses of the lanes of a wave, which run in step.
+__device__ __forceinline__ void wave_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
 // 2^e for e in [-126, 127]
 __device__ __forceinline__ float power(int e) { return __builtin_bit_cast(float, (uint32_t)(e + 127) << 23); }
 
-__device__ __forceinline__ void load4(float* v, const void* p, int64_t i, int type, int vec) {
-    if (vec && type == kF32) {
-        *(float4_t*)v = *(const float4_t*)((const float*)p + i);
-    } else if (vec) {
-        const u32x2 w = *(const u32x2*)((const uint16_t*)p + i);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const uint32_t b = w[e / 2] >> (16 * (e & 1)) & 0xFFFFu;
-            v[e] = type == kBin16 ? h2f(b) : bf2f(b);
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = load_value(p, i + e, type);
-    }
-}
 __device__ __forceinline__ void store4(const float* v, void* p, int64_t i, int type, int vec) {
     if (vec && type == kF32) {
         *(float4_t*)((float*)p + i) = float4_t{v[0], v[1], v[2], v[3]};
@@ -349,6 +360,15 @@ __device__ __forceinline__ void store4(const float* v, void* p, int64_t i, int t
     }
 }
 
+// Four dims of row r (of its sequence's) of a head of keys, and with the first of them the row's lse.
+__device__ __forceinline__ void write_row(const AttendArgs& a, int first, int head, int r, int d, float4_t f, float most, float sum) {
+    const int token = r / a.group, h = head * a.group + r - token * a.group;
+    const float v[4] = {f[0], f[1], f[2], f[3]};
+    store4(v, a.out, (first + token) * a.ldo + (int64_t)h * a.p.dim + d, a.otype, a.vec);
+    if (d == 0 && a.lse)
+        a.lse[(int64_t)(first + token) * a.nheads + h] = sum != 0.0f ? most * 0.693147180559945f + __logf(sum) : -INFINITY;
+}
+
 // The weight of a result whose maximum is m beside one of a maximum `top`.  At m = -inf its sums are zeros, or NaN.
 __device__ __forceinline__ float beside(float m, float top) { return m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - top); }
 
@@ -357,11 +377,19 @@ __host__ __device__ constexpr int64_t part_floats(int rows, int dim) { return (i
 
 // ------------------------------------------------------------------ the pass
 
+// Resources: the queries' parts lie in LDS, read again each step (two 16-byte reads a block), which leaves the
+// registers to the keys and values in flight.
 template <int KT, int VT, int NB, int RT>
-__global__ __launch_bounds__(64 * kAtWaves, NB > 4 || RT > 1 ? 1 : 2) void attend_kernel(AttendArgs a) {
+__global__ __launch_bounds__(64 * kAtWaves, 2) void attend_kernel(AttendArgs a) {
     constexpr int kRows = 16 * RT, kDim = 32 * NB, kTiles = 2 * NB;
     constexpr bool kKeyBlocks = KT != kKvF16, kValBlocks = VT != kKvF16;
-    __shared__ float so[kAtWaves][kRows][kDim + 4], lm[kAtWaves][kRows], ll[kAtWaves][kRows];
+    // The next keys are read before the weights, or after the values where the registers do not hold both.
+    constexpr bool kEarly = NB < 8;
+    // The sums of two waves at a time, at the end; until then a quarter is a wave's own for odd values.
+    __shared__ __attribute__((aligned(16))) float so[2][kRows][kDim + 4];
+    __shared__ float lm[2][kRows], ll[2][kRows], lc[kRows];
+    static_assert(sizeof(so) / kAtWaves >= kRows * kAtStep * 4 + kDim * 2, "weights and a position's values");
+    __shared__ __attribute__((aligned(16))) uint32_t lq[RT][NB][2][64][4];
     const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int head = (int)(blockIdx.x % (uint32_t)a.p.nheads);
@@ -372,66 +400,9 @@ __global__ __launch_bounds__(64 * kAtWaves, NB > 4 || RT > 1 ? 1 : 2) void atten
     // The rows of the tile: lane n's, the positions [rlo, rhi) that they see, and the same over all of them.
     const int row0 = it.tile * kRows, rows = min(kRows, w.n * a.group - row0), cap = a.p.max_pages * a.p.page_size;
     const auto low = [&](int pos) { return a.window > 0 && pos >= a.window ? pos - a.window + 1 : 0; };
-    const int pos0 = w.len - w.n + row0 / a.group, pos1 = w.len - w.n + (row0 + rows - 1) / a.group;
+    const int tok0 = row0 / a.group, tok1 = (row0 + rows - 1) / a.group;
+    const int pos0 = w.len - w.n + tok0, pos1 = w.len - w.n + tok1;
     const int lo_min = low(pos0), lo_max = low(pos1), hi_min = min(pos0 + 1, cap), hi_max = min(pos1 + 1, cap);
-    int rlo[RT], rhi[RT], token[RT];
-    half8_t q[RT][2][NB];
-    float c[RT];  // scores are c times the sums of the scaled operands
-#pragma unroll
-    for (int x = 0; x < RT; ++x) {
-        const int r = row0 + 16 * x + n;
-        const bool live = r < row0 + rows;
-        token[x] = r / a.group;
-        const int pos = w.len - w.n + token[x];
-        rlo[x] = low(pos);
-        rhi[x] = live ? min(pos + 1, cap) : 0;
-        const int64_t at = live ? (w.first + token[x]) * a.ldq + (int64_t)(head * a.group + r - token[x] * a.group) * kDim : 0;
-        float v[NB][8], most = 0.0f;
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            if (live) {
-                load4(v[b], a.q, at + 32 * b + (kKeyBlocks ? 4 * g : 8 * g), a.qtype, a.vec);
-                load4(v[b] + 4, a.q, at + 32 * b + (kKeyBlocks ? 16 + 4 * g : 8 * g + 4), a.qtype, a.vec);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[b][e] = 0.0f;
-            }
-        }
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                v[b][e] *= a.scale;
-                most = __builtin_fmaxf(most, __builtin_fabsf(v[b][e]));
-            }
-        most = rows_max(most);
-        // the power of two that puts the largest in [2^13, 2^14); rows of nothing but tiny values stay what they are
-        const int e = min(max((int)(__builtin_bit_cast(uint32_t, most) >> 23), 40), 254) - 126;
-        const float up = power(14 - e);
-        c[x] = power(e - 14 + (kKeyBlocks ? 10 : 0));
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            uint32_t hi[4], lo[4];
-            // operand element 2 m + i of a block format is dim 32b + 16i + 4g + m
-#pragma unroll
-            for (int m = 0; m < 4; ++m)
-                two_parts((kKeyBlocks ? v[b][m] : v[b][2 * m]) * up, (kKeyBlocks ? v[b][4 + m] : v[b][2 * m + 1]) * up, hi[m], lo[m]);
-            q[x][0][b] = as_half8(hi[0], hi[1], hi[2], hi[3]);
-            q[x][1][b] = as_half8(lo[0], lo[1], lo[2], lo[3]);
-        }
-    }
-
-    float4_t o[RT][kTiles];
-    float m[RT], l[RT], limit[RT], fold[RT];
-#pragma unroll
-    for (int x = 0; x < RT; ++x) {
-        m[x] = -INFINITY;
-        l[x] = 0.0f;
-        limit[x] = power(-24);
-        fold[x] = power(14 + 24);
-#pragma unroll
-        for (int t = 0; t < kTiles; ++t) o[x][t] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    }
 
     // This wave's steps of the part, those that the tile sees.
     int s0 = it.part * it.c, s1 = min(s0 + it.c, w.steps);
@@ -456,11 +427,83 @@ __global__ __launch_bounds__(64 * kAtWaves, NB > 4 || RT > 1 ? 1 : 2) void atten
             keys[h].load(a.k.base + (pg < 0 ? 0 : pg * a.k.stride) + kchunk, lane_of(places, 2 * (k & 31) + h), a.p.page_size);
         }
     };
-
     if (ksteps > 0) {
         read_pages(0);
         load_keys(0);
     }
+
+    // The queries, 16 threads a row: scaled, their two parts laid out as the operand that a lane reads.
+    // Thread j holds the dims 32b + j and 32b + 16 + j (element 2m + i of a block format's operand is dim 32b + 16i
+    // + 4g + m) or 32b + 2j and the next (binary16: element e is 32b + 8g + e).
+#pragma unroll
+    for (int x = 0; x < RT; ++x) {
+        const int r = 16 * x + (int)threadIdx.x / 16, j = threadIdx.x & 15, tok = (row0 + r) / a.group;
+        const bool live = r < rows;
+        const int64_t at = live ? (w.first + tok) * a.ldq + (int64_t)(head * a.group + row0 + r - tok * a.group) * kDim : 0;
+        float v[NB][2], most = 0.0f;
+        if (a.qtype == kF32) {
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) v[b][i] = ((const float*)a.q)[at + 32 * b + (kKeyBlocks ? 16 * i + j : 2 * j + i)];
+        } else {
+            uint32_t raw[NB][2];
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) raw[b][i] = ((const uint16_t*)a.q)[at + 32 * b + (kKeyBlocks ? 16 * i + j : 2 * j + i)];
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) v[b][i] = a.qtype == kBin16 ? h2f(raw[b][i]) : bf2f(raw[b][i]);
+        }
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                v[b][i] = live ? v[b][i] * a.scale : 0.0f;
+                most = __builtin_fmaxf(most, __builtin_fabsf(v[b][i]));
+            }
+        most = __builtin_fmaxf(most, dpp<0xB1>(most));
+        most = __builtin_fmaxf(most, dpp<0x4E>(most));
+        most = __builtin_fmaxf(most, dpp<0x141>(most));
+        most = __builtin_fmaxf(most, dpp<0x140>(most));
+        // the power of two that puts the largest in [2^13, 2^14); rows of nothing but tiny values stay what they are
+        const int e = min(max((int)(__builtin_bit_cast(uint32_t, most) >> 23), 40), 254) - 126;
+        const float up = power(14 - e);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            uint32_t hi, lo;
+            two_parts(v[b][0] * up, v[b][1] * up, hi, lo);
+            lq[x][b][0][16 * (j / 4) + r % 16][j % 4] = hi;
+            lq[x][b][1][16 * (j / 4) + r % 16][j % 4] = lo;
+        }
+        if (j == 0) lc[r] = power(e - 14 + (kKeyBlocks ? 10 : 0));
+    }
+    __syncthreads();
+
+    int rlo[RT], rhi[RT];
+    float c[RT];  // scores are c times the sums of the scaled operands
+    float4_t o[RT][kTiles];
+    float m[RT], l[RT], limit[RT], fold[RT];
+    int bound[RT];  // the binary16 bits of limit, a power of two above the scales of values that the row has seen
+#pragma unroll
+    for (int x = 0; x < RT; ++x) {
+        const int r = 16 * x + n;
+        const int pos = w.len - w.n + (row0 + r) / a.group;
+        rlo[x] = low(pos);
+        rhi[x] = r < rows ? min(pos + 1, cap) : 0;
+        c[x] = lc[r];
+        m[x] = -INFINITY;
+        l[x] = 0.0f;
+        limit[x] = power(-24);
+        fold[x] = power(14 + 24);
+        bound[x] = 1;
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) o[x][t] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    const auto queries = [&](int x, int b, int part) { return __builtin_bit_cast(half8_t, *(const u32x4*)lq[x][b][part][lane]); };
+
     for (int k = 0; k < ksteps; ++k) {
         const int j0 = start + kAtStep * kAtWaves * k;
         const bool exist[2] = {lane_of(pages, 2 * (k & 31)) >= 0, lane_of(pages, 2 * (k & 31) + 1) >= 0};
@@ -471,84 +514,96 @@ __global__ __launch_bounds__(64 * kAtWaves, NB > 4 || RT > 1 ? 1 : 2) void atten
             vals.load(h, a.v.base + (pg < 0 ? 0 : pg * a.v.stride) + vchunk, lane_of(places, 2 * (k & 31) + h), a.p.page_size);
         }
         float z[RT][8];
+        {
+            typename Keys<KT, NB>::Ready ready[2];
+            keys[0].ready(ready[0]);
+            keys[1].ready(ready[1]);
+            float4_t s[RT][2], t[RT][2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            typename Keys<KT, NB>::Ready ready;
-            keys[h].ready(ready);
-            if constexpr (kKeyBlocks) {
+            for (int x = 0; x < RT; ++x)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    s[x][h] = t[x][h] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) z[x][4 * h + r] = 0.0f;
+                }
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                if constexpr (kKeyBlocks) __builtin_amdgcn_sched_barrier(0);
+                const half8_t kb[2] = {Keys<KT, NB>::block(ready[0], b), Keys<KT, NB>::block(ready[1], b)};
+#pragma unroll
+                for (int x = 0; x < RT; ++x) {
+                    const half8_t qh = queries(x, b, 0), ql = queries(x, b, 1);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if constexpr (kKeyBlocks) {
+                            float4_t u = {0.0f, 0.0f, 0.0f, 0.0f};
+                            u = __builtin_amdgcn_mfma_f32_16x16x32_f16(kb[h], ql, u, 0, 0, 0);
+                            u = __builtin_amdgcn_mfma_f32_16x16x32_f16(kb[h], qh, u, 0, 0, 0);
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) z[x][4 * h + r] = __builtin_fmaf(u[r], keys[h].scale(r, b), z[x][4 * h + r]);
+                        } else {
+                            s[x][h] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kb[h], qh, s[x][h], 0, 0, 0);
+                            t[x][h] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kb[h], ql, t[x][h], 0, 0, 0);
+                        }
+                    }
+                }
+            }
+            if constexpr (!kKeyBlocks) {
 #pragma unroll
                 for (int x = 0; x < RT; ++x)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) z[x][4 * h + r] = 0.0f;
-#pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    const half8_t kb = Keys<KT, NB>::block(ready, b);
-#pragma unroll
-                    for (int x = 0; x < RT; ++x) {
-                        float4_t s = {0.0f, 0.0f, 0.0f, 0.0f};
-                        s = __builtin_amdgcn_mfma_f32_16x16x32_f16(kb, q[x][1][b], s, 0, 0, 0);
-                        s = __builtin_amdgcn_mfma_f32_16x16x32_f16(kb, q[x][0][b], s, 0, 0, 0);
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) z[x][4 * h + r] = __builtin_fmaf(s[r], keys[h].scale(r, b), z[x][4 * h + r]);
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int x = 0; x < RT; ++x) {
-                    float4_t s = {0.0f, 0.0f, 0.0f, 0.0f}, t = s;
-#pragma unroll
-                    for (int b = 0; b < NB; ++b) {
-                        const half8_t kb = Keys<KT, NB>::block(ready, b);
-                        s = __builtin_amdgcn_mfma_f32_16x16x32_f16(kb, q[x][0][b], s, 0, 0, 0);
-                        t = __builtin_amdgcn_mfma_f32_16x16x32_f16(kb, q[x][1][b], t, 0, 0, 0);
-                    }
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) z[x][4 * h + r] = s[r] + t[r];
-                }
+                    for (int i = 0; i < 8; ++i) z[x][i] = s[x][i / 4][i & 3] + t[x][i / 4][i & 3];
             }
         }
-        if (k + 1 < ksteps) {
+        __builtin_amdgcn_sched_barrier(0);
+        if (kEarly && k + 1 < ksteps) {
             if ((k & 31) == 31) read_pages(k + 1);
             load_keys(k + 1);
         }
         // Positions that some row of the tile does not see: their scores go, whatever they are.
         const bool masked = j0 < lo_max || j0 + kAtStep > hi_min || !exist[0] || !exist[1];
-        const auto seen = [&](int x, int i) {
-            const int j = j0 + 16 * (i >> 2) + 4 * g + (i & 3);
-            return exist[i >> 2] && j >= rlo[x] && j < rhi[x];
-        };
+        bool seen[RT][8];
         if (masked) {
 #pragma unroll
             for (int x = 0; x < RT; ++x)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) z[x][i] = seen(x, i) ? z[x][i] : -INFINITY;
+                for (int i = 0; i < 8; ++i) {
+                    const int j = j0 + 16 * (i >> 2) + 4 * g + (i & 3);
+                    seen[x][i] = exist[i >> 2] && j >= rlo[x] && j < rhi[x];
+                    z[x][i] = seen[x][i] ? z[x][i] : -INFINITY;
+                }
+        } else {
+#pragma unroll
+            for (int x = 0; x < RT; ++x)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) seen[x][i] = true;
         }
-        float base[RT];
+        float top[RT];
         bool grew = false;
 #pragma unroll
         for (int x = 0; x < RT; ++x) {
-            float top = m[x];
+            top[x] = m[x];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) top = __builtin_fmaxf(top, z[x][i]);
-            top = rows_max(top);
-            grew |= top > m[x];
-            base[x] = top;
+            for (int i = 0; i < 8; ++i) top[x] = __builtin_fmaxf(top[x], z[x][i]);
+            top[x] = rows_max(top[x]);
+            grew |= top[x] > m[x];
         }
         if (__any(grew)) {
 #pragma unroll
             for (int x = 0; x < RT; ++x) {
-                const float shrink = base[x] == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((m[x] - base[x]) * c[x]);
-                m[x] = base[x];
+                const float shrink = top[x] == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((m[x] - top[x]) * c[x]);
+                m[x] = top[x];
                 l[x] *= shrink;
 #pragma unroll
                 for (int t = 0; t < kTiles; ++t) o[x][t] *= shrink;
             }
         }
-        // Weights; of binary16 values times 2^14, of blocks' times the scales and a power of two that keeps those
-        // below 2^14 too.
+        // Weights: of binary16 values times 2^14; of blocks' to be multiplied by the scales and a power of two that
+        // keeps the largest product there.
 #pragma unroll
         for (int x = 0; x < RT; ++x) {
-            const float from = base[x] == -INFINITY ? 0.0f : __builtin_fmaf(-base[x], c[x], kValBlocks ? 0.0f : 14.0f);
+            const float from = m[x] == -INFINITY ? 0.0f : __builtin_fmaf(-m[x], c[x], kValBlocks ? 0.0f : 14.0f);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 z[x][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(z[x][i], c[x], from));
@@ -556,176 +611,175 @@ __global__ __launch_bounds__(64 * kAtWaves, NB > 4 || RT > 1 ? 1 : 2) void atten
             }
         }
         if constexpr (kValBlocks) {
-            // The largest scale a row has seen: limit is a power of two above it.
-            float most[RT];
-            if (!masked) {
-                float d = 0.0f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-#pragma unroll
-                    for (int b = 0; b < NB; ++b) d = __builtin_fmaxf(d, __builtin_fabsf(vals.scale(i, b)));
-#pragma unroll
-                for (int x = 0; x < RT; ++x) most[x] = d;
-            } else {
-#pragma unroll
-                for (int x = 0; x < RT; ++x) {
-                    most[x] = 0.0f;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        float d = 0.0f;
-#pragma unroll
-                        for (int b = 0; b < NB; ++b) d = __builtin_fmaxf(d, __builtin_fabsf(vals.scale(i, b)));
-                        most[x] = __builtin_fmaxf(most[x], seen(x, i) ? d : 0.0f);
-                    }
-                }
-            }
             bool above = false;
+            int most[RT];
 #pragma unroll
-            for (int x = 0; x < RT; ++x) above |= most[x] >= limit[x];
+            for (int x = 0; x < RT; ++x) {
+                most[x] = vals.largest(seen[x], masked);
+                above |= most[x] >= bound[x];
+            }
             if (__any(above)) {
 #pragma unroll
                 for (int x = 0; x < RT; ++x) {
-                    const float d = rows_max(most[x]);  // (an infinity: 2^17)
-                    const int e = min((int)(__builtin_bit_cast(uint32_t, d) >> 23) - 126, 17);
-                    const float to = __builtin_fmaxf(limit[x], power(max(e, -24)));
-                    const float shrink = limit[x] * (1.0f / to);
+                    const float d = rows_max(__builtin_fabsf(h2f(min(most[x], 0x7C00))));  // (an infinity, NaN: 2^17)
+                    const int e = max(min((int)(__builtin_bit_cast(uint32_t, d) >> 23) - 126, 17), -24);
+                    const float to = __builtin_fmaxf(limit[x], power(e)), shrink = limit[x] * (1.0f / to);
                     limit[x] = to;
                     fold[x] = 16384.0f / to;
+                    bound[x] = to > 65536.0f ? 0x10000 : (int)f2h(to);
 #pragma unroll
                     for (int t = 0; t < kTiles; ++t) o[x][t] *= shrink;
                 }
             }
+        } else if (masked) {
+            // Places that no row sees count as zeros.  Infinities and NaN that some rows see and others do not
+            // must not meet the others' zeros in the products: they are added one position at a time, and left out there.
+            bool odd = false;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int j = j0 + 16 * (i >> 2) + 4 * g + (i & 3);
+                const bool some = exist[i >> 2] && j >= lo_min && j < hi_max;
+#pragma unroll
+                for (int e = 0; e < Values<VT, NB>::kWords; ++e) {
+                    vals.w[i][e] = some ? vals.w[i][e] : 0u;
+                    odd |= not_finite(vals.w[i][e]) || not_finite(vals.w[i][e] >> 16);
+                }
+            }
+            if (__any(odd)) {
+                float* weight = &so[0][0][0] + wave * (int)(sizeof(so) / 4 / kAtWaves);
+                uint32_t* row = (uint32_t*)(weight + kRows * kAtStep);
+#pragma unroll
+                for (int x = 0; x < RT; ++x)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) weight[(16 * x + n) * kAtStep + 16 * (i >> 2) + 4 * g + (i & 3)] = seen[x][i] ? z[x][i] : -1.0f;
+                for (int u = 0; u < kAtStep; ++u) {
+                    if (g == u / 4 % 4) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (i == 4 * (u / 16) + u % 4)
+#pragma unroll
+                                for (int e = 0; e < Values<VT, NB>::kWords; ++e) row[n * Values<VT, NB>::kWords + e] = vals.w[i][e];
+                    }
+                    wave_fence();
+#pragma unroll
+                    for (int x = 0; x < RT; ++x) {
+                        const float p = weight[(16 * x + n) * kAtStep + u];
+#pragma unroll
+                        for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) {
+                                const uint32_t v = ((const uint16_t*)row)[Values<VT, NB>::dim(t, 4 * g + r)];
+                                if (p >= 0.0f && not_finite(v)) o[x][t][r] += p * h2f(v);
+                            }
+                    }
+                    wave_fence();
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+#pragma unroll
+                    for (int e = 0; e < Values<VT, NB>::kWords; ++e) {
+                        const uint32_t v = vals.w[i][e];
+                        vals.w[i][e] = (not_finite(v) ? 0u : v & 0xFFFFu) | (not_finite(v >> 16) ? 0u : v & 0xFFFF0000u);
+                    }
+            }
         }
         // The sums of values.
         typename Values<VT, NB>::Ready ready;
-        bool again = false;
-        if constexpr (!kValBlocks) {
-            if (masked) {
-                // Places that no row sees count as zeros; odd values that some rows see and others do not are
-                // taken for one token at a time.
-                bool odd = false;
+        vals.ready(ready);
+        half8_t ph[RT], pl[RT];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int j = j0 + 16 * (i >> 2) + 4 * g + (i & 3);
-                    const bool some = exist[i >> 2] && j >= lo_min && j < hi_max;
-#pragma unroll
-                    for (int e = 0; e < Values<VT, NB>::kWords; ++e) {
-                        vals.w[i][e] = some ? vals.w[i][e] : 0u;
-                        odd |= (vals.w[i][e] & 0x7C00u) == 0x7C00u || (vals.w[i][e] & 0x7C000000u) == 0x7C000000u;
-                    }
-                }
-                again = __any(odd);
-            }
-        }
-        if (again) {
-            const int t0 = row0 / a.group, t1 = (row0 + rows - 1) / a.group;
-            for (int t = t0; t <= t1; ++t) {
-                Values<VT, NB> own = vals;
-                const int pos = w.len - w.n + t;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int j = j0 + 16 * (i >> 2) + 4 * g + (i & 3);
-#pragma unroll
-                    for (int e = 0; e < Values<VT, NB>::kWords; ++e) own.w[i][e] = j >= low(pos) && j <= pos ? vals.w[i][e] : 0u;
-                }
-                own.ready(ready);
+        for (int t = 0; t < kTiles; ++t) {
+            if (kValBlocks ? t % 2 == 0 : t == 0) {
+                if constexpr (kValBlocks) __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int x = 0; x < RT; ++x) {
                     uint32_t hi[4], lo[4];
-                    const bool mine = token[x] == t;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) two_parts(mine ? z[x][2 * i] : 0.0f, mine ? z[x][2 * i + 1] : 0.0f, hi[i], lo[i]);
-                    const half8_t ph = as_half8(hi[0], hi[1], hi[2], hi[3]), pl = as_half8(lo[0], lo[1], lo[2], lo[3]);
+                    for (int i = 0; i < 4; ++i) {
+                        float u[2];
 #pragma unroll
-                    for (int u = 0; u < kTiles; ++u) {
-                        // a row of another token gets sums of zeros with infinities: it keeps what it has
-                        const half8_t v = Values<VT, NB>::tile(ready, u);
-                        float4_t s = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, pl, o[x][u], 0, 0, 0);
-                        s = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, ph, s, 0, 0, 0);
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) o[x][u][r] = mine ? s[r] : o[x][u][r];
+                        for (int e = 0; e < 2; ++e) {
+                            u[e] = z[x][2 * i + e];
+                            if constexpr (kValBlocks) {
+                                u[e] = u[e] * fold[x] * vals.scale(2 * i + e, t / 2);
+                                if (masked) u[e] = seen[x][2 * i + e] ? u[e] : 0.0f;
+                            }
+                        }
+                        two_parts(u[0], u[1], hi[i], lo[i]);
                     }
+                    ph[x] = as_half8(hi[0], hi[1], hi[2], hi[3]);
+                    pl[x] = as_half8(lo[0], lo[1], lo[2], lo[3]);
                 }
             }
-        } else {
-            vals.ready(ready);
+            const half8_t v = Values<VT, NB>::tile(ready, t);
 #pragma unroll
             for (int x = 0; x < RT; ++x) {
-                half8_t ph, pl;
-#pragma unroll
-                for (int t = 0; t < kTiles; ++t) {
-                    if (kValBlocks ? t % 2 == 0 : t == 0) {
-                        uint32_t hi[4], lo[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            float u[2];
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                u[e] = z[x][2 * i + e];
-                                if constexpr (kValBlocks) {
-                                    u[e] = u[e] * fold[x] * vals.scale(2 * i + e, t / 2);
-                                    if (masked) u[e] = seen(x, 2 * i + e) ? u[e] : 0.0f;
-                                }
-                            }
-                            two_parts(u[0], u[1], hi[i], lo[i]);
-                        }
-                        ph = as_half8(hi[0], hi[1], hi[2], hi[3]);
-                        pl = as_half8(lo[0], lo[1], lo[2], lo[3]);
-                    }
-                    const half8_t v = Values<VT, NB>::tile(ready, t);
-                    o[x][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, pl, o[x][t], 0, 0, 0);
-                    o[x][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, ph, o[x][t], 0, 0, 0);
-                }
+                o[x][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, pl[x], o[x][t], 0, 0, 0);
+                o[x][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, ph[x], o[x][t], 0, 0, 0);
             }
+        }
+        if (!kEarly && k + 1 < ksteps) {
+            if ((k & 31) == 31) read_pages(k + 1);
+            load_keys(k + 1);
         }
     }
 
-    // The waves' results, in base-2 units of the scores, joined through LDS.
+    // The waves' results, in base-2 units of the scores: two waves to the other two through LDS, then those.
 #pragma unroll
     for (int x = 0; x < RT; ++x) {
-        const float total = rows_sum(l[x]);
-        if (g == 0) {
-            lm[wave][16 * x + n] = m[x] * c[x];
-            ll[wave][16 * x + n] = kValBlocks ? total : total * power(-14);
-        }
+        l[x] = rows_sum(l[x]) * (kValBlocks ? 1.0f : power(-14));
+        m[x] *= c[x];
         const float back = kValBlocks ? limit[x] * power(10 - 14) : power(-14);
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t)
+        for (int t = 0; t < kTiles; ++t) o[x][t] *= back;
+    }
+    const auto put = [&](int at) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) so[wave][16 * x + n][Values<VT, NB>::dim(t, 4 * g + r)] = o[x][t][r] * back;
+        for (int x = 0; x < RT; ++x) {
+            if (g == 0) {
+                lm[at][16 * x + n] = m[x];
+                ll[at][16 * x + n] = l[x];
+            }
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) so[at][16 * x + n][Values<VT, NB>::dim(t, 4 * g + r)] = o[x][t][r];
+        }
+    };
+    __syncthreads();
+    if (wave >= 2) put(wave - 2);
+    __syncthreads();
+    if (wave < 2) {
+#pragma unroll
+        for (int x = 0; x < RT; ++x) {
+            const float other = lm[wave][16 * x + n], most = __builtin_fmaxf(m[x], other), mine = beside(m[x], most), its = beside(other, most);
+            m[x] = most;
+            l[x] = l[x] * mine + ll[wave][16 * x + n] * its;
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) o[x][t][r] = o[x][t][r] * mine + so[wave][16 * x + n][Values<VT, NB>::dim(t, 4 * g + r)] * its;
+        }
+        put(wave);
     }
     __syncthreads();
     const bool whole = it.parts == 1;
-    const int64_t slot = (int64_t)(it.slot + it.part) * a.p.nheads + head;
     if (!whole && (it.slot < 0 || it.slot + it.part >= a.slots)) return;  // offsets that decrease: no place for it
-    float* part = a.parts + slot * part_floats(kRows, kDim);
+    float* part = a.parts + ((int64_t)(it.slot + it.part) * a.p.nheads + head) * part_floats(kRows, kDim);
     for (int i = threadIdx.x; i < rows * (kDim / 4); i += 64 * kAtWaves) {
         const int r = i / (kDim / 4), d = 4 * (i - r * (kDim / 4));
-        float top = lm[0][r];
-#pragma unroll
-        for (int v = 1; v < kAtWaves; ++v) top = __builtin_fmaxf(top, lm[v][r]);
-        float sum = 0.0f, f[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int v = 0; v < kAtWaves; ++v) {
-            const float e = beside(lm[v][r], top);
-            sum += e * ll[v][r];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) f[u] += e * so[v][r][d + u];
-        }
+        const float most = __builtin_fmaxf(lm[0][r], lm[1][r]), e0 = beside(lm[0][r], most), e1 = beside(lm[1][r], most);
+        const float sum = e0 * ll[0][r] + e1 * ll[1][r];
+        float4_t f = e0 * *(const float4_t*)&so[0][r][d] + e1 * *(const float4_t*)&so[1][r][d];
         if (whole) {
-            const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
-#pragma unroll
-            for (int u = 0; u < 4; ++u) f[u] *= inv;
-            const int tok = (row0 + r) / a.group, h = head * a.group + row0 + r - tok * a.group;
-            store4(f, a.out, (w.first + tok) * a.ldo + (int64_t)h * kDim + d, a.otype, a.vec);
-            if (d == 0 && a.lse)
-                a.lse[(int64_t)(w.first + tok) * a.nheads + h] = sum != 0.0f ? top * 0.693147180559945f + __logf(sum) : -INFINITY;
+            f *= sum != 0.0f ? 1.0f / sum : 0.0f;
+            write_row(a, w.first, head, row0 + r, d, f, most, sum);
         } else {
             if (d == 0) {
-                part[r] = top;
+                part[r] = most;
                 part[kRows + r] = sum;
             }
-            *(float4_t*)(part + 2 * kRows + r * kDim + d) = float4_t{f[0], f[1], f[2], f[3]};
+            *(float4_t*)(part + 2 * kRows + r * kDim + d) = f;
         }
     }
 }

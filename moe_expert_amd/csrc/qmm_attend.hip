@@ -59,53 +59,51 @@ __global__ __launch_bounds__(1024) void attend_plan_kernel(AttendArgs a, int row
     }
 }
 
-// The parts of a tile joined, in the order of the parts: 32 dims of a row are a unit, the tile's workgroups share
-// the units.  Eight lanes hold a unit, 32 groups of them every 32nd part.
-template <int NB>
+// The parts of a tile joined, in the order of the parts.  The tile's workgroups share its groups of four dims; a
+// group's parts go to E lanes of a wave, each every E-th of them, lanes of neighbouring groups beside each other.
+template <int E>
+__device__ __forceinline__ void join(const AttendArgs& a, const Item& it, int head, int tile_rows) {
+    const int dim = a.p.dim, row0 = it.tile * tile_rows, rows = min(tile_rows, it.w.n * a.group - row0), quads = rows * (dim / 4);
+    const int lane = threadIdx.x & 63, run = lane / (64 / E);
+    const int64_t step = a.p.nheads * part_floats(tile_rows, dim);
+    const float* part = a.parts + ((int64_t)it.slot * a.p.nheads + head) * part_floats(tile_rows, dim);
+    for (int u = (it.part * 4 + (int)(threadIdx.x >> 6)) * (64 / E); u < quads; u += it.parts * 4 * (64 / E)) {
+        const int at = min(u + lane % (64 / E), quads - 1), r = at / (dim / 4), d = 4 * (at - r * (dim / 4));
+        float most = -INFINITY, sum = 0.0f;
+        float4_t f = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+        for (int i = run; i < it.parts; i += E) {
+            const float* p = part + i * step;
+            const float m = p[r], l = p[tile_rows + r];
+            const float4_t o = *(const float4_t*)(p + 2 * tile_rows + r * dim + d);
+            const float now = __builtin_fmaxf(most, m), old = beside(most, now), fresh = beside(m, now);
+            most = now;
+            sum = sum * old + l * fresh;
+            f = f * old + o * fresh;
+        }
+#pragma unroll
+        for (int x = 64 / E; x < 64; x <<= 1) {
+            const float m = __shfl_xor(most, x, 64), l = __shfl_xor(sum, x, 64);
+            const float now = __builtin_fmaxf(most, m), old = beside(most, now), fresh = beside(m, now);
+            most = now;
+            sum = sum * old + l * fresh;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[e] = f[e] * old + __shfl_xor(f[e], x, 64) * fresh;
+        }
+        if (run == 0 && u + lane < quads) {
+            f *= sum != 0.0f ? 1.0f / sum : 0.0f;
+            write_row(a, it.w.first, head, row0 + r, d, f, most, sum);
+        }
+    }
+}
+
 __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, int tile_rows) {
-    __shared__ float sm[32], sl[32], so[32][36];
     const int head = (int)(blockIdx.x % (uint32_t)a.p.nheads);
     Item it;
     if (!find_item(a, (int)(blockIdx.x / (uint32_t)a.p.nheads), tile_rows, it) || it.parts == 1) return;
     if (it.slot < 0 || it.slot + it.parts > a.slots) return;
-    const int row0 = it.tile * tile_rows, rows = min(tile_rows, it.w.n * a.group - row0);
-    const int run = threadIdx.x / 8, e = threadIdx.x & 7;
-    const int64_t size = part_floats(tile_rows, 32 * NB);
-    const float* part = a.parts + ((int64_t)it.slot * a.p.nheads + head) * size;
-    for (int u = it.part; u < rows * NB; u += it.parts) {
-        const int r = u / NB, d = 32 * (u - r * NB) + 4 * e;
-        float top = -INFINITY, sum = 0.0f;
-        float4_t f = {0.0f, 0.0f, 0.0f, 0.0f};
-        for (int i = run; i < it.parts; i += 32) {
-            const float* p = part + (int64_t)i * a.p.nheads * size;
-            const float m = p[r], l = p[tile_rows + r];
-            const float4_t o = *(const float4_t*)(p + 2 * tile_rows + r * (32 * NB) + d);
-            const float now = __builtin_fmaxf(top, m), old = beside(top, now), fresh = beside(m, now);
-            top = now;
-            sum = sum * old + l * fresh;
-            f = f * old + o * fresh;
-        }
-        __syncthreads();
-        if (e == 0) {
-            sm[run] = top;
-            sl[run] = sum;
-        }
-        *(float4_t*)&so[run][4 * e] = f;
-        __syncthreads();
-        if (threadIdx.x < 32) {
-            float most = -INFINITY, total = 0.0f, v = 0.0f;
-            for (int i = 0; i < 32; ++i) most = __builtin_fmaxf(most, sm[i]);
-            for (int i = 0; i < 32; ++i) {
-                const float x = beside(sm[i], most);
-                total += x * sl[i];
-                v += x * so[i][threadIdx.x];
-            }
-            const int tok = (row0 + r) / a.group, h = head * a.group + row0 + r - tok * a.group, dim = 32 * (u - r * NB) + (int)threadIdx.x;
-            store_value(a.out, (it.w.first + tok) * a.ldo + (int64_t)h * (32 * NB) + dim, a.otype, total != 0.0f ? v * (1.0f / total) : 0.0f);
-            if (dim == 0 && a.lse)
-                a.lse[(int64_t)(it.w.first + tok) * a.nheads + h] = total != 0.0f ? most * 0.693147180559945f + __logf(total) : -INFINITY;
-        }
-    }
+    if (it.parts <= 16) join<1>(a, it, head, tile_rows);
+    else join<16>(a, it, head, tile_rows);
 }
 
 }  // namespace qmm
@@ -197,21 +195,13 @@ extern "C" int qmm_kv_attend(const qmm_kv_cache* c, const int32_t* pages, int64_
     a.target = s.target;
     a.least = s.least;
     a.slots = (int)s.slots;
-    a.vec = fours(q, ldq, qtype) && fours(out, ldo, otype);
+    a.vec = fours(out, ldo, otype);
     const hipStream_t st = as_stream(stream);
     if (a.plan) hipLaunchKernelGGL(attend_plan_kernel, dim3(1), dim3(1024), 0, st, a, 16 * s.rt, const_cast<int32_t*>(a.plan));
     const unsigned grid = (unsigned)(s.items * c->nheads);
     if (c->ktype == QMM_F16) attend_f16(a, grid, s.rt, st);
     else if (c->ktype == QMM_Q8_0) attend_q8(a, grid, s.rt, st);
     else attend_iq4(a, grid, s.rt, st);
-    if (s.slots) {
-        switch (c->head_dim / 32) {
-            case 2: hipLaunchKernelGGL(attend_join_kernel<2>, dim3(grid), dim3(256), 0, st, a, 16 * s.rt); break;
-            case 3: hipLaunchKernelGGL(attend_join_kernel<3>, dim3(grid), dim3(256), 0, st, a, 16 * s.rt); break;
-            case 4: hipLaunchKernelGGL(attend_join_kernel<4>, dim3(grid), dim3(256), 0, st, a, 16 * s.rt); break;
-            case 6: hipLaunchKernelGGL(attend_join_kernel<6>, dim3(grid), dim3(256), 0, st, a, 16 * s.rt); break;
-            default: hipLaunchKernelGGL(attend_join_kernel<8>, dim3(grid), dim3(256), 0, st, a, 16 * s.rt); break;
-        }
-    }
+    if (s.slots) hipLaunchKernelGGL(attend_join_kernel, dim3(grid), dim3(256), 0, st, a, 16 * s.rt);
     return launch_status();
 }
