@@ -231,6 +231,8 @@ struct Keys {
     }
 };
 
+__device__ __forceinline__ bool not_finite(uint32_t half) { return (half & 0x7C00u) == 0x7C00u; }
+
 // The values of 32 positions: lane (n, g) holds, of the positions 4g .. 4g+3 of both halves, the dims that
 // row n of the 2 NB operands V^T takes: tile (b, i) dim 32b + 16i + n (binary16: tile j dim 2 NB n + j).
 template <int TYPE, int NB>
@@ -248,12 +250,13 @@ struct Values {
         if constexpr (TYPE != kKvF16)
             load_bytes<8 * NB>(d[half], chunk + (uint32_t)(page_size * Side<TYPE, NB>::kFactor + (place + 4 * g) * (2 * NB)));
     }
-    __device__ __forceinline__ float scale(int x, int b) const {
+    __device__ __forceinline__ _Float16 scale(int x, int b) const {
         const int i = (x & 3) * NB + b;
-        return (float)__builtin_bit_cast(half2_t, d[x >> 2][i / 2])[i & 1];
+        return __builtin_bit_cast(half2_t, d[x >> 2][i / 2])[i & 1];
     }
-    // The binary16 bits of the largest magnitude among the scales (of the positions seen, if any is not).
-    __device__ __forceinline__ int largest(const bool (&seen)[8], bool masked) const {
+    // The binary16 bits of the largest magnitude among the scales, of all positions or of those seen.
+    template <bool MASKED>
+    __device__ __forceinline__ int largest(int seen) const {
         typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
         u16x2 most = {0, 0};
 #pragma unroll
@@ -261,14 +264,48 @@ struct Values {
 #pragma unroll
             for (int i = 0; i < 2 * NB; ++i) {
                 uint32_t v = d[h][i] & 0x7FFF7FFFu;
-                if (masked) {
+                if constexpr (MASKED) {
                     const int x = 4 * h + 2 * i / NB, y = 4 * h + (2 * i + 1) / NB;
-                    if (x == y) v = seen[x] ? v : 0u;
-                    else v = (seen[x] ? v & 0xFFFFu : 0u) | (seen[y] ? v & 0xFFFF0000u : 0u);
+                    if (x == y) v = seen >> x & 1 ? v : 0u;
+                    else v = (seen >> x & 1 ? v & 0xFFFFu : 0u) | (seen >> y & 1 ? v & 0xFFFF0000u : 0u);
                 }
                 most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2, v));
             }
         return max((int)most.x, (int)most.y);
+    }
+    // Scales that are not finite: whether there are any, the blocks (bits) where a position seen has one, and without them.
+    __device__ __forceinline__ bool any_odd() const {
+        bool odd = false;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 2 * NB; ++i) odd |= not_finite(d[h][i]) || not_finite(d[h][i] >> 16);
+        return odd;
+    }
+    __device__ __forceinline__ int odd_blocks(int seen) const {
+        int blocks = 0;
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+                blocks |= seen >> x & 1 && not_finite(__builtin_bit_cast(uint16_t, scale(x, b))) ? 1 << b : 0;
+        return blocks;
+    }
+    // The scales as they are loaded, two a register, also past a branch that may change them.
+    __device__ __forceinline__ void keep_words() {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 2 * NB; ++i) asm("" : "+v"(d[h][i]));
+    }
+    __device__ __forceinline__ void drop_odd() {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 2 * NB; ++i) {
+                const uint32_t v = d[h][i];
+                d[h][i] = (not_finite(v) ? 0u : v & 0xFFFFu) | (not_finite(v >> 16) ? 0u : v & 0xFFFF0000u);
+            }
     }
     // Biased bytes; of iq4_nl the levels, where two half dwords of neighbouring positions share a lookup.
     struct Ready {
@@ -309,10 +346,19 @@ struct Values {
     __device__ static __forceinline__ int dim(int t, int m) { return TYPE == kKvF16 ? 2 * NB * m + t : 16 * t + m; }
 };
 
+// Constants that the compiler does not see through: a product and sum with them stays one v_fma_mix_f32, which
+// takes binary16 factors as they are; a plain difference or product would convert them first.
+struct Mix {
+    float minus, zero;
+    __device__ __forceinline__ Mix() : minus(-1.0f), zero(0.0f) { asm("" : "+s"(minus), "+s"(zero)); }
+    __device__ __forceinline__ float product(float x, _Float16 h) const { return __builtin_fmaf((float)h, x, zero); }
+    __device__ __forceinline__ float rest(float x, _Float16 h) const { return __builtin_fmaf((float)h, minus, x); }
+};
+
 // Two binary16 parts of pairs of values: the nearest, and the nearest of what is left.
-__device__ __forceinline__ void two_parts(float x, float y, uint32_t& hi, uint32_t& lo) {
+__device__ __forceinline__ void two_parts(const Mix& mix, float x, float y, uint32_t& hi, uint32_t& lo) {
     const half2_t h = __builtin_convertvector((float2_t{x, y}), half2_t);
-    const float2_t rest = {__builtin_fmaf((float)h.x, -1.0f, x), __builtin_fmaf((float)h.y, -1.0f, y)};
+    const float2_t rest = {mix.rest(x, h.x), mix.rest(y, h.y)};
     hi = __builtin_bit_cast(uint32_t, h);
     lo = __builtin_bit_cast(uint32_t, __builtin_convertvector(rest, half2_t));
 }
@@ -335,12 +381,17 @@ __device__ __forceinline__ float rows_sum(float v) {
     return __builtin_bit_cast(float, (int)r[0]) + __builtin_bit_cast(float, (int)r[1]);
 }
 
-__device__ __forceinline__ bool not_finite(uint32_t half) { return (half & 0x7C00u) == 0x7C00u; }
-
 // Orders LDS accesses of the lanes of a wave, which run in step.
 __device__ __forceinline__ void wave_fence() {
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
+}
+
+__device__ __forceinline__ int rows_or(int v) {
+    auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    v = (int)r[0] | (int)r[1];
+    r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return (int)r[0] | (int)r[1];
 }
 
 // 2^e for e in [-126, 127]
@@ -410,6 +461,7 @@ __global__ __launch_bounds__(64 * kAtWaves, 2) void attend_kernel(AttendArgs a) 
     s1 = min(s1, (hi_max - w.base + kAtStep - 1) / kAtStep);  // (hi_max below 0: none)
     const int ksteps = s1 > s0 + wave ? (s1 - s0 - wave + kAtWaves - 1) / kAtWaves : 0;
     const int start = w.base + kAtStep * (s0 + wave);
+    const Mix mix;
     const int64_t kchunk = (int64_t)head * a.p.page_size * Side<KT, NB>::kRow, vchunk = (int64_t)head * a.p.page_size * Side<VT, NB>::kRow;
     int pages = 0, places = 0;  // lane 2 i + half: the page of step i (of 32) and the place in it
     const auto read_pages = [&](int k) {
@@ -474,7 +526,7 @@ __global__ __launch_bounds__(64 * kAtWaves, 2) void attend_kernel(AttendArgs a) 
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
             uint32_t hi, lo;
-            two_parts(v[b][0] * up, v[b][1] * up, hi, lo);
+            two_parts(mix, v[b][0] * up, v[b][1] * up, hi, lo);
             lq[x][b][0][16 * (j / 4) + r % 16][j % 4] = hi;
             lq[x][b][1][16 * (j / 4) + r % 16][j % 4] = lo;
         }
@@ -561,23 +613,23 @@ __global__ __launch_bounds__(64 * kAtWaves, 2) void attend_kernel(AttendArgs a) 
             if ((k & 31) == 31) read_pages(k + 1);
             load_keys(k + 1);
         }
-        // Positions that some row of the tile does not see: their scores go, whatever they are.
+        // Positions that some row of the tile does not see: their scores go, whatever they are.  (The empty asm keeps
+        // this a branch that steps in the middle of a cache skip.)
         const bool masked = j0 < lo_max || j0 + kAtStep > hi_min || !exist[0] || !exist[1];
-        bool seen[RT][8];
+        int seen[RT], most[RT];  // bit i of seen: position i of z
         if (masked) {
+            asm volatile("");
 #pragma unroll
-            for (int x = 0; x < RT; ++x)
+            for (int x = 0; x < RT; ++x) {
+                seen[x] = 0;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int j = j0 + 16 * (i >> 2) + 4 * g + (i & 3);
-                    seen[x][i] = exist[i >> 2] && j >= rlo[x] && j < rhi[x];
-                    z[x][i] = seen[x][i] ? z[x][i] : -INFINITY;
+                    const bool in = exist[i >> 2] && j >= rlo[x] && j < rhi[x];
+                    seen[x] |= in ? 1 << i : 0;
+                    z[x][i] = in ? z[x][i] : -INFINITY;
                 }
-        } else {
-#pragma unroll
-            for (int x = 0; x < RT; ++x)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) seen[x][i] = true;
+            }
         }
         float top[RT];
         bool grew = false;
@@ -612,12 +664,30 @@ __global__ __launch_bounds__(64 * kAtWaves, 2) void attend_kernel(AttendArgs a) 
         }
         if constexpr (kValBlocks) {
             bool above = false;
-            int most[RT];
+            vals.keep_words();
+            if (masked) {
+                asm volatile("");
 #pragma unroll
-            for (int x = 0; x < RT; ++x) {
-                most[x] = vals.largest(seen[x], masked);
-                above |= most[x] >= bound[x];
+                for (int x = 0; x < RT; ++x) most[x] = vals.template largest<true>(seen[x]);
+                // A scale that is not finite must not meet the weight 0 of a row that does not see it: it is left
+                // out, and makes its block NaN in the rows that do.
+                if (__any(vals.any_odd())) {
+#pragma unroll
+                    for (int x = 0; x < RT; ++x) {
+                        const int blocks = rows_or(vals.odd_blocks(seen[x]));
+#pragma unroll
+                        for (int t = 0; t < kTiles; ++t)
+                            if (blocks >> (t / 2) & 1) o[x][t] = float4_t{NAN, NAN, NAN, NAN};
+                    }
+                    vals.drop_odd();
+                }
+            } else {
+#pragma unroll
+                for (int x = 0; x < RT; ++x) most[x] = x ? most[0] : vals.template largest<false>(0);
             }
+            vals.keep_words();
+#pragma unroll
+            for (int x = 0; x < RT; ++x) above |= most[x] >= bound[x];
             if (__any(above)) {
 #pragma unroll
                 for (int x = 0; x < RT; ++x) {
@@ -632,6 +702,7 @@ __global__ __launch_bounds__(64 * kAtWaves, 2) void attend_kernel(AttendArgs a) 
                 }
             }
         } else if (masked) {
+            asm volatile("");
             // Places that no row sees count as zeros.  Infinities and NaN that some rows see and others do not
             // must not meet the others' zeros in the products: they are added one position at a time, and left out there.
             bool odd = false;
@@ -651,7 +722,7 @@ __global__ __launch_bounds__(64 * kAtWaves, 2) void attend_kernel(AttendArgs a) 
 #pragma unroll
                 for (int x = 0; x < RT; ++x)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) weight[(16 * x + n) * kAtStep + 16 * (i >> 2) + 4 * g + (i & 3)] = seen[x][i] ? z[x][i] : -1.0f;
+                    for (int i = 0; i < 8; ++i) weight[(16 * x + n) * kAtStep + 16 * (i >> 2) + 4 * g + (i & 3)] = seen[x] >> i & 1 ? z[x][i] : -1.0f;
                 for (int u = 0; u < kAtStep; ++u) {
                     if (g == u / 4 % 4) {
 #pragma unroll
@@ -683,6 +754,12 @@ __global__ __launch_bounds__(64 * kAtWaves, 2) void attend_kernel(AttendArgs a) 
                     }
             }
         }
+        if constexpr (kValBlocks) {
+#pragma unroll
+            for (int x = 0; x < RT; ++x)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) z[x][i] *= fold[x];
+        }
         // The sums of values.
         typename Values<VT, NB>::Ready ready;
         vals.ready(ready);
@@ -700,12 +777,9 @@ __global__ __launch_bounds__(64 * kAtWaves, 2) void attend_kernel(AttendArgs a) 
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             u[e] = z[x][2 * i + e];
-                            if constexpr (kValBlocks) {
-                                u[e] = u[e] * fold[x] * vals.scale(2 * i + e, t / 2);
-                                if (masked) u[e] = seen[x][2 * i + e] ? u[e] : 0.0f;
-                            }
+                            if constexpr (kValBlocks) u[e] = mix.product(u[e], vals.scale(2 * i + e, t / 2));
                         }
-                        two_parts(u[0], u[1], hi[i], lo[i]);
+                        two_parts(mix, u[0], u[1], hi[i], lo[i]);
                     }
                     ph[x] = as_half8(hi[0], hi[1], hi[2], hi[3]);
                     pl[x] = as_half8(lo[0], lo[1], lo[2], lo[3]);
