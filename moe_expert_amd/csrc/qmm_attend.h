@@ -17,6 +17,8 @@
 // part keeps 2^-24 2^-14 of it.  One part alone would cost 2^-11, the error of a binary16 output.
 #pragma once
 
+#include <type_traits>
+
 #include "qmm_kv.h"
 
 namespace qmm {
@@ -25,7 +27,7 @@ typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
 typedef float float2_t __attribute__((ext_vector_type(2)));
 typedef float float4_t __attribute__((ext_vector_type(4)));
 
-constexpr int kAtWaves = 4;      // waves of a workgroup, which take turns at the steps of a part
+constexpr int kAtLds = 80 * 1024 - 512;  // bytes of LDS of a workgroup of which two share a CU
 constexpr int kAtStep = 32;      // positions a step
 constexpr int kAtInline = 256;   // sequences that a workgroup plans by itself; beyond, a launch of its own
 
@@ -75,17 +77,26 @@ __device__ __forceinline__ SeqWork lane_work(const AttendArgs& a, int s, int row
     return s < a.p.nseq ? seq_work(a, s, rows) : SeqWork{0, 0, 0, 0, 0, 0, 0};
 }
 
-// Steps of a part: the whole work over the target, at least `least`.
-__device__ __forceinline__ int part_steps(const AttendArgs& a, int64_t work) {
-    const int64_t c = (work + a.target - 1) / a.target;
-    return (int)min(max(c, (int64_t)a.least), (int64_t)1 << 28);
+// Steps of the longest part.  c0, the whole work over the target, where that makes no more parts than the target:
+// all run at once and are nearly equal.  Otherwise parts wait for others, and their length is what balances the time
+// that a part costs beside its steps (kAtCost steps of it, on all its waves) and the wait for the last one: with
+// c0 steps a place, (kAtCost / c) c0 + c is least at sqrt(kAtCost c0).  No more than kAtRounds targets of parts.
+constexpr int kAtCost = 12, kAtRounds = 3;
+__device__ __forceinline__ int clamp_steps(const AttendArgs& a, int64_t c) { return (int)min(max(c, (int64_t)a.least), (int64_t)1 << 28); }
+template <class F>
+__device__ __forceinline__ int part_steps(const AttendArgs& a, int64_t work, F split) {
+    const int64_t c0 = (work + a.target - 1) / a.target;
+    const int c = clamp_steps(a, c0);
+    if (split(c) <= a.target) return c;
+    return clamp_steps(a, max((int64_t)sqrtf((float)(kAtCost * c0)), (c0 + kAtRounds - 1) / kAtRounds));
 }
 
 __device__ __forceinline__ int parts_of(const SeqWork& w, int c) { return w.n > 0 ? max(1, (w.steps + c - 1) / c) : 0; }
 
 struct Item {
     SeqWork w;
-    int tile, part, parts, c;
+    int tile, part, parts;
+    int c;     // steps of a part: the sequence's in equal pieces
     int slot;  // of its tile's part 0, where there are several parts
 };
 
@@ -96,7 +107,6 @@ __device__ __forceinline__ bool find_item(const AttendArgs& a, int i, int rows, 
     if (a.plan) {
         // c, then for each sequence the items before it, and all of them; the same of the slots
         const int32_t *items = a.plan + 1, *slots = items + nseq + 1;
-        it.c = a.plan[0];
         if (i >= items[nseq]) return false;
         const int stride = (nseq + 63) / 64;
         int s = stride * __popcll(__ballot(items[min((lane + 1) * stride, nseq)] <= i));
@@ -105,7 +115,7 @@ __device__ __forceinline__ bool find_item(const AttendArgs& a, int i, int rows, 
         for (int j = s; j < end; j += 64) more += __popcll(__ballot(j + lane < end && items[min(j + lane + 1, nseq)] <= i));
         s = __builtin_amdgcn_readfirstlane(s + more);
         it.w = seq_work(a, s, rows);
-        it.parts = parts_of(it.w, it.c);
+        it.parts = parts_of(it.w, a.plan[0]);
         it.slot = slots[s];
         i -= items[s];
     } else {
@@ -116,12 +126,19 @@ __device__ __forceinline__ bool find_item(const AttendArgs& a, int i, int rows, 
             const int64_t mine = (int64_t)w.steps * w.tiles;  // below 2^49 in all: two sums that fit 32 bits
             work += ((int64_t)wave_total((int)(mine >> 24)) << 24) + wave_total((int)(mine & 0xFFFFFF));
         }
-        it.c = part_steps(a, work);
+        const int c = part_steps(a, work, [&](int c) {
+            int all = 0;
+            for (int j = 0; j < nseq; j += 64) {
+                if (nseq > 64) w = lane_work(a, j + lane, rows);
+                all += wave_total(w.tiles * parts_of(w, c));
+            }
+            return all;
+        });
         int before = 0, slots = 0;
         bool found = false;
         for (int j = 0; j < nseq && !found; j += 64) {
             if (nseq > 64) w = lane_work(a, j + lane, rows);
-            const int parts = parts_of(w, it.c), mine = parts * w.tiles, slot = parts > 1 ? mine : 0;
+            const int parts = parts_of(w, c), mine = parts * w.tiles, slot = parts > 1 ? mine : 0;
             const int upto = wave_scan(mine), sl = wave_scan(slot), total = lane_of(upto, 63);
             if (i < before + total) {
                 const int s = __popcll(__ballot(before + upto <= i));
@@ -144,6 +161,7 @@ __device__ __forceinline__ bool find_item(const AttendArgs& a, int i, int rows, 
     }
     it.tile = i / it.parts;
     it.part = i - it.tile * it.parts;
+    it.c = (it.w.steps + it.parts - 1) / it.parts;
     it.slot += it.tile * it.parts;
     return true;
 }
@@ -156,6 +174,113 @@ struct Side {
     static constexpr int kScale = TYPE == kKvF16 ? 0 : 2 * NB;
     static constexpr int kRow = kFactor + kScale;
 };
+
+// ------------------------------------------------------------------ blocks on their way through LDS
+
+// Lane l's 16 bytes at base + offset + IMM to lds + IMM + 16 l (lds and base are the wave's).  Not the builtin: behind that
+// the compiler waits for every load on its way before any read of LDS.  Its own counts stay safe: it waits for more
+// than it means to.
+template <int IMM>
+__device__ __forceinline__ void to_lds(char* lds, const char* base, uint32_t offset) {
+    static_assert(IMM >= 0 && IMM < 4096, "the instruction's offset");
+    const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2 offset:%3" : : "s"(at), "v"(offset), "s"(base), "n"(IMM) : "memory", "m0");
+}
+
+// 32 positions of a block format, as they lie in a page: the factors of both 16-position halves, then their scales,
+// copied by the wave itself 16 bytes a lane without passing registers, so that whole steps are on their way
+// while one is worked on.  A piece of 16 bytes keeps its row and goes, where a row is a power of two of them, to
+// place c ^ turn(row): sixteen lanes that read the same piece of as many rows meet different banks.
+template <int TYPE, int NB>
+struct Stage {
+    static constexpr int kFactor = Side<TYPE, NB>::kFactor, kRowPieces = kFactor / 16;
+    static constexpr int kHalf = kFactor;  // pieces of 16 rows
+    static constexpr int kHalfLoads = (kHalf + 63) / 64, kLoads = 2 * (kHalfLoads + 1);
+    static constexpr int kScales = 32 * kHalf;  // their place
+    static constexpr int kBytes = kScales + 64 * NB;
+    static constexpr bool kTurn = (kRowPieces & (kRowPieces - 1)) == 0;
+    // Loads of a lane whose offsets differ by more than the instruction's: 64 pieces on, the turn of the row is the
+    // same but for rows of 16 pieces.
+    static constexpr int kOffsets = kRowPieces == 16 ? 2 : 1;
+
+    __device__ static __forceinline__ int turn(int row) {
+        return !kTurn ? 0 : kRowPieces >= 8 ? row & 7 : row / (8 / kRowPieces) & (kRowPieces - 1);
+    }
+    // Where byte `at` of row `row` (of 32) lies.
+    __device__ static __forceinline__ int place(int row, int at) { return (row * kRowPieces + (at / 16 ^ turn(row))) * 16 + at % 16; }
+
+    uint32_t offset[kOffsets];
+    __device__ __forceinline__ Stage() {
+#pragma unroll
+        for (int i = 0; i < kOffsets; ++i) {
+            const int p = 64 * i + (threadIdx.x & 63), row = p / kRowPieces;
+            offset[i] = row * kFactor + 16 * (p % kRowPieces ^ turn(row));
+        }
+    }
+    // One half: 16 positions from `first` on of a chunk.
+    __device__ __forceinline__ void fetch(char* lds, int h, const char* chunk, int first, int page_size) const {
+        fetch_rows<0>(lds + 16 * kHalf * h, chunk + first * kFactor);
+        const int lane = threadIdx.x & 63;
+        if (lane < 2 * NB) to_lds<0>(lds + kScales + 32 * NB * h, chunk + (int64_t)page_size * kFactor + first * (2 * NB), 16 * lane);
+    }
+    template <int I>
+    __device__ __forceinline__ void fetch_rows(char* lds, const char* rows) const {
+        if constexpr (I < kHalfLoads) {
+            constexpr int kBase = I % kOffsets, kImm = 1024 * (I - kBase);
+            if (kHalf >= 64 * I + 64 || (int)(threadIdx.x & 63) < kHalf - 64 * I) to_lds<kImm>(lds + 1024 * kBase, rows, offset[kBase]);
+            fetch_rows<I + 1>(lds, rows);
+        }
+    }
+    // N bytes of a row from `at` on; N divides 16 or is a multiple of it where rows are turned.
+    template <int N>
+    __device__ static __forceinline__ void read(uint32_t* w, const char* lds, int row, int at) {
+        if constexpr (!kTurn) {
+            if constexpr (N % 4) w[N / 4] = 0;
+            constexpr int kAlign = N % 16 == 0 ? 16 : N % 8 == 0 ? 8 : N % 4 == 0 ? 4 : N % 2 == 0 ? 2 : 1;
+            __builtin_memcpy(w, __builtin_assume_aligned(lds + row * kFactor + at, kAlign), N);
+        } else if constexpr (N >= 16) {
+#pragma unroll
+            for (int i = 0; i < N / 16; ++i) __builtin_memcpy(w + 4 * i, __builtin_assume_aligned(lds + place(row, at + 16 * i), 16), 16);
+        } else {
+            if constexpr (N % 4) w[N / 4] = 0;
+            __builtin_memcpy(w, __builtin_assume_aligned(lds + place(row, at), N), N);
+        }
+    }
+    // The scales of positions 4g .. 4g+3 of a half.
+    __device__ static __forceinline__ void scales(uint32_t* d, const char* lds, int h, int g) {
+        __builtin_memcpy(d, __builtin_assume_aligned(lds + kScales + (32 * h + 8 * g) * NB, 8), 8 * NB);
+    }
+    // The binary16 bits of the largest magnitude among the scales of positions 4g .. 4g+3 that a lane's place n
+    // among 16 falls to.
+    __device__ static __forceinline__ int largest_part(const char* lds, int n, int g) {
+        uint32_t most = 0;
+#pragma unroll
+        for (int i = 0; i < (4 * NB + 15) / 16; ++i) {
+            const int j = min(n + 16 * i, 4 * NB - 1);
+            const uint32_t v = *(const uint32_t*)(lds + kScales + (32 * (j / (2 * NB)) + 8 * g) * NB + 4 * (j % (2 * NB))) & 0x7FFF7FFFu;
+            most = max(most, max(v >> 16, v & 0xFFFFu));
+        }
+        return (int)most;
+    }
+};
+
+// At most n vector memory operations of the wave outstanding; what is read from LDS afterwards is what the others
+// brought there.
+template <int N>
+__device__ __forceinline__ void arrived() {
+    static_assert(N < 64, "six bits");
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4) << 14 | 0x0F70);
+    asm volatile("" ::: "memory");
+}
+// What this wave reads from LDS is in its registers, so the place may be written.
+__device__ __forceinline__ void taken() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xC07F);
+    asm volatile("" ::: "memory");
+}
+
+// ------------------------------------------------------------------ operands
 
 // N bytes from an address of any alignment, the last dword filled up with zeros.
 template <int N>
@@ -197,6 +322,11 @@ struct Keys {
             load_bytes<kBytes>(w, chunk + (uint32_t)((place + n) * Side<TYPE, NB>::kFactor + g * kBytes));
             load_bytes<8 * NB>(d, chunk + (uint32_t)(page_size * Side<TYPE, NB>::kFactor + (place + 4 * g) * (2 * NB)));
         }
+    }
+    __device__ __forceinline__ void read(int h, const char* lds) {
+        const int n = threadIdx.x & 15, g = threadIdx.x >> 4 & 3;
+        Stage<TYPE, NB>::template read<kBytes>(w, lds, 16 * h + n, g * kBytes);
+        Stage<TYPE, NB>::scales(d, lds, h, g);
     }
     // Biases the bytes of q8_0, looks the levels of iq4_nl up.
     struct Ready {
@@ -249,6 +379,15 @@ struct Values {
         for (int r = 0; r < 4; ++r) load_bytes<kBytes>(w[4 * half + r], p + r * Side<TYPE, NB>::kFactor);
         if constexpr (TYPE != kKvF16)
             load_bytes<8 * NB>(d[half], chunk + (uint32_t)(page_size * Side<TYPE, NB>::kFactor + (place + 4 * g) * (2 * NB)));
+    }
+    __device__ __forceinline__ void read(const char* lds) {
+        const int n = threadIdx.x & 15, g = threadIdx.x >> 4 & 3;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) Stage<TYPE, NB>::template read<kBytes>(w[4 * h + r], lds, 16 * h + 4 * g + r, n * kBytes);
+            Stage<TYPE, NB>::scales(d[h], lds, h, g);
+        }
     }
     __device__ __forceinline__ _Float16 scale(int x, int b) const {
         const int i = (x & 3) * NB + b;
@@ -428,19 +567,42 @@ __host__ __device__ constexpr int64_t part_floats(int rows, int dim) { return (i
 
 // ------------------------------------------------------------------ the pass
 
-// Resources: the queries' parts lie in LDS, read again each step (two 16-byte reads a block), which leaves the
-// registers to the keys and values in flight.
+struct Nothing {};
+
+// How a pair of formats, a width and a number of row tiles are run: waves of a workgroup, whether keys and values pass
+// through LDS on their way (block formats do, if the keys are one), and how many steps ahead they set out.
 template <int KT, int VT, int NB, int RT>
-__global__ __launch_bounds__(64 * kAtWaves, 2) void attend_kernel(AttendArgs a) {
-    constexpr int kRows = 16 * RT, kDim = 32 * NB, kTiles = 2 * NB;
-    constexpr bool kKeyBlocks = KT != kKvF16, kValBlocks = VT != kKvF16;
-    // The next keys are read before the weights, or after the values where the registers do not hold both.
+struct Shape {
+    static constexpr bool kStaged = KT != kKvF16;
+    static constexpr int kKeys = kStaged ? Stage<KT, NB>::kBytes : 0, kVals = kStaged ? Stage<VT, NB>::kBytes : 0;
+    static constexpr int kQueries = RT * NB * 2 * 64 * 16;
+    static constexpr int kWaves = kQueries + 4 * (kKeys + kVals) > kAtLds ? 8 : 4;
+    static constexpr int kDepth = kStaged && kWaves == 4 && kQueries + 8 * (kKeys + kVals) <= kAtLds ? 2 : 1;
+    static constexpr int kRing = kDepth * (kKeys + kVals);  // bytes a wave
+    static constexpr int kRows = 16 * RT, kPitch = 32 * NB + 4;
+    static constexpr int kSums = kWaves / 2 * kRows * (kPitch + 2) * 4;  // of half the waves, at the end
+    static constexpr int kBytes = kQueries + (kWaves * kRing > kSums ? kWaves * kRing : kSums);
+};
+
+// Resources: the queries' parts lie in LDS, read again each step (two 16-byte reads a block), which leaves the
+// registers to the keys and values.
+template <int KT, int VT, int NB, int RT>
+__global__ __launch_bounds__((64 * Shape<KT, VT, NB, RT>::kWaves), 2) void attend_kernel(AttendArgs a) {
+    using S = Shape<KT, VT, NB, RT>;
+    constexpr int kRows = 16 * RT, kDim = 32 * NB, kTiles = 2 * NB, kWaves = S::kWaves, kDepth = S::kDepth;
+    constexpr bool kKeyBlocks = KT != kKvF16, kValBlocks = VT != kKvF16, kStaged = S::kStaged;
+    // Binary16 keys are read into registers, a step ahead: before the weights, or after the values where the registers
+    // do not hold both.
     constexpr bool kEarly = NB < 8;
-    // The sums of two waves at a time, at the end; until then a quarter is a wave's own for odd values.
-    __shared__ __attribute__((aligned(16))) float so[2][kRows][kDim + 4];
-    __shared__ float lm[2][kRows], ll[2][kRows], lc[kRows];
-    static_assert(sizeof(so) / kAtWaves >= kRows * kAtStep * 4 + kDim * 2, "weights and a position's values");
-    __shared__ __attribute__((aligned(16))) uint32_t lq[RT][NB][2][64][4];
+    // Queries, then what is on its way, wave by wave; at the end the sums of half the waves, and of binary16 values a
+    // place a wave for odd ones until then.
+    __shared__ __attribute__((aligned(16))) char lds[S::kBytes];
+    __shared__ float lc[kRows];
+    auto& lq = *(uint32_t(*)[RT][NB][2][64][4])lds;
+    auto& so = *(float(*)[kWaves / 2][kRows][S::kPitch])(lds + S::kQueries);
+    auto& lm = *(float(*)[kWaves / 2][kRows])(lds + S::kQueries + sizeof(so));
+    auto& ll = *(float(*)[kWaves / 2][kRows])(lds + S::kQueries + sizeof(so) + sizeof(lm));
+    static_assert(kValBlocks || S::kSums / kWaves >= kRows * kAtStep * 4 + kDim * 2, "weights and a position's values");
     const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int head = (int)(blockIdx.x % (uint32_t)a.p.nheads);
@@ -451,69 +613,109 @@ __global__ __launch_bounds__(64 * kAtWaves, 2) void attend_kernel(AttendArgs a) 
     // The rows of the tile: lane n's, the positions [rlo, rhi) that they see, and the same over all of them.
     const int row0 = it.tile * kRows, rows = min(kRows, w.n * a.group - row0), cap = a.p.max_pages * a.p.page_size;
     const auto low = [&](int pos) { return a.window > 0 && pos >= a.window ? pos - a.window + 1 : 0; };
-    const int tok0 = row0 / a.group, tok1 = (row0 + rows - 1) / a.group;
-    const int pos0 = w.len - w.n + tok0, pos1 = w.len - w.n + tok1;
+    const int pos0 = w.len - w.n + row0 / a.group, pos1 = w.len - w.n + (row0 + rows - 1) / a.group;
     const int lo_min = low(pos0), lo_max = low(pos1), hi_min = min(pos0 + 1, cap), hi_max = min(pos1 + 1, cap);
+
+    // The queries, 16 threads a row: read before the keys set out, since loads return in order; then scaled, their two
+    // parts laid out as the operand that a lane reads.  Thread j holds the dims 32b + j and 32b + 16 + j (element 2m
+    // + i of a block format's operand is dim 32b + 16i + 4g + m) or 32b + 2j and the next (binary16: element e is
+    // 32b + 8g + e).
+    uint32_t raw[RT][NB][2];
+#pragma unroll
+    for (int x = 0; x < RT; ++x) {
+        const int r = min(16 * x + (int)threadIdx.x / 16, rows - 1), j = threadIdx.x & 15, tok = (row0 + r) / a.group;
+        const int64_t at = (w.first + tok) * a.ldq + (int64_t)(head * a.group + row0 + r - tok * a.group) * kDim;
+        if (a.qtype == kF32) {
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) raw[x][b][i] = ((const uint32_t*)a.q)[at + 32 * b + (kKeyBlocks ? 16 * i + j : 2 * j + i)];
+        } else {
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) raw[x][b][i] = ((const uint16_t*)a.q)[at + 32 * b + (kKeyBlocks ? 16 * i + j : 2 * j + i)];
+        }
+    }
 
     // This wave's steps of the part, those that the tile sees.
     int s0 = it.part * it.c, s1 = min(s0 + it.c, w.steps);
     s0 = max(s0, (lo_min - w.base) / kAtStep);
     s1 = min(s1, (hi_max - w.base + kAtStep - 1) / kAtStep);  // (hi_max below 0: none)
-    const int ksteps = s1 > s0 + wave ? (s1 - s0 - wave + kAtWaves - 1) / kAtWaves : 0;
+    const int ksteps = s1 > s0 + wave ? (s1 - s0 - wave + kWaves - 1) / kWaves : 0;
     const int start = w.base + kAtStep * (s0 + wave);
     const Mix mix;
-    const int64_t kchunk = (int64_t)head * a.p.page_size * Side<KT, NB>::kRow, vchunk = (int64_t)head * a.p.page_size * Side<VT, NB>::kRow;
-    int pages = 0, places = 0;  // lane 2 i + half: the page of step i (of 32) and the place in it
-    const auto read_pages = [&](int k) {
-        const int pos = start + kAtStep * kAtWaves * (k + (lane >> 1)) + 16 * (lane & 1);
-        const bool in = k + (lane >> 1) < ksteps;
-        pages = in ? kv_page(a.p, w.seq, pos) : -1;
-        places = in ? (int)((uint32_t)pos % (uint32_t)a.p.page_size) : 0;
+    const char* const kbase = a.k.base + (int64_t)head * a.p.page_size * Side<KT, NB>::kRow;
+    const char* const vbase = a.v.base + (int64_t)head * a.p.page_size * Side<VT, NB>::kRow;
+    // Lane 2 i + half: the page of step run + i, and the place in it.  A run of 32 steps is read anew after 30, before
+    // the steps that set out then.
+    int pages = -1, places = 0, run = 0;
+    uint64_t missing = 0;
+    const auto read_pages = [&](int from) {
+        const int k = from + (lane >> 1), pos = start + kAtStep * kWaves * k + 16 * (lane & 1);
+        run = from;
+        pages = k < ksteps ? kv_page(a.p, w.seq, pos) : -1;
+        places = k < ksteps ? (int)((uint32_t)pos % (uint32_t)a.p.page_size) : 0;
+        missing = __ballot(pages < 0);
     };
+    const auto page_of = [&](int k, int h) { return lane_of(pages, 2 * (k - run) + h); };
+    const auto place_of = [&](int k, int h) { return lane_of(places, 2 * (k - run) + h); };
     // A position that does not exist is read at page 0 and not seen.
+    const auto chunk_of = [&](const char* base, int64_t stride, int k, int h) {
+        const int pg = page_of(k, h);
+        return base + (pg < 0 ? 0 : pg * stride);
+    };
+    char* const ring = lds + S::kQueries + wave * S::kRing;
+    std::conditional_t<kStaged, Stage<KT, NB>, Nothing> kstage;
+    std::conditional_t<kStaged, Stage<VT, NB>, Nothing> vstage;
     Keys<KT, NB> keys[2];
-    const auto load_keys = [&](int k) {
+    const auto fetch_keys = [&](int k) {
+        const char* const chunk[2] = {chunk_of(kbase, a.k.stride, k, 0), chunk_of(kbase, a.k.stride, k, 1)};
+        const int first[2] = {place_of(k, 0), place_of(k, 1)};
+        if constexpr (kStaged) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int pg = lane_of(pages, 2 * (k & 31) + h);
-            keys[h].load(a.k.base + (pg < 0 ? 0 : pg * a.k.stride) + kchunk, lane_of(places, 2 * (k & 31) + h), a.p.page_size);
+            for (int h = 0; h < 2; ++h) kstage.fetch(ring + k % kDepth * S::kKeys, h, chunk[h], first[h], a.p.page_size);
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) keys[h].load(chunk[h], first[h], a.p.page_size);
         }
     };
+    const auto fetch_values = [&](int k, Values<VT, NB>& vals) {
+        const char* const chunk[2] = {chunk_of(vbase, a.v.stride, k, 0), chunk_of(vbase, a.v.stride, k, 1)};
+        const int first[2] = {place_of(k, 0), place_of(k, 1)};
+        if constexpr (kStaged) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) vstage.fetch(ring + kDepth * S::kKeys + k % kDepth * S::kVals, h, chunk[h], first[h], a.p.page_size);
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) vals.load(h, chunk[h], first[h], a.p.page_size);
+        }
+    };
+    Values<VT, NB> vals;
     if (ksteps > 0) {
         read_pages(0);
-        load_keys(0);
+        if constexpr (kStaged) arrived<0>();  // the queries too: a wait for them further on would wait for what sets out now
+        fetch_keys(0);
+        if constexpr (kStaged) {
+            fetch_values(0, vals);
+            if (kDepth > 1 && ksteps > 1) {
+                fetch_keys(1);
+                fetch_values(1, vals);
+            }
+        }
     }
 
-    // The queries, 16 threads a row: scaled, their two parts laid out as the operand that a lane reads.
-    // Thread j holds the dims 32b + j and 32b + 16 + j (element 2m + i of a block format's operand is dim 32b + 16i
-    // + 4g + m) or 32b + 2j and the next (binary16: element e is 32b + 8g + e).
 #pragma unroll
     for (int x = 0; x < RT; ++x) {
-        const int r = 16 * x + (int)threadIdx.x / 16, j = threadIdx.x & 15, tok = (row0 + r) / a.group;
-        const bool live = r < rows;
-        const int64_t at = live ? (w.first + tok) * a.ldq + (int64_t)(head * a.group + row0 + r - tok * a.group) * kDim : 0;
+        if (kWaves > 4 && wave >= 4) break;
+        const int r = 16 * x + (int)threadIdx.x / 16, j = threadIdx.x & 15;
         float v[NB][2], most = 0.0f;
-        if (a.qtype == kF32) {
-#pragma unroll
-            for (int b = 0; b < NB; ++b)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) v[b][i] = ((const float*)a.q)[at + 32 * b + (kKeyBlocks ? 16 * i + j : 2 * j + i)];
-        } else {
-            uint32_t raw[NB][2];
-#pragma unroll
-            for (int b = 0; b < NB; ++b)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) raw[b][i] = ((const uint16_t*)a.q)[at + 32 * b + (kKeyBlocks ? 16 * i + j : 2 * j + i)];
-#pragma unroll
-            for (int b = 0; b < NB; ++b)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) v[b][i] = a.qtype == kBin16 ? h2f(raw[b][i]) : bf2f(raw[b][i]);
-        }
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                v[b][i] = live ? v[b][i] * a.scale : 0.0f;
+                const float f = a.qtype == kF32 ? __builtin_bit_cast(float, raw[x][b][i]) : a.qtype == kBin16 ? h2f(raw[x][b][i]) : bf2f(raw[x][b][i]);
+                v[b][i] = r < rows ? f * a.scale : 0.0f;
                 most = __builtin_fmaxf(most, __builtin_fabsf(v[b][i]));
             }
         most = __builtin_fmaxf(most, dpp<0xB1>(most));
@@ -554,16 +756,21 @@ __global__ __launch_bounds__(64 * kAtWaves, 2) void attend_kernel(AttendArgs a) 
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) o[x][t] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
     }
+    int least = 1;  // the least of the rows' bounds
     const auto queries = [&](int x, int b, int part) { return __builtin_bit_cast(half8_t, *(const u32x4*)lq[x][b][part][lane]); };
 
     for (int k = 0; k < ksteps; ++k) {
-        const int j0 = start + kAtStep * kAtWaves * k;
-        const bool exist[2] = {lane_of(pages, 2 * (k & 31)) >= 0, lane_of(pages, 2 * (k & 31) + 1) >= 0};
-        Values<VT, NB> vals;
+        const int j0 = start + kAtStep * kWaves * k;
+        if (k - run == 30) read_pages(k);
+        const bool exist[2] = {!(missing >> (2 * (k - run)) & 1), !(missing >> (2 * (k - run) + 1) & 1)};
+        if constexpr (kStaged) {
+            // Behind this step's keys: its values, and the keys and values of the steps that have set out since.
+            if (kDepth > 1 && k + 1 < ksteps) arrived<2 * Stage<VT, NB>::kLoads + Stage<KT, NB>::kLoads>();
+            else arrived<Stage<VT, NB>::kLoads>();
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int pg = lane_of(pages, 2 * (k & 31) + h);
-            vals.load(h, a.v.base + (pg < 0 ? 0 : pg * a.v.stride) + vchunk, lane_of(places, 2 * (k & 31) + h), a.p.page_size);
+            for (int h = 0; h < 2; ++h) keys[h].read(h, ring + k % kDepth * S::kKeys);
+        } else {
+            fetch_values(k, vals);
         }
         float z[RT][8];
         {
@@ -609,9 +816,11 @@ __global__ __launch_bounds__(64 * kAtWaves, 2) void attend_kernel(AttendArgs a) 
             }
         }
         __builtin_amdgcn_sched_barrier(0);
-        if (kEarly && k + 1 < ksteps) {
-            if ((k & 31) == 31) read_pages(k + 1);
-            load_keys(k + 1);
+        if constexpr (kStaged) {
+            taken();
+            if (k + kDepth < ksteps) fetch_keys(k + kDepth);
+        } else if (kEarly && k + 1 < ksteps) {
+            fetch_keys(k + 1);
         }
         // Positions that some row of the tile does not see: their scores go, whatever they are.  (The empty asm keeps
         // this a branch that steps in the middle of a cache skip.)
@@ -662,6 +871,14 @@ __global__ __launch_bounds__(64 * kAtWaves, 2) void attend_kernel(AttendArgs a) 
                 l[x] += z[x][i];
             }
         }
+        if constexpr (kStaged) {
+            // Behind this step's values: the keys and values that have set out since.
+            constexpr int kK = Stage<KT, NB>::kLoads, kV = Stage<VT, NB>::kLoads;
+            if (k + kDepth < ksteps) arrived<kDepth * kK + (kDepth - 1) * kV>();
+            else if (kDepth > 1 && k + 1 < ksteps) arrived<kK + kV>();
+            else arrived<0>();
+            vals.read(ring + kDepth * S::kKeys + k % kDepth * S::kVals);
+        }
         if constexpr (kValBlocks) {
             bool above = false;
             vals.keep_words();
@@ -681,14 +898,24 @@ __global__ __launch_bounds__(64 * kAtWaves, 2) void attend_kernel(AttendArgs a) 
                     }
                     vals.drop_odd();
                 }
+#pragma unroll
+                for (int x = 0; x < RT; ++x) above |= most[x] >= bound[x];
+            } else if constexpr (kStaged) {
+                // (the sixteen lanes with the same scales share them)
+                above = Stage<VT, NB>::largest_part(ring + kDepth * S::kKeys + k % kDepth * S::kVals, n, g) >= least;
             } else {
 #pragma unroll
                 for (int x = 0; x < RT; ++x) most[x] = x ? most[0] : vals.template largest<false>(0);
+#pragma unroll
+                for (int x = 0; x < RT; ++x) above |= most[x] >= bound[x];
             }
             vals.keep_words();
-#pragma unroll
-            for (int x = 0; x < RT; ++x) above |= most[x] >= bound[x];
             if (__any(above)) {
+                int now = 0x10000;
+                if (kStaged && !masked) {
+#pragma unroll
+                    for (int x = 0; x < RT; ++x) most[x] = x ? most[0] : vals.template largest<false>(0);
+                }
 #pragma unroll
                 for (int x = 0; x < RT; ++x) {
                     const float d = rows_max(__builtin_fabsf(h2f(min(most[x], 0x7C00))));  // (an infinity, NaN: 2^17)
@@ -699,7 +926,13 @@ __global__ __launch_bounds__(64 * kAtWaves, 2) void attend_kernel(AttendArgs a) 
                     bound[x] = to > 65536.0f ? 0x10000 : (int)f2h(to);
 #pragma unroll
                     for (int t = 0; t < kTiles; ++t) o[x][t] *= shrink;
+                    now = min(now, bound[x]);
                 }
+                now = min(now, dpp_i<0xB1>(now));
+                now = min(now, dpp_i<0x4E>(now));
+                now = min(now, dpp_i<0x141>(now));
+                now = min(now, dpp_i<0x140>(now));
+                least = __builtin_amdgcn_readfirstlane(now);
             }
         } else if (masked) {
             asm volatile("");
@@ -717,7 +950,7 @@ __global__ __launch_bounds__(64 * kAtWaves, 2) void attend_kernel(AttendArgs a) 
                 }
             }
             if (__any(odd)) {
-                float* weight = &so[0][0][0] + wave * (int)(sizeof(so) / 4 / kAtWaves);
+                float* weight = (float*)(lds + S::kQueries + wave * (S::kSums / kWaves / 16 * 16));
                 uint32_t* row = (uint32_t*)(weight + kRows * kAtStep);
 #pragma unroll
                 for (int x = 0; x < RT; ++x)
@@ -792,13 +1025,15 @@ __global__ __launch_bounds__(64 * kAtWaves, 2) void attend_kernel(AttendArgs a) 
                 o[x][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, ph[x], o[x][t], 0, 0, 0);
             }
         }
-        if (!kEarly && k + 1 < ksteps) {
-            if ((k & 31) == 31) read_pages(k + 1);
-            load_keys(k + 1);
+        if constexpr (kStaged) {
+            taken();
+            if (k + kDepth < ksteps) fetch_values(k + kDepth, vals);
+        } else if (!kEarly && k + 1 < ksteps) {
+            fetch_keys(k + 1);
         }
     }
 
-    // The waves' results, in base-2 units of the scores: two waves to the other two through LDS, then those.
+    // The waves' results, in base-2 units of the scores: half the waves to the other half through LDS, until two are left, then those.
 #pragma unroll
     for (int x = 0; x < RT; ++x) {
         l[x] = rows_sum(l[x]) * (kValBlocks ? 1.0f : power(-14));
@@ -820,10 +1055,12 @@ __global__ __launch_bounds__(64 * kAtWaves, 2) void attend_kernel(AttendArgs a) 
                 for (int r = 0; r < 4; ++r) so[at][16 * x + n][Values<VT, NB>::dim(t, 4 * g + r)] = o[x][t][r];
         }
     };
-    __syncthreads();
-    if (wave >= 2) put(wave - 2);
-    __syncthreads();
-    if (wave < 2) {
+#pragma unroll
+    for (int half = kWaves / 2; half >= 2; half /= 2) {
+        __syncthreads();
+        if (wave >= half && wave < 2 * half) put(wave - half);
+        __syncthreads();
+        if (wave >= half) continue;
 #pragma unroll
         for (int x = 0; x < RT; ++x) {
             const float other = lm[wave][16 * x + n], most = __builtin_fmaxf(m[x], other), mine = beside(m[x], most), its = beside(other, most);
@@ -834,13 +1071,14 @@ __global__ __launch_bounds__(64 * kAtWaves, 2) void attend_kernel(AttendArgs a) 
 #pragma unroll
                 for (int r = 0; r < 4; ++r) o[x][t][r] = o[x][t][r] * mine + so[wave][16 * x + n][Values<VT, NB>::dim(t, 4 * g + r)] * its;
         }
-        put(wave);
     }
+    __syncthreads();
+    if (wave < 2) put(wave);
     __syncthreads();
     const bool whole = it.parts == 1;
     if (!whole && (it.slot < 0 || it.slot + it.part >= a.slots)) return;  // offsets that decrease: no place for it
     float* part = a.parts + ((int64_t)(it.slot + it.part) * a.p.nheads + head) * part_floats(kRows, kDim);
-    for (int i = threadIdx.x; i < rows * (kDim / 4); i += 64 * kAtWaves) {
+    for (int i = threadIdx.x; i < rows * (kDim / 4); i += 64 * kWaves) {
         const int r = i / (kDim / 4), d = 4 * (i - r * (kDim / 4));
         const float most = __builtin_fmaxf(lm[0][r], lm[1][r]), e0 = beside(lm[0][r], most), e1 = beside(lm[1][r], most);
         const float sum = e0 * ll[0][r] + e1 * ll[1][r];
@@ -858,19 +1096,23 @@ __global__ __launch_bounds__(64 * kAtWaves, 2) void attend_kernel(AttendArgs a) 
     }
 }
 
+template <int KT, int VT, int NB, int RT>
+void attend_launch(const AttendArgs& a, unsigned grid, hipStream_t st) {
+    hipLaunchKernelGGL((attend_kernel<KT, VT, NB, RT>), dim3(grid), dim3(64 * Shape<KT, VT, NB, RT>::kWaves), 0, st, a);
+}
+
 // The launch of one pair of formats, instantiated in a source of its own per format of the keys.
 template <int KT, int VT>
 void attend_pair(const AttendArgs& a, unsigned grid, int rt, hipStream_t st) {
-    const dim3 block(64 * kAtWaves);
     switch (a.p.dim / 32 * 2 + rt) {
-        case 5: hipLaunchKernelGGL((attend_kernel<KT, VT, 2, 1>), dim3(grid), block, 0, st, a); break;
-        case 6: hipLaunchKernelGGL((attend_kernel<KT, VT, 2, 2>), dim3(grid), block, 0, st, a); break;
-        case 7: hipLaunchKernelGGL((attend_kernel<KT, VT, 3, 1>), dim3(grid), block, 0, st, a); break;
-        case 8: hipLaunchKernelGGL((attend_kernel<KT, VT, 3, 2>), dim3(grid), block, 0, st, a); break;
-        case 9: hipLaunchKernelGGL((attend_kernel<KT, VT, 4, 1>), dim3(grid), block, 0, st, a); break;
-        case 10: hipLaunchKernelGGL((attend_kernel<KT, VT, 4, 2>), dim3(grid), block, 0, st, a); break;
-        case 13: hipLaunchKernelGGL((attend_kernel<KT, VT, 6, 1>), dim3(grid), block, 0, st, a); break;
-        default: hipLaunchKernelGGL((attend_kernel<KT, VT, 8, 1>), dim3(grid), block, 0, st, a); break;
+        case 5: attend_launch<KT, VT, 2, 1>(a, grid, st); break;
+        case 6: attend_launch<KT, VT, 2, 2>(a, grid, st); break;
+        case 7: attend_launch<KT, VT, 3, 1>(a, grid, st); break;
+        case 8: attend_launch<KT, VT, 3, 2>(a, grid, st); break;
+        case 9: attend_launch<KT, VT, 4, 1>(a, grid, st); break;
+        case 10: attend_launch<KT, VT, 4, 2>(a, grid, st); break;
+        case 13: attend_launch<KT, VT, 6, 1>(a, grid, st); break;
+        default: attend_launch<KT, VT, 8, 1>(a, grid, st); break;
     }
 }
 void attend_f16(const AttendArgs& a, unsigned grid, int rt, hipStream_t st);

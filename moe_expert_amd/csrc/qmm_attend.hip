@@ -11,18 +11,15 @@ __global__ __launch_bounds__(1024) void attend_plan_kernel(AttendArgs a, int row
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, nseq = a.p.nseq;
     int64_t sum = 0;
     for (int s = threadIdx.x; s - lane < nseq; s += 1024) {
-        int64_t mine = 0;
-        if (s < nseq) {
-            const SeqWork w = seq_work(a, s, rows);
-            mine = (int64_t)w.steps * w.tiles;
-        }
+        const SeqWork w = lane_work(a, s, rows);
+        const int64_t mine = (int64_t)w.steps * w.tiles;
         sum += ((int64_t)wave_total((int)(mine >> 24)) << 24) + wave_total((int)(mine & 0xFFFFFF));
     }
     if (lane == 0) work[wave] = sum;
     __syncthreads();
     sum = 0;
     for (int i = 0; i < 16; ++i) sum += work[i];
-    const int c = part_steps(a, sum);
+    const int c = part_steps(a, sum, [&](int) { return a.target + 1; });
     int before = 0, sbefore = 0;
     for (int s0 = 0; s0 < nseq; s0 += 1024) {
         const int s = s0 + threadIdx.x;
@@ -116,7 +113,7 @@ using namespace qmm;
 
 namespace {
 
-constexpr int64_t kAtTarget = 1024;  // workgroups to split the caches over
+constexpr int64_t kAtTarget = 512;  // workgroups to split the caches over: two for every CU, what runs at once
 constexpr int kAtLeast = 8;          // steps of the shortest part
 
 struct AttendShape {
@@ -139,11 +136,11 @@ int attend_shape(AttendShape& s, const qmm_kv_cache* c, const int32_t* pages, in
     const bool wide = c->head_dim <= 128;  // two tiles of wider heads do not fit the registers
     s.rt = wide && nseq && group * ((ntok + nseq - 1) / nseq) > 16 ? 2 : 1;
     const int64_t rows = 16 * s.rt, tiles = std::min(nseq + ntok * group / rows, ntok * ((group + rows - 1) / rows));
-    s.target = (int)((kAtTarget + c->nheads - 1) / c->nheads);
+    s.target = (int)std::max(kAtTarget / c->nheads, (int64_t)1);
     s.least = kAtLeast;
     const int64_t steps = (max_pages * c->page_size + kAtStep - 1) / kAtStep + 1, most = (steps + s.least - 1) / s.least;
-    s.items = std::min(s.target + tiles, tiles * most);
-    s.slots = most > 1 ? std::min((int64_t)2 * s.target, tiles * most) : 0;
+    s.items = std::min(kAtRounds * s.target + tiles, tiles * most);
+    s.slots = most > 1 ? std::min((int64_t)2 * kAtRounds * s.target, tiles * most) : 0;
     if (s.items * c->nheads >= 1 << 24) return QMM_EUNSUPPORTED;  // below 2^32 threads
     // (sized for 32 rows where a call of other proportions would take them)
     s.plan = (size_t)(s.slots * c->nheads * part_floats(wide ? 32 : 16, c->head_dim) * 4 + 15) & ~(size_t)15;
