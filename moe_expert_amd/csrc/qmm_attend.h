@@ -35,7 +35,7 @@ struct AttendArgs {
     const void* q;
     void* out;
     float* lse;
-    float* parts;            // partial results: [slot][head][rows (m), rows (l), rows * dim]
+    float* parts;            // pieces: [slot][head][rows (m), rows (l), rows * dim]
     const int32_t* plan;     // of attend_plan_kernel, or null
     int64_t ldq, ldo;
     KvSide k, v;
@@ -43,7 +43,7 @@ struct AttendArgs {
     int nheads, group, qtype, otype;  // group: heads of queries a head of keys
     float scale;                      // times log2(e)
     int window;                       // 0: none
-    int target, least, slots;         // workgroups a head of keys to split the cache over, steps of the shortest part, places for parts
+    int target, least;                // workgroups a head of keys, steps that a tile counts for at least
     int vec;                          // out: groups of four values are aligned
 };
 
@@ -77,93 +77,147 @@ __device__ __forceinline__ SeqWork lane_work(const AttendArgs& a, int s, int row
     return s < a.p.nseq ? seq_work(a, s, rows) : SeqWork{0, 0, 0, 0, 0, 0, 0};
 }
 
-// Steps of the longest part.  c0, the whole work over the target, where that makes no more parts than the target:
-// all run at once and are nearly equal.  Otherwise parts wait for others, and their length is what balances the time
-// that a part costs beside its steps (kAtCost steps of it, on all its waves) and the wait for the last one: with
-// c0 steps a place, (kAtCost / c) c0 + c is least at sqrt(kAtCost c0).  No more than kAtRounds targets of parts.
-constexpr int kAtCost = 12, kAtRounds = 3;
-__device__ __forceinline__ int clamp_steps(const AttendArgs& a, int64_t c) { return (int)min(max(c, (int64_t)a.least), (int64_t)1 << 28); }
-template <class F>
-__device__ __forceinline__ int part_steps(const AttendArgs& a, int64_t work, F split) {
-    const int64_t c0 = (work + a.target - 1) / a.target;
-    const int c = clamp_steps(a, c0);
-    if (split(c) <= a.target) return c;
-    return clamp_steps(a, max((int64_t)sqrtf((float)(kAtCost * c0)), (c0 + kAtRounds - 1) / kAtRounds));
-}
-
-__device__ __forceinline__ int parts_of(const SeqWork& w, int c) { return w.n > 0 ? max(1, (w.steps + c - 1) / c) : 0; }
-
-struct Item {
-    SeqWork w;
-    int tile, part, parts;
-    int c;     // steps of a part: the sequence's in equal pieces
-    int slot;  // of its tile's part 0, where there are several parts
+// How a call is split.  Every tile of rows, sequence by sequence, takes its steps' place on a line, at least `least` of
+// them (about what a tile costs beside its steps), and each of the workgroups of a head takes the same length of it: the
+// pieces of tiles that lie there.  A tile that goes on beyond its workgroup's length is joined from its pieces;
+// since a workgroup has at most one piece of a tile that began before and one of a tile that goes on, two places a
+// workgroup hold all pieces.
+//
+// Where the pieces of a length c, every tile cut by itself, are no more than the workgroups, and c is not much longer
+// than the equal share of the steps, tiles take whole lengths: a workgroup has one piece then, and pays once for what
+// it does beside its steps (kAtCost steps of its time, about).
+constexpr int kAtCost = 12;
+struct Split {
+    int shift;      // a unit is 2^shift steps (0, but for lines of more than 2^30 steps)
+    int len, all;   // units of a workgroup, and all
+    bool whole;     // tiles take whole lengths
 };
 
-// Item i of the call's: every sequence's tiles of rows times its parts, in order.  False past the last.  Every
-// wave finds it by itself.
-__device__ __forceinline__ bool find_item(const AttendArgs& a, int i, int rows, Item& it) {
-    const int lane = threadIdx.x & 63, nseq = a.p.nseq;
-    if (a.plan) {
-        // c, then for each sequence the items before it, and all of them; the same of the slots
-        const int32_t *items = a.plan + 1, *slots = items + nseq + 1;
-        if (i >= items[nseq]) return false;
-        const int stride = (nseq + 63) / 64;
-        int s = stride * __popcll(__ballot(items[min((lane + 1) * stride, nseq)] <= i));
-        const int end = min(s + stride, nseq);
-        int more = 0;
-        for (int j = s; j < end; j += 64) more += __popcll(__ballot(j + lane < end && items[min(j + lane + 1, nseq)] <= i));
-        s = __builtin_amdgcn_readfirstlane(s + more);
-        it.w = seq_work(a, s, rows);
-        it.parts = parts_of(it.w, a.plan[0]);
-        it.slot = slots[s];
-        i -= items[s];
-    } else {
-        SeqWork w;
-        int64_t work = 0;
-        for (int j = 0; j < nseq; j += 64) {
-            w = lane_work(a, j + lane, rows);
-            const int64_t mine = (int64_t)w.steps * w.tiles;  // below 2^49 in all: two sums that fit 32 bits
-            work += ((int64_t)wave_total((int)(mine >> 24)) << 24) + wave_total((int)(mine & 0xFFFFFF));
+// Units of a tile that hold steps (one if there are none, for the zeros), and its units.
+__device__ __forceinline__ int live_units(int steps, int shift) { return max(1, (steps + (1 << shift) - 1) >> shift); }
+__device__ __forceinline__ int tile_units(const AttendArgs& a, int steps, const Split& s) {
+    const int live = live_units(steps, s.shift);
+    return s.whole ? (live + s.len - 1) / s.len * s.len : max(live, a.least >> s.shift);
+}
+
+// From the sums over the sequences of tiles times steps (or the least) and of tokens.  Offsets that decrease give more
+// tokens than there are: nothing is done then.
+__device__ __forceinline__ int line_shift(int64_t work) {
+    int shift = 0;
+    while (work >> shift > 1 << 29) ++shift;
+    return shift;
+}
+__device__ __forceinline__ int share(const AttendArgs& a, int units, int shift, int lengths) {
+    return max((units + lengths - 1) / lengths, max(a.least >> shift, 1));
+}
+// units: of all tiles, counted for the line; lengths(len): how many whole lengths all tiles take.
+template <class F>
+__device__ __forceinline__ Split line_split(const AttendArgs& a, int shift, int units, int tiles, int64_t tokens, F lengths) {
+    Split s;
+    s.shift = shift;
+    const int even = share(a, units, shift, a.target);
+    for (int i = 0; i < 2; ++i) {
+        // the equal share, then one that leaves half a length a tile
+        const int left = a.target - tiles / 2;
+        if (i && left <= 0) break;
+        s.len = i ? share(a, units, shift, left) : even;
+        if (s.len > even + (kAtCost >> shift)) break;
+        const int count = lengths(s.len);
+        if (count <= a.target) {
+            s.whole = true;
+            s.all = tokens > a.p.ntok ? 0 : count * s.len;
+            return s;
         }
-        const int c = part_steps(a, work, [&](int c) {
-            int all = 0;
-            for (int j = 0; j < nseq; j += 64) {
-                if (nseq > 64) w = lane_work(a, j + lane, rows);
-                all += wave_total(w.tiles * parts_of(w, c));
-            }
-            return all;
-        });
-        int before = 0, slots = 0;
-        bool found = false;
-        for (int j = 0; j < nseq && !found; j += 64) {
-            if (nseq > 64) w = lane_work(a, j + lane, rows);
-            const int parts = parts_of(w, c), mine = parts * w.tiles, slot = parts > 1 ? mine : 0;
-            const int upto = wave_scan(mine), sl = wave_scan(slot), total = lane_of(upto, 63);
-            if (i < before + total) {
-                const int s = __popcll(__ballot(before + upto <= i));
-                it.w.first = lane_of(w.first, s);
-                it.w.n = lane_of(w.n, s);
-                it.w.len = lane_of(w.len, s);
-                it.w.base = lane_of(w.base, s);
-                it.w.steps = lane_of(w.steps, s);
-                it.w.tiles = lane_of(w.tiles, s);
-                it.w.seq = j + s;
-                it.parts = lane_of(parts, s);
-                it.slot = slots + lane_of(sl - slot, s);
-                i -= before + lane_of(upto - mine, s);
-                found = true;
+    }
+    s.whole = false;
+    s.len = even;
+    s.all = tokens > a.p.ntok ? 0 : units;
+    return s;
+}
+
+// A tile on the line: its first unit.
+struct Tile {
+    SeqWork w;
+    int tile, at, live, units;
+};
+
+// The split, by every wave for itself; w: the lane's sequence of the first 64, for find_tile.
+__device__ __forceinline__ Split find_split(const AttendArgs& a, int rows, SeqWork& w) {
+    const int lane = threadIdx.x & 63, nseq = a.p.nseq;
+    Split s;
+    if (a.plan) {
+        s.shift = a.plan[0];
+        s.len = a.plan[1];
+        s.all = a.plan[2];
+        s.whole = false;
+        return s;
+    }
+    int64_t work = 0;
+    int tokens = 0, tiles = 0;
+    for (int j = (nseq - 1) & ~63; j >= 0; j -= 64) {
+        w = lane_work(a, j + lane, rows);
+        const int64_t mine = (int64_t)max(w.steps, a.least) * w.tiles;  // below 2^49 in all: two sums that fit 32 bits
+        work += ((int64_t)wave_total((int)(mine >> 24)) << 24) + wave_total((int)(mine & 0xFFFFFF));
+        tokens += wave_total(w.n);
+        tiles += wave_total(w.tiles);
+    }
+    const int shift = line_shift(work);
+    const auto sum = [&](auto value) {
+        int all = 0;
+        for (int j = 0; j < nseq; j += 64) {
+            const SeqWork v = j || nseq > 64 ? lane_work(a, j + lane, rows) : w;
+            all += wave_total(v.tiles * value(live_units(v.steps, shift)));
+        }
+        return all;
+    };
+    const int units = shift ? sum([&](int live) { return max(live, a.least >> shift); }) : (int)work;
+    return line_split(a, shift, units, tiles, tokens, [&](int len) { return sum([&](int live) { return (live + len - 1) / len; }); });
+}
+
+// The tile that unit `at` of the line belongs to; w: the lane's sequence of the first 64.
+__device__ __forceinline__ Tile find_tile(const AttendArgs& a, const Split& s, int at, int rows, const SeqWork& first) {
+    const int lane = threadIdx.x & 63, nseq = a.p.nseq;
+    Tile t;
+    int before = 0;
+    if (a.plan) {
+        const int32_t* units = a.plan + 3;  // before each sequence, and all
+        const int stride = (nseq + 63) / 64;
+        int seq = stride * __popcll(__ballot(units[min((lane + 1) * stride, nseq)] <= at));
+        const int end = min(seq + stride, nseq);
+        int more = 0;
+        for (int j = seq; j < end; j += 64) more += __popcll(__ballot(j + lane < end && units[min(j + lane + 1, nseq)] <= at));
+        seq = __builtin_amdgcn_readfirstlane(seq + more);
+        t.w = seq_work(a, seq, rows);
+        before = units[seq];
+    } else {
+        for (int j = 0; j < nseq; j += 64) {
+            const SeqWork w = j ? lane_work(a, j + lane, rows) : first;
+            const int mine = w.tiles * tile_units(a, w.steps, s), upto = wave_scan(mine), total = lane_of(upto, 63);
+            if (at < before + total) {
+                const int l = __popcll(__ballot(before + upto <= at));
+                t.w.first = lane_of(w.first, l);
+                t.w.n = lane_of(w.n, l);
+                t.w.len = lane_of(w.len, l);
+                t.w.base = lane_of(w.base, l);
+                t.w.steps = lane_of(w.steps, l);
+                t.w.tiles = lane_of(w.tiles, l);
+                t.w.seq = j + l;
+                before += lane_of(upto - mine, l);
+                break;
             }
             before += total;
-            slots += lane_of(sl, 63);
         }
-        if (!found) return false;
     }
-    it.tile = i / it.parts;
-    it.part = i - it.tile * it.parts;
-    it.c = (it.w.steps + it.parts - 1) / it.parts;
-    it.slot += it.tile * it.parts;
-    return true;
+    t.live = live_units(t.w.steps, s.shift);
+    t.units = tile_units(a, t.w.steps, s);
+    t.tile = (at - before) / t.units;
+    t.at = before + t.tile * t.units;
+    return t;
+}
+
+// The place of a tile's piece in workgroup `run` (of its head): the second, if the tile begins there.
+__device__ __forceinline__ int64_t piece_slot(const AttendArgs& a, const Split& s, const Tile& t, int run, int head) {
+    return ((int64_t)(2 * run + (t.at >= run * s.len ? 1 : 0))) * a.p.nheads + head;
 }
 
 // ------------------------------------------------------------------ values as the matrix instructions take them
@@ -179,12 +233,12 @@ struct Side {
 
 // Lane l's 16 bytes at base + offset + IMM to lds + IMM + 16 l (lds and base are the wave's).  Not the builtin: behind that
 // the compiler waits for every load on its way before any read of LDS.  Its own counts stay safe: it waits for more
-// than it means to.
+// than it means to.  (m0 is no register that it keeps anything in.)
 template <int IMM>
 __device__ __forceinline__ void to_lds(char* lds, const char* base, uint32_t offset) {
     static_assert(IMM >= 0 && IMM < 4096, "the instruction's offset");
     const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2 offset:%3" : : "s"(at), "v"(offset), "s"(base), "n"(IMM) : "memory", "m0");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2 offset:%3" : : "s"(at), "v"(offset), "s"(base), "n"(IMM) : "memory");
 }
 
 // 32 positions of a block format, as they lie in a page: the factors of both 16-position halves, then their scales,
@@ -210,25 +264,24 @@ struct Stage {
     __device__ static __forceinline__ int place(int row, int at) { return (row * kRowPieces + (at / 16 ^ turn(row))) * 16 + at % 16; }
 
     uint32_t offset[kOffsets];
-    __device__ __forceinline__ Stage() {
+    __device__ __forceinline__ Stage(int lane) {
 #pragma unroll
         for (int i = 0; i < kOffsets; ++i) {
-            const int p = 64 * i + (threadIdx.x & 63), row = p / kRowPieces;
+            const int p = 64 * i + lane, row = p / kRowPieces;
             offset[i] = row * kFactor + 16 * (p % kRowPieces ^ turn(row));
         }
     }
     // One half: 16 positions from `first` on of a chunk.
-    __device__ __forceinline__ void fetch(char* lds, int h, const char* chunk, int first, int page_size) const {
-        fetch_rows<0>(lds + 16 * kHalf * h, chunk + first * kFactor);
-        const int lane = threadIdx.x & 63;
+    __device__ __forceinline__ void fetch(int lane, char* lds, int h, const char* chunk, int first, int page_size) const {
+        fetch_rows<0>(lane, lds + 16 * kHalf * h, chunk + first * kFactor);
         if (lane < 2 * NB) to_lds<0>(lds + kScales + 32 * NB * h, chunk + (int64_t)page_size * kFactor + first * (2 * NB), 16 * lane);
     }
     template <int I>
-    __device__ __forceinline__ void fetch_rows(char* lds, const char* rows) const {
+    __device__ __forceinline__ void fetch_rows(int lane, char* lds, const char* rows) const {
         if constexpr (I < kHalfLoads) {
             constexpr int kBase = I % kOffsets, kImm = 1024 * (I - kBase);
-            if (kHalf >= 64 * I + 64 || (int)(threadIdx.x & 63) < kHalf - 64 * I) to_lds<kImm>(lds + 1024 * kBase, rows, offset[kBase]);
-            fetch_rows<I + 1>(lds, rows);
+            if (kHalf >= 64 * I + 64 || lane < kHalf - 64 * I) to_lds<kImm>(lds + 1024 * kBase, rows, offset[kBase]);
+            fetch_rows<I + 1>(lane, lds, rows);
         }
     }
     // N bytes of a row from `at` on; N divides 16 or is a multiple of it where rows are turned.
@@ -312,8 +365,8 @@ struct Keys {
     uint32_t w[TYPE == kKvF16 ? 4 * NB : kBytes / 4];
     uint32_t d[TYPE == kKvF16 ? 1 : 2 * NB];  // scales [position 4g + r][block], two a dword
 
-    __device__ __forceinline__ void load(const char* chunk, int place, int page_size) {
-        const int n = threadIdx.x & 15, g = threadIdx.x >> 4 & 3;
+    __device__ __forceinline__ void load(int lane, const char* chunk, int place, int page_size) {
+        const int n = lane & 15, g = lane >> 4;
         if constexpr (TYPE == kKvF16) {
             const char* p = chunk + (uint32_t)((place + n) * (64 * NB) + 16 * g);
 #pragma unroll
@@ -323,8 +376,8 @@ struct Keys {
             load_bytes<8 * NB>(d, chunk + (uint32_t)(page_size * Side<TYPE, NB>::kFactor + (place + 4 * g) * (2 * NB)));
         }
     }
-    __device__ __forceinline__ void read(int h, const char* lds) {
-        const int n = threadIdx.x & 15, g = threadIdx.x >> 4 & 3;
+    __device__ __forceinline__ void read(int lane, int h, const char* lds) {
+        const int n = lane & 15, g = lane >> 4;
         Stage<TYPE, NB>::template read<kBytes>(w, lds, 16 * h + n, g * kBytes);
         Stage<TYPE, NB>::scales(d, lds, h, g);
     }
@@ -372,16 +425,16 @@ struct Values {
     uint32_t w[8][kWords];
     uint32_t d[2][TYPE == kKvF16 ? 1 : 2 * NB];  // scales [half][position 4g + r][block]
 
-    __device__ __forceinline__ void load(int half, const char* chunk, int place, int page_size) {
-        const int n = threadIdx.x & 15, g = threadIdx.x >> 4 & 3;
+    __device__ __forceinline__ void load(int lane, int half, const char* chunk, int place, int page_size) {
+        const int n = lane & 15, g = lane >> 4;
         const char* p = chunk + (uint32_t)((place + 4 * g) * Side<TYPE, NB>::kFactor + n * kBytes);
 #pragma unroll
         for (int r = 0; r < 4; ++r) load_bytes<kBytes>(w[4 * half + r], p + r * Side<TYPE, NB>::kFactor);
         if constexpr (TYPE != kKvF16)
             load_bytes<8 * NB>(d[half], chunk + (uint32_t)(page_size * Side<TYPE, NB>::kFactor + (place + 4 * g) * (2 * NB)));
     }
-    __device__ __forceinline__ void read(const char* lds) {
-        const int n = threadIdx.x & 15, g = threadIdx.x >> 4 & 3;
+    __device__ __forceinline__ void read(int lane, const char* lds) {
+        const int n = lane & 15, g = lane >> 4;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
 #pragma unroll
@@ -567,7 +620,9 @@ __host__ __device__ constexpr int64_t part_floats(int rows, int dim) { return (i
 
 // ------------------------------------------------------------------ the pass
 
-struct Nothing {};
+struct Nothing {
+    __device__ Nothing(int) {}
+};
 
 // How a pair of formats, a width and a number of row tiles are run: waves of a workgroup, whether keys and values pass
 // through LDS on their way (block formats do, if the keys are one), and how many steps ahead they set out.
@@ -586,8 +641,10 @@ struct Shape {
 
 // Resources: the queries' parts lie in LDS, read again each step (two 16-byte reads a block), which leaves the
 // registers to the keys and values.
+// A piece of a tile: `count` steps of it from step `from` on.  part: its place if it is not the whole tile.
 template <int KT, int VT, int NB, int RT>
-__global__ __launch_bounds__((64 * Shape<KT, VT, NB, RT>::kWaves), 2) void attend_kernel(AttendArgs a) {
+__device__ __forceinline__ void attend_piece(const AttendArgs& a, const SeqWork& w, int tile, int from, int count, char* lds, float* lc,
+                                             int head, float* part) {
     using S = Shape<KT, VT, NB, RT>;
     constexpr int kRows = 16 * RT, kDim = 32 * NB, kTiles = 2 * NB, kWaves = S::kWaves, kDepth = S::kDepth;
     constexpr bool kKeyBlocks = KT != kKvF16, kValBlocks = VT != kKvF16, kStaged = S::kStaged;
@@ -596,22 +653,17 @@ __global__ __launch_bounds__((64 * Shape<KT, VT, NB, RT>::kWaves), 2) void atten
     constexpr bool kEarly = NB < 8;
     // Queries, then what is on its way, wave by wave; at the end the sums of half the waves, and of binary16 values a
     // place a wave for odd ones until then.
-    __shared__ __attribute__((aligned(16))) char lds[S::kBytes];
-    __shared__ float lc[kRows];
     auto& lq = *(uint32_t(*)[RT][NB][2][64][4])lds;
     auto& so = *(float(*)[kWaves / 2][kRows][S::kPitch])(lds + S::kQueries);
     auto& lm = *(float(*)[kWaves / 2][kRows])(lds + S::kQueries + sizeof(so));
     auto& ll = *(float(*)[kWaves / 2][kRows])(lds + S::kQueries + sizeof(so) + sizeof(lm));
     static_assert(kValBlocks || S::kSums / kWaves >= kRows * kAtStep * 4 + kDim * 2, "weights and a position's values");
-    const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int head = (int)(blockIdx.x % (uint32_t)a.p.nheads);
-    Item it;
-    if (!find_item(a, (int)(blockIdx.x / (uint32_t)a.p.nheads), kRows, it)) return;
-    const SeqWork& w = it.w;
-
+    int tid = threadIdx.x;
+    asm volatile("" : "+v"(tid));  // what depends on it is not kept from one piece to the next
+    const int lane = tid & 63, n = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     // The rows of the tile: lane n's, the positions [rlo, rhi) that they see, and the same over all of them.
-    const int row0 = it.tile * kRows, rows = min(kRows, w.n * a.group - row0), cap = a.p.max_pages * a.p.page_size;
+    const int row0 = tile * kRows, rows = min(kRows, w.n * a.group - row0), cap = a.p.max_pages * a.p.page_size;
     const auto low = [&](int pos) { return a.window > 0 && pos >= a.window ? pos - a.window + 1 : 0; };
     const int pos0 = w.len - w.n + row0 / a.group, pos1 = w.len - w.n + (row0 + rows - 1) / a.group;
     const int lo_min = low(pos0), lo_max = low(pos1), hi_min = min(pos0 + 1, cap), hi_max = min(pos1 + 1, cap);
@@ -623,7 +675,7 @@ __global__ __launch_bounds__((64 * Shape<KT, VT, NB, RT>::kWaves), 2) void atten
     uint32_t raw[RT][NB][2];
 #pragma unroll
     for (int x = 0; x < RT; ++x) {
-        const int r = min(16 * x + (int)threadIdx.x / 16, rows - 1), j = threadIdx.x & 15, tok = (row0 + r) / a.group;
+        const int r = min(16 * x + tid / 16, rows - 1), j = tid & 15, tok = (row0 + r) / a.group;
         const int64_t at = (w.first + tok) * a.ldq + (int64_t)(head * a.group + row0 + r - tok * a.group) * kDim;
         if (a.qtype == kF32) {
 #pragma unroll
@@ -638,8 +690,8 @@ __global__ __launch_bounds__((64 * Shape<KT, VT, NB, RT>::kWaves), 2) void atten
         }
     }
 
-    // This wave's steps of the part, those that the tile sees.
-    int s0 = it.part * it.c, s1 = min(s0 + it.c, w.steps);
+    // This wave's steps of the piece, those that the tile sees.
+    int s0 = from, s1 = min(from + count, w.steps);
     s0 = max(s0, (lo_min - w.base) / kAtStep);
     s1 = min(s1, (hi_max - w.base + kAtStep - 1) / kAtStep);  // (hi_max below 0: none)
     const int ksteps = s1 > s0 + wave ? (s1 - s0 - wave + kWaves - 1) / kWaves : 0;
@@ -647,37 +699,37 @@ __global__ __launch_bounds__((64 * Shape<KT, VT, NB, RT>::kWaves), 2) void atten
     const Mix mix;
     const char* const kbase = a.k.base + (int64_t)head * a.p.page_size * Side<KT, NB>::kRow;
     const char* const vbase = a.v.base + (int64_t)head * a.p.page_size * Side<VT, NB>::kRow;
-    // Lane 2 i + half: the page of step run + i, and the place in it.  A run of 32 steps is read anew after 30, before
+    // Lane 2 i + half: the page of step block + i, and the place in it.  A block of 32 steps is read anew after 30, before
     // the steps that set out then.
-    int pages = -1, places = 0, run = 0;
+    int pages = -1, places = 0, block = 0;
     uint64_t missing = 0;
-    const auto read_pages = [&](int from) {
-        const int k = from + (lane >> 1), pos = start + kAtStep * kWaves * k + 16 * (lane & 1);
-        run = from;
+    const auto read_pages = [&](int start_step) {
+        const int k = start_step + (lane >> 1), pos = start + kAtStep * kWaves * k + 16 * (lane & 1);
+        block = start_step;
         pages = k < ksteps ? kv_page(a.p, w.seq, pos) : -1;
         places = k < ksteps ? (int)((uint32_t)pos % (uint32_t)a.p.page_size) : 0;
         missing = __ballot(pages < 0);
     };
-    const auto page_of = [&](int k, int h) { return lane_of(pages, 2 * (k - run) + h); };
-    const auto place_of = [&](int k, int h) { return lane_of(places, 2 * (k - run) + h); };
+    const auto page_of = [&](int k, int h) { return lane_of(pages, 2 * (k - block) + h); };
+    const auto place_of = [&](int k, int h) { return lane_of(places, 2 * (k - block) + h); };
     // A position that does not exist is read at page 0 and not seen.
     const auto chunk_of = [&](const char* base, int64_t stride, int k, int h) {
         const int pg = page_of(k, h);
         return base + (pg < 0 ? 0 : pg * stride);
     };
     char* const ring = lds + S::kQueries + wave * S::kRing;
-    std::conditional_t<kStaged, Stage<KT, NB>, Nothing> kstage;
-    std::conditional_t<kStaged, Stage<VT, NB>, Nothing> vstage;
+    const std::conditional_t<kStaged, Stage<KT, NB>, Nothing> kstage(lane);
+    const std::conditional_t<kStaged, Stage<VT, NB>, Nothing> vstage(lane);
     Keys<KT, NB> keys[2];
     const auto fetch_keys = [&](int k) {
         const char* const chunk[2] = {chunk_of(kbase, a.k.stride, k, 0), chunk_of(kbase, a.k.stride, k, 1)};
         const int first[2] = {place_of(k, 0), place_of(k, 1)};
         if constexpr (kStaged) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) kstage.fetch(ring + k % kDepth * S::kKeys, h, chunk[h], first[h], a.p.page_size);
+            for (int h = 0; h < 2; ++h) kstage.fetch(lane, ring + k % kDepth * S::kKeys, h, chunk[h], first[h], a.p.page_size);
         } else {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) keys[h].load(chunk[h], first[h], a.p.page_size);
+            for (int h = 0; h < 2; ++h) keys[h].load(lane, chunk[h], first[h], a.p.page_size);
         }
     };
     const auto fetch_values = [&](int k, Values<VT, NB>& vals) {
@@ -685,10 +737,10 @@ __global__ __launch_bounds__((64 * Shape<KT, VT, NB, RT>::kWaves), 2) void atten
         const int first[2] = {place_of(k, 0), place_of(k, 1)};
         if constexpr (kStaged) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) vstage.fetch(ring + kDepth * S::kKeys + k % kDepth * S::kVals, h, chunk[h], first[h], a.p.page_size);
+            for (int h = 0; h < 2; ++h) vstage.fetch(lane, ring + kDepth * S::kKeys + k % kDepth * S::kVals, h, chunk[h], first[h], a.p.page_size);
         } else {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) vals.load(h, chunk[h], first[h], a.p.page_size);
+            for (int h = 0; h < 2; ++h) vals.load(lane, h, chunk[h], first[h], a.p.page_size);
         }
     };
     Values<VT, NB> vals;
@@ -708,7 +760,7 @@ __global__ __launch_bounds__((64 * Shape<KT, VT, NB, RT>::kWaves), 2) void atten
 #pragma unroll
     for (int x = 0; x < RT; ++x) {
         if (kWaves > 4 && wave >= 4) break;
-        const int r = 16 * x + (int)threadIdx.x / 16, j = threadIdx.x & 15;
+        const int r = 16 * x + tid / 16, j = tid & 15;
         float v[NB][2], most = 0.0f;
 #pragma unroll
         for (int b = 0; b < NB; ++b)
@@ -761,14 +813,14 @@ __global__ __launch_bounds__((64 * Shape<KT, VT, NB, RT>::kWaves), 2) void atten
 
     for (int k = 0; k < ksteps; ++k) {
         const int j0 = start + kAtStep * kWaves * k;
-        if (k - run == 30) read_pages(k);
-        const bool exist[2] = {!(missing >> (2 * (k - run)) & 1), !(missing >> (2 * (k - run) + 1) & 1)};
+        if (k - block == 30) read_pages(k);
+        const bool exist[2] = {!(missing >> (2 * (k - block)) & 1), !(missing >> (2 * (k - block) + 1) & 1)};
         if constexpr (kStaged) {
             // Behind this step's keys: its values, and the keys and values of the steps that have set out since.
             if (kDepth > 1 && k + 1 < ksteps) arrived<2 * Stage<VT, NB>::kLoads + Stage<KT, NB>::kLoads>();
             else arrived<Stage<VT, NB>::kLoads>();
 #pragma unroll
-            for (int h = 0; h < 2; ++h) keys[h].read(h, ring + k % kDepth * S::kKeys);
+            for (int h = 0; h < 2; ++h) keys[h].read(lane, h, ring + k % kDepth * S::kKeys);
         } else {
             fetch_values(k, vals);
         }
@@ -877,7 +929,7 @@ __global__ __launch_bounds__((64 * Shape<KT, VT, NB, RT>::kWaves), 2) void atten
             if (k + kDepth < ksteps) arrived<kDepth * kK + (kDepth - 1) * kV>();
             else if (kDepth > 1 && k + 1 < ksteps) arrived<kK + kV>();
             else arrived<0>();
-            vals.read(ring + kDepth * S::kKeys + k % kDepth * S::kVals);
+            vals.read(lane, ring + kDepth * S::kKeys + k % kDepth * S::kVals);
         }
         if constexpr (kValBlocks) {
             bool above = false;
@@ -1075,15 +1127,12 @@ __global__ __launch_bounds__((64 * Shape<KT, VT, NB, RT>::kWaves), 2) void atten
     __syncthreads();
     if (wave < 2) put(wave);
     __syncthreads();
-    const bool whole = it.parts == 1;
-    if (!whole && (it.slot < 0 || it.slot + it.part >= a.slots)) return;  // offsets that decrease: no place for it
-    float* part = a.parts + ((int64_t)(it.slot + it.part) * a.p.nheads + head) * part_floats(kRows, kDim);
-    for (int i = threadIdx.x; i < rows * (kDim / 4); i += 64 * kWaves) {
+    for (int i = tid; i < rows * (kDim / 4); i += 64 * kWaves) {
         const int r = i / (kDim / 4), d = 4 * (i - r * (kDim / 4));
         const float most = __builtin_fmaxf(lm[0][r], lm[1][r]), e0 = beside(lm[0][r], most), e1 = beside(lm[1][r], most);
         const float sum = e0 * ll[0][r] + e1 * ll[1][r];
         float4_t f = e0 * *(const float4_t*)&so[0][r][d] + e1 * *(const float4_t*)&so[1][r][d];
-        if (whole) {
+        if (!part) {
             f *= sum != 0.0f ? 1.0f / sum : 0.0f;
             write_row(a, w.first, head, row0 + r, d, f, most, sum);
         } else {
@@ -1093,6 +1142,31 @@ __global__ __launch_bounds__((64 * Shape<KT, VT, NB, RT>::kWaves), 2) void atten
             }
             *(float4_t*)(part + 2 * kRows + r * kDim + d) = f;
         }
+    }
+}
+
+
+template <int KT, int VT, int NB, int RT>
+__global__ __launch_bounds__((64 * Shape<KT, VT, NB, RT>::kWaves), 2) void attend_kernel(AttendArgs a) {
+    using S = Shape<KT, VT, NB, RT>;
+    constexpr int kRows = 16 * RT, kDim = 32 * NB;
+    __shared__ __attribute__((aligned(16))) char lds[S::kBytes];
+    __shared__ float lc[kRows];
+    const int head = (int)(blockIdx.x % (uint32_t)a.p.nheads);
+    const int run = (int)(blockIdx.x / (uint32_t)a.p.nheads);
+    SeqWork mine;
+    const Split split = find_split(a, kRows, mine);
+    const int begin = run * split.len, end = min(begin + split.len, split.all);
+    for (int at = begin; at < end;) {
+        if (at > begin && !a.plan) mine = lane_work(a, threadIdx.x & 63, kRows);  // (not kept beside the sums)
+        const Tile tl = find_tile(a, split, at, kRows, mine);
+        const SeqWork& w = tl.w;
+        const int piece = at - tl.at, units = min(end - tl.at, tl.live) - piece;
+        at = tl.at + tl.units;
+        if (units <= 0) continue;
+        attend_piece<KT, VT, NB, RT>(a, w, tl.tile, piece << split.shift, units << split.shift, lds, lc, head,
+                                     units == tl.live ? nullptr : a.parts + piece_slot(a, split, tl, run, head) * part_floats(kRows, kDim));
+        __syncthreads();
     }
 }
 

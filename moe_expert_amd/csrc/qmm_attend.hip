@@ -4,73 +4,68 @@
 
 namespace qmm {
 
-// The split of more sequences than a wave's registers hold: items and slots before each sequence.
+// The split of more sequences than a wave looks through: shift, length, all, then the units before each sequence.
 __global__ __launch_bounds__(1024) void attend_plan_kernel(AttendArgs a, int rows, int32_t* plan) {
-    __shared__ int64_t work[16];
-    __shared__ int items[16], slots[16];
+    __shared__ int64_t work[16], tokens[16];
+    __shared__ int units[16];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, nseq = a.p.nseq;
-    int64_t sum = 0;
+    int64_t sum = 0, all = 0;
     for (int s = threadIdx.x; s - lane < nseq; s += 1024) {
         const SeqWork w = lane_work(a, s, rows);
-        const int64_t mine = (int64_t)w.steps * w.tiles;
+        const int64_t mine = (int64_t)max(w.steps, a.least) * w.tiles;
         sum += ((int64_t)wave_total((int)(mine >> 24)) << 24) + wave_total((int)(mine & 0xFFFFFF));
+        all += wave_total(w.n);
     }
-    if (lane == 0) work[wave] = sum;
+    if (lane == 0) {
+        work[wave] = sum;
+        tokens[wave] = all;
+    }
     __syncthreads();
-    sum = 0;
-    for (int i = 0; i < 16; ++i) sum += work[i];
-    const int c = part_steps(a, sum, [&](int) { return a.target + 1; });
-    int before = 0, sbefore = 0;
+    sum = all = 0;
+    for (int i = 0; i < 16; ++i) {
+        sum += work[i];
+        all += tokens[i];
+    }
+    Split split{line_shift(sum), 0, 0, false};
+    int before = 0;
     for (int s0 = 0; s0 < nseq; s0 += 1024) {
         const int s = s0 + threadIdx.x;
-        int mine = 0, slot = 0;
-        if (s < nseq) {
-            const SeqWork w = seq_work(a, s, rows);
-            const int parts = parts_of(w, c);
-            mine = parts * w.tiles;
-            slot = parts > 1 ? mine : 0;
-        }
-        const int upto = wave_scan(mine), sl = wave_scan(slot);
+        const SeqWork w = lane_work(a, s, rows);
+        const int mine = w.tiles * tile_units(a, w.steps, split), upto = wave_scan(mine);
         __syncthreads();
-        if (lane == 63) {
-            items[wave] = upto;
-            slots[wave] = sl;
-        }
+        if (lane == 63) units[wave] = upto;
         __syncthreads();
-        int off = before, soff = sbefore;
+        int off = before;
         for (int i = 0; i < 16; ++i) {
-            off += i < wave ? items[i] : 0;
-            soff += i < wave ? slots[i] : 0;
-            before += items[i];
-            sbefore += slots[i];
+            off += i < wave ? units[i] : 0;
+            before += units[i];
         }
-        if (s < nseq) {
-            plan[1 + s] = off + upto - mine;
-            plan[2 + nseq + s] = soff + sl - slot;
-        }
+        if (s < nseq) plan[3 + s] = off + upto - mine;
     }
+    split = line_split(a, split.shift, before, 0, all, [&](int) { return a.target + 1; });
     if (threadIdx.x == 0) {
-        plan[0] = c;
-        plan[1 + nseq] = before;
-        plan[2 + 2 * nseq] = sbefore;
+        plan[0] = split.shift;
+        plan[1] = split.len;
+        plan[2] = split.all;
+        plan[3 + nseq] = before;
     }
 }
 
-// The parts of a tile joined, in the order of the parts.  The tile's workgroups share its groups of four dims; a
-// group's parts go to E lanes of a wave, each every E-th of them, lanes of neighbouring groups beside each other.
+// The pieces of a tile joined, in their order, by as many workgroups as it has pieces: they share the tile's groups of
+// four dims.  A group's pieces go to E lanes of a wave, each every E-th of them, lanes of neighbouring groups
+// beside each other.  Bound: two loads one after the other (the sequences, the pieces), 4-5 us.
 template <int E>
-__device__ __forceinline__ void join(const AttendArgs& a, const Item& it, int head, int tile_rows) {
-    const int dim = a.p.dim, row0 = it.tile * tile_rows, rows = min(tile_rows, it.w.n * a.group - row0), quads = rows * (dim / 4);
-    const int lane = threadIdx.x & 63, run = lane / (64 / E);
-    const int64_t step = a.p.nheads * part_floats(tile_rows, dim);
-    const float* part = a.parts + ((int64_t)it.slot * a.p.nheads + head) * part_floats(tile_rows, dim);
-    for (int u = (it.part * 4 + (int)(threadIdx.x >> 6)) * (64 / E); u < quads; u += it.parts * 4 * (64 / E)) {
+__device__ __forceinline__ void join(const AttendArgs& a, const Split& split, const Tile& t, int from, int pieces, int mine, int head, int tile_rows) {
+    const int dim = a.p.dim, row0 = t.tile * tile_rows, rows = min(tile_rows, t.w.n * a.group - row0), quads = rows * (dim / 4);
+    const int lane = threadIdx.x & 63, turn = lane / (64 / E);
+    const int64_t size = part_floats(tile_rows, dim);
+    for (int u = (mine * 4 + (int)(threadIdx.x >> 6)) * (64 / E); u < quads; u += pieces * 4 * (64 / E)) {
         const int at = min(u + lane % (64 / E), quads - 1), r = at / (dim / 4), d = 4 * (at - r * (dim / 4));
         float most = -INFINITY, sum = 0.0f;
         float4_t f = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 4
-        for (int i = run; i < it.parts; i += E) {
-            const float* p = part + i * step;
+        for (int i = turn; i < pieces; i += E) {
+            const float* p = a.parts + piece_slot(a, split, t, from + i, head) * size;
             const float m = p[r], l = p[tile_rows + r];
             const float4_t o = *(const float4_t*)(p + 2 * tile_rows + r * dim + d);
             const float now = __builtin_fmaxf(most, m), old = beside(most, now), fresh = beside(m, now);
@@ -87,20 +82,26 @@ __device__ __forceinline__ void join(const AttendArgs& a, const Item& it, int he
 #pragma unroll
             for (int e = 0; e < 4; ++e) f[e] = f[e] * old + __shfl_xor(f[e], x, 64) * fresh;
         }
-        if (run == 0 && u + lane < quads) {
+        if (turn == 0 && u + lane < quads) {
             f *= sum != 0.0f ? 1.0f / sum : 0.0f;
-            write_row(a, it.w.first, head, row0 + r, d, f, most, sum);
+            write_row(a, t.w.first, head, row0 + r, d, f, most, sum);
         }
     }
 }
 
 __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, int tile_rows) {
-    const int head = (int)(blockIdx.x % (uint32_t)a.p.nheads);
-    Item it;
-    if (!find_item(a, (int)(blockIdx.x / (uint32_t)a.p.nheads), tile_rows, it) || it.parts == 1) return;
-    if (it.slot < 0 || it.slot + it.parts > a.slots) return;
-    if (it.parts <= 16) join<1>(a, it, head, tile_rows);
-    else join<16>(a, it, head, tile_rows);
+    const int head = (int)(blockIdx.x % (uint32_t)a.p.nheads), run = (int)(blockIdx.x / (uint32_t)a.p.nheads);
+    SeqWork mine;
+    const Split split = find_split(a, tile_rows, mine);
+    // The tile that goes on from the workgroup before, or the one that begins here and goes on.
+    const int begin = run * split.len, end = begin + split.len;
+    if (blockIdx.y ? end >= split.all : !run || begin >= split.all) return;
+    const Tile t = find_tile(a, split, blockIdx.y ? end - 1 : begin, tile_rows, mine);
+    if (blockIdx.y ? t.at < begin || t.at + t.live <= end : t.at >= begin || t.at + t.live <= begin) return;
+    const int from = t.at / split.len, pieces = (t.at + t.live - 1) / split.len - from + 1;
+    if (pieces <= 4) join<1>(a, split, t, from, pieces, run - from, head, tile_rows);
+    else if (pieces <= 64) join<8>(a, split, t, from, pieces, run - from, head, tile_rows);
+    else join<16>(a, split, t, from, pieces, run - from, head, tile_rows);
 }
 
 }  // namespace qmm
@@ -113,16 +114,15 @@ using namespace qmm;
 
 namespace {
 
-constexpr int64_t kAtTarget = 512;  // workgroups to split the caches over: two for every CU, what runs at once
-constexpr int kAtLeast = 8;          // steps of the shortest part
+constexpr int kAtTarget = 512;  // workgroups: two for every CU, what runs at once
+constexpr int kAtLeast = 8;     // steps that a tile counts for at least, two for each wave
 
 struct AttendShape {
     KvPlace p;
     int rt;          // 16-row tiles a workgroup
-    int target, least;
-    int64_t items;   // workgroups a head of keys, at most
-    int64_t slots;   // parts of tiles that have several, at most
-    size_t bytes;    // of the workspace: parts, then the plan
+    int target;      // workgroups a head of keys, at most
+    bool split;      // a tile can have more than one piece
+    size_t bytes;    // of the workspace: pieces, then the plan
     size_t plan;     // its offset
 };
 
@@ -136,15 +136,14 @@ int attend_shape(AttendShape& s, const qmm_kv_cache* c, const int32_t* pages, in
     const bool wide = c->head_dim <= 128;  // two tiles of wider heads do not fit the registers
     s.rt = wide && nseq && group * ((ntok + nseq - 1) / nseq) > 16 ? 2 : 1;
     const int64_t rows = 16 * s.rt, tiles = std::min(nseq + ntok * group / rows, ntok * ((group + rows - 1) / rows));
-    s.target = (int)std::max(kAtTarget / c->nheads, (int64_t)1);
-    s.least = kAtLeast;
-    const int64_t steps = (max_pages * c->page_size + kAtStep - 1) / kAtStep + 1, most = (steps + s.least - 1) / s.least;
-    s.items = std::min(kAtRounds * s.target + tiles, tiles * most);
-    s.slots = most > 1 ? std::min((int64_t)2 * kAtRounds * s.target, tiles * most) : 0;
-    if (s.items * c->nheads >= 1 << 24) return QMM_EUNSUPPORTED;  // below 2^32 threads
+    // At most this many steps a tile (a walk may begin 15 positions early), and so workgroups with a length of the line.
+    const int64_t steps = (max_pages * c->page_size + kAtStep - 1) / kAtStep + 1;
+    const int64_t line = tiles * ((std::max(steps, (int64_t)kAtLeast) + kAtLeast - 1) / kAtLeast);
+    s.target = (int)std::max(std::min((int64_t)(kAtTarget / c->nheads), line), (int64_t)1);
+    s.split = steps > kAtLeast || tiles > s.target;
     // (sized for 32 rows where a call of other proportions would take them)
-    s.plan = (size_t)(s.slots * c->nheads * part_floats(wide ? 32 : 16, c->head_dim) * 4 + 15) & ~(size_t)15;
-    s.bytes = s.plan + (nseq > kAtInline ? (size_t)(2 * nseq + 3) * 4 : 0);
+    s.plan = s.split ? (size_t)(2 * s.target * c->nheads * part_floats(wide ? 32 : 16, c->head_dim) * 4 + 15) & ~(size_t)15 : 0;
+    s.bytes = s.plan + (nseq > kAtInline ? (size_t)(nseq + 4) * 4 : 0);
     s.bytes = s.bytes < 16 ? 16 : s.bytes;
     return QMM_OK;
 }
@@ -190,15 +189,14 @@ extern "C" int qmm_kv_attend(const qmm_kv_cache* c, const int32_t* pages, int64_
     a.scale = (float)((double)scale * 1.4426950408889634);
     a.window = (int)std::min(window, (int64_t)0x7FFFFFFF);  // more than any position
     a.target = s.target;
-    a.least = s.least;
-    a.slots = (int)s.slots;
+    a.least = kAtLeast;
     a.vec = fours(out, ldo, otype);
     const hipStream_t st = as_stream(stream);
     if (a.plan) hipLaunchKernelGGL(attend_plan_kernel, dim3(1), dim3(1024), 0, st, a, 16 * s.rt, const_cast<int32_t*>(a.plan));
-    const unsigned grid = (unsigned)(s.items * c->nheads);
+    const unsigned grid = (unsigned)(s.target * c->nheads);
     if (c->ktype == QMM_F16) attend_f16(a, grid, s.rt, st);
     else if (c->ktype == QMM_Q8_0) attend_q8(a, grid, s.rt, st);
     else attend_iq4(a, grid, s.rt, st);
-    if (s.slots) hipLaunchKernelGGL(attend_join_kernel, dim3(grid), dim3(256), 0, st, a, 16 * s.rt);
+    if (s.split) hipLaunchKernelGGL(attend_join_kernel, dim3(grid, 2), dim3(256), 0, st, a, 16 * s.rt);
     return launch_status();
 }
