@@ -342,8 +342,11 @@ __device__ __forceinline__ void load_bytes(uint32_t* w, const char* p) {
     __builtin_memcpy(w, p, N);
 }
 
-// (u - 128) 2^-10 of two biased bytes, which perm lays into the low bytes of two halves: as binary16 they are u 2^-24.
-__device__ __forceinline__ uint32_t biased_pair(uint32_t x) {
+// Two biased bytes u = q + 128, which perm laid into the low bytes of two halves, are u 2^-24 as binary16 values.  As
+// they are (BIASED), what 128 in their place would give is taken from the sums; or (u - 128) 2^-10.
+template <bool BIASED>
+__device__ __forceinline__ uint32_t value_pair(uint32_t x) {
+    if constexpr (BIASED) return x;
     const half2_t scale = {(_Float16)16384.0f, (_Float16)16384.0f}, bias = {(_Float16)-0.125f, (_Float16)-0.125f};
     return __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(__builtin_bit_cast(half2_t, x), scale, bias));
 }
@@ -400,10 +403,10 @@ struct Keys {
         for (int m = 0; m < 4; ++m) {
             if constexpr (TYPE == kKvQ8) {
                 const int at = (m * NB + b) * 2;
-                x[m] = biased_pair(perm(r.a[at / 4], r.a[at / 4], pair_sel(at % 4, at % 4 + 1)));
+                x[m] = perm(r.a[at / 4], r.a[at / 4], pair_sel(at % 4, at % 4 + 1));
             } else {
                 const int at = m * NB + b;
-                x[m] = biased_pair(perm(r.b[at / 4], r.a[at / 4], pair_sel(at % 4, at % 4 + 4)));
+                x[m] = perm(r.b[at / 4], r.a[at / 4], pair_sel(at % 4, at % 4 + 4));
             }
         }
         return as_half8(x[0], x[1], x[2], x[3]);
@@ -518,6 +521,7 @@ struct Values {
                 }
             }
     }
+    template <bool BIASED>
     __device__ static __forceinline__ half8_t tile(const Ready& r, int t) {
         uint32_t o[4];
 #pragma unroll
@@ -525,11 +529,11 @@ struct Values {
             if constexpr (TYPE == kKvF16) {
                 o[m] = perm(r.a[2 * m + 1][t / 2], r.a[2 * m][t / 2], t & 1 ? 0x07060302u : 0x05040100u);
             } else if constexpr (TYPE == kKvQ8) {
-                o[m] = biased_pair(perm(r.a[2 * m + 1][t / 4], r.a[2 * m][t / 4], pair_sel(t % 4, t % 4 + 4)));
+                o[m] = value_pair<BIASED>(perm(r.a[2 * m + 1][t / 4], r.a[2 * m][t / 4], pair_sel(t % 4, t % 4 + 4)));
             } else {
                 const int b = t / 2, i = b / 4, shared = kBytes % 4 == 2 && i == kWords - 1 ? 2 : 0;
                 const uint32_t lo = t & 1 ? r.b[2 * m][i] : r.a[2 * m][i], hi = t & 1 ? r.b[2 * m + 1][i] : r.a[2 * m + 1][i];
-                o[m] = biased_pair(perm(hi, lo, pair_sel(b % 4, b % 4 + 4 + shared)));
+                o[m] = value_pair<BIASED>(perm(hi, lo, pair_sel(b % 4, b % 4 + 4 + shared)));
             }
         }
         return as_half8(o[0], o[1], o[2], o[3]);
@@ -630,7 +634,9 @@ template <int KT, int VT, int NB, int RT>
 struct Shape {
     static constexpr bool kStaged = KT != kKvF16;
     static constexpr int kKeys = kStaged ? Stage<KT, NB>::kBytes : 0, kVals = kStaged ? Stage<VT, NB>::kBytes : 0;
-    static constexpr int kQueries = RT * NB * 2 * 64 * 16;
+    // Keys of a block format enter as u 2^-24, their sums begin at -128 2^-24 times the queries' sum.  Values do where the registers hold the sums of their weights beside the others.
+    static constexpr bool kBiased = VT != kKvF16 && NB * RT <= 4;
+    static constexpr int kQueries = RT * NB * (2 * 64 + (kStaged ? 16 : 0)) * 16;
     static constexpr int kWaves = kQueries + 4 * (kKeys + kVals) > kAtLds ? 8 : 4;
     static constexpr int kDepth = kStaged && kWaves == 4 && kQueries + 8 * (kKeys + kVals) <= kAtLds ? 2 : 1;
     static constexpr int kRing = kDepth * (kKeys + kVals);  // bytes a wave
@@ -647,13 +653,14 @@ __device__ __forceinline__ void attend_piece(const AttendArgs& a, const SeqWork&
                                              int head, float* part) {
     using S = Shape<KT, VT, NB, RT>;
     constexpr int kRows = 16 * RT, kDim = 32 * NB, kTiles = 2 * NB, kWaves = S::kWaves, kDepth = S::kDepth;
-    constexpr bool kKeyBlocks = KT != kKvF16, kValBlocks = VT != kKvF16, kStaged = S::kStaged;
+    constexpr bool kKeyBlocks = KT != kKvF16, kValBlocks = VT != kKvF16, kStaged = S::kStaged, kBiased = S::kBiased;
     // Binary16 keys are read into registers, a step ahead: before the weights, or after the values where the registers
     // do not hold both.
     constexpr bool kEarly = NB < 8;
     // Queries, then what is on its way, wave by wave; at the end the sums of half the waves, and of binary16 values a
     // place a wave for odd ones until then.
     auto& lq = *(uint32_t(*)[RT][NB][2][64][4])lds;
+    auto& lb = *(float(*)[RT][NB][16][4])(lds + sizeof(lq));  // where a block's sums begin, for the four positions of a lane
     auto& so = *(float(*)[kWaves / 2][kRows][S::kPitch])(lds + S::kQueries);
     auto& lm = *(float(*)[kWaves / 2][kRows])(lds + S::kQueries + sizeof(so));
     auto& ll = *(float(*)[kWaves / 2][kRows])(lds + S::kQueries + sizeof(so) + sizeof(lm));
@@ -783,14 +790,23 @@ __device__ __forceinline__ void attend_piece(const AttendArgs& a, const SeqWork&
             two_parts(mix, v[b][0] * up, v[b][1] * up, hi, lo);
             lq[x][b][0][16 * (j / 4) + r % 16][j % 4] = hi;
             lq[x][b][1][16 * (j / 4) + r % 16][j % 4] = lo;
+            if constexpr (kKeyBlocks) {
+                const half2_t h = __builtin_bit_cast(half2_t, hi), l = __builtin_bit_cast(half2_t, lo);
+                float sum = ((float)h.x + (float)h.y) + ((float)l.x + (float)l.y);
+                sum += dpp<0xB1>(sum);
+                sum += dpp<0x4E>(sum);
+                sum += dpp<0x141>(sum);
+                sum += dpp<0x140>(sum);
+                if (j < 4) lb[x][b][r % 16][j] = sum * -power(7 - 24);
+            }
         }
-        if (j == 0) lc[r] = power(e - 14 + (kKeyBlocks ? 10 : 0));
+        if (j == 0) lc[r] = power(e - 14 + (kKeyBlocks ? 24 : 0));
     }
     __syncthreads();
 
     int rlo[RT], rhi[RT];
     float c[RT];  // scores are c times the sums of the scaled operands
-    float4_t o[RT][kTiles];
+    float4_t o[RT][kTiles], weights[RT][kBiased ? NB : 1];  // weights: 128 2^-24 times the sums of a block's
     float m[RT], l[RT], limit[RT], fold[RT];
     int bound[RT];  // the binary16 bits of limit, a power of two above the scales of values that the row has seen
 #pragma unroll
@@ -807,7 +823,10 @@ __device__ __forceinline__ void attend_piece(const AttendArgs& a, const SeqWork&
         bound[x] = 1;
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) o[x][t] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int b = 0; b < (kBiased ? NB : 1); ++b) weights[x][b] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
     }
+    const half8_t ones = as_half8(0x00800080u, 0x00800080u, 0x00800080u, 0x00800080u);
     int least = 1;  // the least of the rows' bounds
     const auto queries = [&](int x, int b, int part) { return __builtin_bit_cast(half8_t, *(const u32x4*)lq[x][b][part][lane]); };
 
@@ -848,7 +867,7 @@ __device__ __forceinline__ void attend_piece(const AttendArgs& a, const SeqWork&
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         if constexpr (kKeyBlocks) {
-                            float4_t u = {0.0f, 0.0f, 0.0f, 0.0f};
+                            float4_t u = *(const float4_t*)lb[x][b][n];
                             u = __builtin_amdgcn_mfma_f32_16x16x32_f16(kb[h], ql, u, 0, 0, 0);
                             u = __builtin_amdgcn_mfma_f32_16x16x32_f16(kb[h], qh, u, 0, 0, 0);
 #pragma unroll
@@ -910,6 +929,10 @@ __device__ __forceinline__ void attend_piece(const AttendArgs& a, const SeqWork&
                 l[x] *= shrink;
 #pragma unroll
                 for (int t = 0; t < kTiles; ++t) o[x][t] *= shrink;
+                if constexpr (kBiased) {
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) weights[x][b] *= shrink;
+                }
             }
         }
         // Weights: of binary16 values times 2^14; of blocks' to be multiplied by the scales and a power of two that
@@ -978,6 +1001,10 @@ __device__ __forceinline__ void attend_piece(const AttendArgs& a, const SeqWork&
                     bound[x] = to > 65536.0f ? 0x10000 : (int)f2h(to);
 #pragma unroll
                     for (int t = 0; t < kTiles; ++t) o[x][t] *= shrink;
+                    if constexpr (kBiased) {
+#pragma unroll
+                        for (int b = 0; b < NB; ++b) weights[x][b] *= shrink;
+                    }
                     now = min(now, bound[x]);
                 }
                 now = min(now, dpp_i<0xB1>(now));
@@ -1070,7 +1097,16 @@ __device__ __forceinline__ void attend_piece(const AttendArgs& a, const SeqWork&
                     pl[x] = as_half8(lo[0], lo[1], lo[2], lo[3]);
                 }
             }
-            const half8_t v = Values<VT, NB>::tile(ready, t);
+            if constexpr (kBiased) {
+                if (t % 2 == 0) {
+#pragma unroll
+                    for (int x = 0; x < RT; ++x) {
+                        weights[x][t / 2] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ones, pl[x], weights[x][t / 2], 0, 0, 0);
+                        weights[x][t / 2] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ones, ph[x], weights[x][t / 2], 0, 0, 0);
+                    }
+                }
+            }
+            const half8_t v = Values<VT, NB>::template tile<kBiased>(ready, t);
 #pragma unroll
             for (int x = 0; x < RT; ++x) {
                 o[x][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, pl[x], o[x][t], 0, 0, 0);
@@ -1090,9 +1126,9 @@ __device__ __forceinline__ void attend_piece(const AttendArgs& a, const SeqWork&
     for (int x = 0; x < RT; ++x) {
         l[x] = rows_sum(l[x]) * (kValBlocks ? 1.0f : power(-14));
         m[x] *= c[x];
-        const float back = kValBlocks ? limit[x] * power(10 - 14) : power(-14);
+        const float back = kValBlocks ? limit[x] * power((kBiased ? 24 : 10) - 14) : power(-14);
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t) o[x][t] *= back;
+        for (int t = 0; t < kTiles; ++t) o[x][t] = (kBiased ? o[x][t] - weights[x][kBiased ? t / 2 : 0] : o[x][t]) * back;
     }
     const auto put = [&](int at) {
 #pragma unroll
