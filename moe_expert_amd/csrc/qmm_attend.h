@@ -47,6 +47,14 @@ struct AttendArgs {
     int vec;                          // out: groups of four values are aligned
 };
 
+// The kernel's argument where it is needed: read again from its segment rather than kept in scalar registers, of which
+// there are too few for all that a loop of steps does not need.
+__device__ __forceinline__ const AttendArgs& launch_args() {
+    auto p = (const __attribute__((address_space(4))) AttendArgs*)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(p));
+    return *(const AttendArgs*)p;
+}
+
 // ------------------------------------------------------------------ what a workgroup does
 
 // Sequence s as the split sees it.
@@ -216,9 +224,7 @@ __device__ __forceinline__ Tile find_tile(const AttendArgs& a, const Split& s, i
 }
 
 // The place of a tile's piece in workgroup `run` (of its head): the second, if the tile begins there.
-__device__ __forceinline__ int64_t piece_slot(const AttendArgs& a, const Split& s, const Tile& t, int run, int head) {
-    return ((int64_t)(2 * run + (t.at >= run * s.len ? 1 : 0))) * a.p.nheads + head;
-}
+__device__ __forceinline__ int piece_slot(const Split& s, const Tile& t, int run) { return 2 * run + (t.at >= run * s.len ? 1 : 0); }
 
 // ------------------------------------------------------------------ values as the matrix instructions take them
 
@@ -234,11 +240,20 @@ struct Side {
 // Lane l's 16 bytes at base + offset + IMM to lds + IMM + 16 l (lds and base are the wave's).  Not the builtin: behind that
 // the compiler waits for every load on its way before any read of LDS.  Its own counts stay safe: it waits for more
 // than it means to.  (m0 is no register that it keeps anything in.)
-template <int IMM>
+// (Five states from base's last v_readlane to its use.)  The first LANES lanes of a wave of 64 whose lanes are all
+// active.
+template <int IMM, int LANES>
 __device__ __forceinline__ void to_lds(char* lds, const char* base, uint32_t offset) {
-    static_assert(IMM >= 0 && IMM < 4096, "the instruction's offset");
+    static_assert(IMM >= 0 && IMM < 4096 && LANES > 0 && LANES <= 64, "the instruction's offset, a wave");
     const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2 offset:%3" : : "s"(at), "v"(offset), "s"(base), "n"(IMM) : "memory");
+    if constexpr (LANES == 64) {
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %1, %2 offset:%3" : : "s"(at), "v"(offset), "s"(base), "n"(IMM) : "memory");
+    } else {
+        constexpr uint32_t kLow = LANES >= 32 ? ~0u : (1u << (LANES & 31)) - 1, kHigh = LANES > 32 ? (1u << ((LANES - 32) & 31)) - 1 : 0;
+        asm volatile("s_mov_b32 m0, %0\n\ts_mov_b32 exec_lo, %4\n\ts_mov_b32 exec_hi, %5\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %1, %2 offset:%3\n\t"
+                     "s_mov_b64 exec, -1"
+                     : : "s"(at), "v"(offset), "s"(base), "n"(IMM), "n"(kLow), "n"(kHigh) : "memory");
+    }
 }
 
 // 32 positions of a block format, as they lie in a page: the factors of both 16-position halves, then their scales,
@@ -271,17 +286,17 @@ struct Stage {
             offset[i] = row * kFactor + 16 * (p % kRowPieces ^ turn(row));
         }
     }
-    // One half: 16 positions from `first` on of a chunk.
-    __device__ __forceinline__ void fetch(int lane, char* lds, int h, const char* chunk, int first, int page_size) const {
-        fetch_rows<0>(lane, lds + 16 * kHalf * h, chunk + first * kFactor);
-        if (lane < 2 * NB) to_lds<0>(lds + kScales + 32 * NB * h, chunk + (int64_t)page_size * kFactor + first * (2 * NB), 16 * lane);
+    // One half: 16 positions, whose factors begin at rows and whose scales are `scales` bytes on.
+    __device__ __forceinline__ void fetch(int lane, char* lds, int h, const char* rows, int scales) const {
+        fetch_rows<0>(lds + 16 * kHalf * h, rows);
+        to_lds<0, 2 * NB>(lds + kScales + 32 * NB * h, rows + scales, 16 * lane);
     }
     template <int I>
-    __device__ __forceinline__ void fetch_rows(int lane, char* lds, const char* rows) const {
+    __device__ __forceinline__ void fetch_rows(char* lds, const char* rows) const {
         if constexpr (I < kHalfLoads) {
             constexpr int kBase = I % kOffsets, kImm = 1024 * (I - kBase);
-            if (kHalf >= 64 * I + 64 || lane < kHalf - 64 * I) to_lds<kImm>(lds + 1024 * kBase, rows, offset[kBase]);
-            fetch_rows<I + 1>(lane, lds, rows);
+            to_lds<kImm, kHalf >= 64 * I + 64 ? 64 : kHalf - 64 * I>(lds + 1024 * kBase, rows, offset[kBase]);
+            fetch_rows<I + 1>(lds, rows);
         }
     }
     // N bytes of a row from `at` on; N divides 16 or is a multiple of it where rows are turned.
@@ -368,15 +383,15 @@ struct Keys {
     uint32_t w[TYPE == kKvF16 ? 4 * NB : kBytes / 4];
     uint32_t d[TYPE == kKvF16 ? 1 : 2 * NB];  // scales [position 4g + r][block], two a dword
 
-    __device__ __forceinline__ void load(int lane, const char* chunk, int place, int page_size) {
+    __device__ __forceinline__ void load(int lane, const char* rows, int scales) {
         const int n = lane & 15, g = lane >> 4;
         if constexpr (TYPE == kKvF16) {
-            const char* p = chunk + (uint32_t)((place + n) * (64 * NB) + 16 * g);
+            const char* p = rows + (uint32_t)(n * (64 * NB) + 16 * g);
 #pragma unroll
             for (int b = 0; b < NB; ++b) __builtin_memcpy(w + 4 * b, __builtin_assume_aligned(p + 64 * b, 16), 16);
         } else {
-            load_bytes<kBytes>(w, chunk + (uint32_t)((place + n) * Side<TYPE, NB>::kFactor + g * kBytes));
-            load_bytes<8 * NB>(d, chunk + (uint32_t)(page_size * Side<TYPE, NB>::kFactor + (place + 4 * g) * (2 * NB)));
+            load_bytes<kBytes>(w, rows + (uint32_t)(n * Side<TYPE, NB>::kFactor + g * kBytes));
+            load_bytes<8 * NB>(d, rows + scales + (uint32_t)(4 * g * (2 * NB)));
         }
     }
     __device__ __forceinline__ void read(int lane, int h, const char* lds) {
@@ -428,13 +443,13 @@ struct Values {
     uint32_t w[8][kWords];
     uint32_t d[2][TYPE == kKvF16 ? 1 : 2 * NB];  // scales [half][position 4g + r][block]
 
-    __device__ __forceinline__ void load(int lane, int half, const char* chunk, int place, int page_size) {
+    __device__ __forceinline__ void load(int lane, int half, const char* rows, int scales) {
         const int n = lane & 15, g = lane >> 4;
-        const char* p = chunk + (uint32_t)((place + 4 * g) * Side<TYPE, NB>::kFactor + n * kBytes);
+        const char* p = rows + (uint32_t)(4 * g * Side<TYPE, NB>::kFactor + n * kBytes);
 #pragma unroll
         for (int r = 0; r < 4; ++r) load_bytes<kBytes>(w[4 * half + r], p + r * Side<TYPE, NB>::kFactor);
         if constexpr (TYPE != kKvF16)
-            load_bytes<8 * NB>(d[half], chunk + (uint32_t)(page_size * Side<TYPE, NB>::kFactor + (place + 4 * g) * (2 * NB)));
+            load_bytes<8 * NB>(d[half], rows + scales + (uint32_t)(4 * g * (2 * NB)));
     }
     __device__ __forceinline__ void read(int lane, const char* lds) {
         const int n = lane & 15, g = lane >> 4;
@@ -647,10 +662,11 @@ struct Shape {
 
 // Resources: the queries' parts lie in LDS, read again each step (two 16-byte reads a block), which leaves the
 // registers to the keys and values.
-// A piece of a tile: `count` steps of it from step `from` on.  part: its place if it is not the whole tile.
+// A piece of a tile: `count` steps of it from step `from` on.  slot: its place, or -1 for a whole tile.
 template <int KT, int VT, int NB, int RT>
-__device__ __forceinline__ void attend_piece(const AttendArgs& a, const SeqWork& w, int tile, int from, int count, char* lds, float* lc,
-                                             int head, float* part) {
+__device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int from, int count, char* lds, float* lc,
+                                             int head, int slot) {
+    const AttendArgs& a = launch_args();
     using S = Shape<KT, VT, NB, RT>;
     constexpr int kRows = 16 * RT, kDim = 32 * NB, kTiles = 2 * NB, kWaves = S::kWaves, kDepth = S::kDepth;
     constexpr bool kKeyBlocks = KT != kKvF16, kValBlocks = VT != kKvF16, kStaged = S::kStaged, kBiased = S::kBiased;
@@ -704,50 +720,43 @@ __device__ __forceinline__ void attend_piece(const AttendArgs& a, const SeqWork&
     const int ksteps = s1 > s0 + wave ? (s1 - s0 - wave + kWaves - 1) / kWaves : 0;
     const int start = w.base + kAtStep * (s0 + wave);
     const Mix mix;
-    const char* const kbase = a.k.base + (int64_t)head * a.p.page_size * Side<KT, NB>::kRow;
-    const char* const vbase = a.v.base + (int64_t)head * a.p.page_size * Side<VT, NB>::kRow;
-    // Lane 2 i + half: the page of step block + i, and the place in it.  A block of 32 steps is read anew after 30, before
-    // the steps that set out then.
-    int pages = -1, places = 0, block = 0;
-    uint64_t missing = 0;
+    // Lane 2 i + half: where the half's keys and values lie of step block + i, and how far their scales are from there.  A
+    // block of 32 steps is read anew after 30, before the steps that set out then.  A position that does not exist is
+    // read at page 0 and not seen.
+    int block = 0, kfar = 0, vfar = 0;
+    uint64_t krows = 0, vrows = 0, missing = 0;
     const auto read_pages = [&](int start_step) {
-        const int k = start_step + (lane >> 1), pos = start + kAtStep * kWaves * k + 16 * (lane & 1);
+        const AttendArgs& b = launch_args();
+        const int k = start_step + (lane >> 1), pos = start + kAtStep * kWaves * k + 16 * (lane & 1), size = b.p.page_size;
         block = start_step;
-        pages = k < ksteps ? kv_page(a.p, w.seq, pos) : -1;
-        places = k < ksteps ? (int)((uint32_t)pos % (uint32_t)a.p.page_size) : 0;
-        missing = __ballot(pages < 0);
+        const int page = k < ksteps ? kv_page(b.p, w.seq, pos) : -1, place = k < ksteps ? (int)((uint32_t)pos % (uint32_t)size) : 0;
+        missing = __ballot(page < 0);
+        krows = (uint64_t)b.k.base + max(page, 0) * b.k.stride + ((int64_t)head * size * Side<KT, NB>::kRow + place * Side<KT, NB>::kFactor);
+        vrows = (uint64_t)b.v.base + max(page, 0) * b.v.stride + ((int64_t)head * size * Side<VT, NB>::kRow + place * Side<VT, NB>::kFactor);
+        kfar = (size - place) * Side<KT, NB>::kFactor + place * Side<KT, NB>::kScale;
+        vfar = (size - place) * Side<VT, NB>::kFactor + place * Side<VT, NB>::kScale;
     };
-    const auto page_of = [&](int k, int h) { return lane_of(pages, 2 * (k - block) + h); };
-    const auto place_of = [&](int k, int h) { return lane_of(places, 2 * (k - block) + h); };
-    // A position that does not exist is read at page 0 and not seen.
-    const auto chunk_of = [&](const char* base, int64_t stride, int k, int h) {
-        const int pg = page_of(k, h);
-        return base + (pg < 0 ? 0 : pg * stride);
+    const auto rows_of = [&](uint64_t rows, int i) {
+        return (const char*)((uint64_t)(uint32_t)lane_of((int)(rows >> 32), i) << 32 | (uint32_t)lane_of((int)rows, i));
     };
     char* const ring = lds + S::kQueries + wave * S::kRing;
     const std::conditional_t<kStaged, Stage<KT, NB>, Nothing> kstage(lane);
     const std::conditional_t<kStaged, Stage<VT, NB>, Nothing> vstage(lane);
     Keys<KT, NB> keys[2];
     const auto fetch_keys = [&](int k) {
-        const char* const chunk[2] = {chunk_of(kbase, a.k.stride, k, 0), chunk_of(kbase, a.k.stride, k, 1)};
-        const int first[2] = {place_of(k, 0), place_of(k, 1)};
-        if constexpr (kStaged) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) kstage.fetch(lane, ring + k % kDepth * S::kKeys, h, chunk[h], first[h], a.p.page_size);
-        } else {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) keys[h].load(lane, chunk[h], first[h], a.p.page_size);
+        for (int h = 0; h < 2; ++h) {
+            const int i = 2 * (k - block) + h;
+            if constexpr (kStaged) kstage.fetch(lane, ring + k % kDepth * S::kKeys, h, rows_of(krows, i), lane_of(kfar, i));
+            else keys[h].load(lane, rows_of(krows, i), lane_of(kfar, i));
         }
     };
     const auto fetch_values = [&](int k, Values<VT, NB>& vals) {
-        const char* const chunk[2] = {chunk_of(vbase, a.v.stride, k, 0), chunk_of(vbase, a.v.stride, k, 1)};
-        const int first[2] = {place_of(k, 0), place_of(k, 1)};
-        if constexpr (kStaged) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) vstage.fetch(lane, ring + kDepth * S::kKeys + k % kDepth * S::kVals, h, chunk[h], first[h], a.p.page_size);
-        } else {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) vals.load(lane, h, chunk[h], first[h], a.p.page_size);
+        for (int h = 0; h < 2; ++h) {
+            const int i = 2 * (k - block) + h;
+            if constexpr (kStaged) vstage.fetch(lane, ring + kDepth * S::kKeys + k % kDepth * S::kVals, h, rows_of(vrows, i), lane_of(vfar, i));
+            else vals.load(lane, h, rows_of(vrows, i), lane_of(vfar, i));
         }
     };
     Values<VT, NB> vals;
@@ -1163,14 +1172,16 @@ __device__ __forceinline__ void attend_piece(const AttendArgs& a, const SeqWork&
     __syncthreads();
     if (wave < 2) put(wave);
     __syncthreads();
+    const AttendArgs& b = launch_args();
+    float* part = b.parts + ((int64_t)slot * b.p.nheads + head) * part_floats(kRows, kDim);
     for (int i = tid; i < rows * (kDim / 4); i += 64 * kWaves) {
         const int r = i / (kDim / 4), d = 4 * (i - r * (kDim / 4));
         const float most = __builtin_fmaxf(lm[0][r], lm[1][r]), e0 = beside(lm[0][r], most), e1 = beside(lm[1][r], most);
         const float sum = e0 * ll[0][r] + e1 * ll[1][r];
         float4_t f = e0 * *(const float4_t*)&so[0][r][d] + e1 * *(const float4_t*)&so[1][r][d];
-        if (!part) {
+        if (slot < 0) {
             f *= sum != 0.0f ? 1.0f / sum : 0.0f;
-            write_row(a, w.first, head, row0 + r, d, f, most, sum);
+            write_row(b, w.first, head, row0 + r, d, f, most, sum);
         } else {
             if (d == 0) {
                 part[r] = most;
@@ -1183,7 +1194,8 @@ __device__ __forceinline__ void attend_piece(const AttendArgs& a, const SeqWork&
 
 
 template <int KT, int VT, int NB, int RT>
-__global__ __launch_bounds__((64 * Shape<KT, VT, NB, RT>::kWaves), 2) void attend_kernel(AttendArgs a) {
+__global__ __launch_bounds__((64 * Shape<KT, VT, NB, RT>::kWaves), 2) void attend_kernel(AttendArgs) {
+    const AttendArgs& a = launch_args();
     using S = Shape<KT, VT, NB, RT>;
     constexpr int kRows = 16 * RT, kDim = 32 * NB;
     __shared__ __attribute__((aligned(16))) char lds[S::kBytes];
@@ -1200,8 +1212,8 @@ __global__ __launch_bounds__((64 * Shape<KT, VT, NB, RT>::kWaves), 2) void atten
         const int piece = at - tl.at, units = min(end - tl.at, tl.live) - piece;
         at = tl.at + tl.units;
         if (units <= 0) continue;
-        attend_piece<KT, VT, NB, RT>(a, w, tl.tile, piece << split.shift, units << split.shift, lds, lc, head,
-                                     units == tl.live ? nullptr : a.parts + piece_slot(a, split, tl, run, head) * part_floats(kRows, kDim));
+        attend_piece<KT, VT, NB, RT>(w, tl.tile, piece << split.shift, units << split.shift, lds, lc, head,
+                                     units == tl.live ? -1 : piece_slot(split, tl, run));
         __syncthreads();
     }
 }

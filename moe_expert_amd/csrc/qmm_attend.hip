@@ -65,7 +65,7 @@ __device__ __forceinline__ void join(const AttendArgs& a, const Split& split, co
         float4_t f = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 4
         for (int i = turn; i < pieces; i += E) {
-            const float* p = a.parts + piece_slot(a, split, t, from + i, head) * size;
+            const float* p = a.parts + ((int64_t)piece_slot(split, t, from + i) * a.p.nheads + head) * size;
             const float m = p[r], l = p[tile_rows + r];
             const float4_t o = *(const float4_t*)(p + 2 * tile_rows + r * dim + d);
             const float now = __builtin_fmaxf(most, m), old = beside(most, now), fresh = beside(m, now);
