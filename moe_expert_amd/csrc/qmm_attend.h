@@ -605,9 +605,6 @@ __device__ __forceinline__ int rows_or(int v) {
     return (int)r[0] | (int)r[1];
 }
 
-// 2^e for e in [-126, 127]
-__device__ __forceinline__ float power(int e) { return __builtin_bit_cast(float, (uint32_t)(e + 127) << 23); }
-
 __device__ __forceinline__ void store4(const float* v, void* p, int64_t i, int type, int vec) {
     if (vec && type == kF32) {
         *(float4_t*)((float*)p + i) = float4_t{v[0], v[1], v[2], v[3]};

@@ -25,9 +25,8 @@ struct KvPlace {
 __host__ __device__ constexpr int kv_factor_bytes(int type, int dim) { return type == kKvF16 ? 2 * dim : type == kKvQ8 ? dim : dim / 2; }
 __host__ __device__ constexpr int kv_row_bytes(int type, int dim) { return kv_factor_bytes(type, dim) + (type == kKvF16 ? 0 : dim / 16); }
 
-__device__ __forceinline__ float iq4nl_value(int i) {
-    return (float)(int8_t)((i & 8 ? 0x7159453526190D01ull : 0xF6EADDCFBFAD9881ull) >> (8 * (i & 7)));
-}
+// 2^e for e in [-126, 127]
+__device__ __forceinline__ float power(int e) { return __builtin_bit_cast(float, (uint32_t)(e + 127) << 23); }
 
 // The first and last + 1 token of sequence s.
 __device__ __forceinline__ void kv_segment(const KvPlace& p, int s, int& first, int& end) {
@@ -40,17 +39,35 @@ __device__ __forceinline__ void kv_segment(const KvPlace& p, int s, int& first, 
     end = min(max(p.seg_off[s + 1], first), p.ntok);
 }
 
-// The sequence of token t, or -1: how many sequences end at or before it, counted by the 16 lanes of a
-// row (each with the same t).
-__device__ __forceinline__ int kv_sequence16(const KvPlace& p, int t) {
-    if (!p.seg_off) return t < p.nseq ? t : -1;
-    int n = 0;
-    for (int i = threadIdx.x & 15; i < p.nseq; i += 16) n += min(max(p.seg_off[i + 1], 0), p.ntok) <= t ? 1 : 0;
-    n += dpp_i<0xB1>(n);
-    n += dpp_i<0x4E>(n);
-    n += dpp_i<0x141>(n);
-    n += dpp_i<0x140>(n);
-    return n < p.nseq && max(p.seg_off[n], 0) <= t ? n : -1;
+// The sequence of token t with the end of its new tokens and its length, or -1: one more than the sequences
+// that end at or before it.  By the 16 lanes of a row (each with the same t): the sixteenths of what is left until
+// it is 16 sequences, whose ends and lengths arrive together.
+__device__ __forceinline__ int sum16(int v) {
+    v += dpp_i<0xB1>(v);
+    v += dpp_i<0x4E>(v);
+    v += dpp_i<0x141>(v);
+    v += dpp_i<0x140>(v);
+    return v;
+}
+__device__ __forceinline__ int kv_sequence16(const KvPlace& p, int t, int& end, int& len) {
+    end = t + 1;
+    if (!p.seg_off) {
+        len = t < p.nseq ? p.lens[t] : 0;
+        return t < p.nseq ? t : -1;
+    }
+    const int i = threadIdx.x & 15;
+    int from = 0, n = p.nseq;  // the sequence is one of the n from `from` on, or none
+    while (n > 16) {
+        const int step = (n + 15) / 16, last = (i + 1) * step;
+        const int over = sum16(last < n && min(max(p.seg_off[from + last], 0), p.ntok) <= t ? 1 : 0) * step;
+        from += over;
+        n = min(step, n - over);
+    }
+    const int begin = p.seg_off[0], e = i < n ? min(max(p.seg_off[from + i + 1], 0), p.ntok) : 0, l = i < n ? p.lens[from + i] : 0;
+    const int over = sum16(i < n && e <= t ? 1 : 0), at = 4 * ((threadIdx.x & 48) + min(over, 15));
+    end = __builtin_amdgcn_ds_bpermute(at, e);
+    len = __builtin_amdgcn_ds_bpermute(at, l);
+    return over < n && begin <= t ? from + over : -1;
 }
 
 // The page of position pos of sequence s, or -1 where there is none.
