@@ -726,7 +726,8 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
         const AttendArgs& b = launch_args();
         const int k = start_step + (lane >> 1), pos = start + kAtStep * kWaves * k + 16 * (lane & 1), size = b.p.page_size;
         block = start_step;
-        const int page = k < ksteps ? kv_page(b.p, w.seq, pos) : -1, place = k < ksteps ? (int)((uint32_t)pos % (uint32_t)size) : 0;
+        int place;
+        const int page = kv_page(b.p, w.seq, k < ksteps ? pos : -1, place);
         missing = __ballot(page < 0);
         krows = (uint64_t)b.k.base + max(page, 0) * b.k.stride + ((int64_t)head * size * Side<KT, NB>::kRow + place * Side<KT, NB>::kFactor);
         vrows = (uint64_t)b.v.base + max(page, 0) * b.v.stride + ((int64_t)head * size * Side<VT, NB>::kRow + place * Side<VT, NB>::kFactor);

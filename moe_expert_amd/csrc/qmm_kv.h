@@ -20,7 +20,20 @@ struct KvPlace {
     int64_t ldpages;
     int64_t npages;
     int max_pages, page_size, nheads, dim, nseq, ntok;
+    uint32_t per_head, per_page;  // kv_per(nheads), kv_per(page_size)
 };
+
+// Quotients of numbers up to 2^31 by n through 2^32 / n, rounded down and below 2^32: at most one too low.
+inline uint32_t kv_per(int n) { return n == 1 ? ~0u : (uint32_t)((1ull << 32) / (unsigned)n); }
+__device__ __forceinline__ uint32_t kv_divide(uint32_t v, uint32_t n, uint32_t per, uint32_t& rest) {
+    uint32_t q = (uint32_t)(((uint64_t)v * per) >> 32);
+    rest = v - q * n;
+    if (rest >= n) {
+        rest -= n;
+        ++q;
+    }
+    return q;
+}
 
 __host__ __device__ constexpr int kv_factor_bytes(int type, int dim) { return type == kKvF16 ? 2 * dim : type == kKvQ8 ? dim : dim / 2; }
 __host__ __device__ constexpr int kv_row_bytes(int type, int dim) { return kv_factor_bytes(type, dim) + (type == kKvF16 ? 0 : dim / 16); }
@@ -63,18 +76,23 @@ __device__ __forceinline__ int kv_sequence16(const KvPlace& p, int t, int& end, 
         from += over;
         n = min(step, n - over);
     }
-    const int begin = p.seg_off[0], e = i < n ? min(max(p.seg_off[from + i + 1], 0), p.ntok) : 0, l = i < n ? p.lens[from + i] : 0;
+    const int at_most = from + min(i, max(n, 1) - 1);  // (nseq > 0: all three arrive together)
+    const int begin = p.seg_off[0], l = p.lens[min(at_most, p.nseq - 1)], e = min(max(p.seg_off[min(at_most, p.nseq - 1) + 1], 0), p.ntok);
     const int over = sum16(i < n && e <= t ? 1 : 0), at = 4 * ((threadIdx.x & 48) + min(over, 15));
     end = __builtin_amdgcn_ds_bpermute(at, e);
     len = __builtin_amdgcn_ds_bpermute(at, l);
     return over < n && begin <= t ? from + over : -1;
 }
 
-// The page of position pos of sequence s, or -1 where there is none.
-__device__ __forceinline__ int kv_page(const KvPlace& p, int s, int64_t pos) {
-    if (pos < 0 || pos >= (int64_t)p.max_pages * p.page_size) return -1;
-    const int pg = p.pages[(int64_t)s * p.ldpages + (uint32_t)pos / (uint32_t)p.page_size];
-    return pg >= 0 && pg < p.npages ? pg : -1;
+// The page of position pos of sequence s and the place there, or -1 (and a place) where there is none; s in
+// [0, nseq).
+__device__ __forceinline__ int kv_page(const KvPlace& p, int s, int64_t pos, int& place) {
+    const bool in = pos >= 0 && pos < (int64_t)p.max_pages * p.page_size;
+    uint32_t rest;
+    const uint32_t at = kv_divide(in ? (uint32_t)pos : 0, p.page_size, p.per_page, rest);
+    place = (int)rest;
+    const int pg = p.pages[(int64_t)s * p.ldpages + at];
+    return in && pg >= 0 && pg < p.npages ? pg : -1;
 }
 
 // The chunk of a page and head.

@@ -37,7 +37,8 @@ inline int kv_place(KvPlace& p, const qmm_kv_cache* c, const int32_t* pages, int
     if (ntok > kKvMaxTokens || nseq > kKvMaxSeq || max_pages > kKvMaxLength || max_pages * c->page_size > kKvMaxLength) return QMM_EUNSUPPORTED;
     if (ntok && nseq && (!pages || !lens)) return QMM_EINVAL;
     if (!aligned(pages, 4) || !aligned(lens, 4) || !aligned(seg_off, 4)) return QMM_EALIGN;
-    p = KvPlace{pages, lens, seg_off, ldpages, c->npages, (int)max_pages, c->page_size, c->nheads, c->head_dim, nseq, (int)ntok};
+    p = KvPlace{pages, lens, seg_off, ldpages, c->npages, (int)max_pages, c->page_size, c->nheads, c->head_dim, nseq, (int)ntok,
+                kv_per(c->nheads), kv_per(c->page_size)};
     return QMM_OK;
 }
 
