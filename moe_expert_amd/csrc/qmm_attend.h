@@ -31,11 +31,17 @@ constexpr int kAtLds = 80 * 1024 - 512;  // bytes of LDS of a workgroup of which
 constexpr int kAtStep = 32;      // positions a step
 constexpr int kAtInline = 256;   // sequences that a workgroup plans by itself; beyond, a launch of its own
 
+// What a workgroup leaves of a tile that goes on beyond it: the tile's pieces (0: none) and which of them, and its rows.
+struct Piece {
+    int count, mine, first, rows;  // first: of the sequence's new tokens;  rows: the tile's, and 64 times the tile
+};
+
 struct AttendArgs {
     const void* q;
     void* out;
     float* lse;
     float* parts;            // pieces: [slot][head][rows (m), rows (l), rows * dim]
+    Piece* pieces;           // [slot], or null: no tile has more than one piece
     const int32_t* plan;     // of attend_plan_kernel, or null
     int64_t ldq, ldo;
     KvSide k, v;
@@ -45,6 +51,7 @@ struct AttendArgs {
     int window;                       // 0: none
     int target, least;                // workgroups a head of keys, steps that a tile counts for at least
     int vec;                          // out: groups of four values are aligned
+    uint32_t per_group;               // kv_per(group)
 };
 
 // The kernel's argument where it is needed: read again from its segment rather than kept in scalar registers, of which
@@ -222,9 +229,6 @@ __device__ __forceinline__ Tile find_tile(const AttendArgs& a, const Split& s, i
     t.at = before + t.tile * t.units;
     return t;
 }
-
-// The place of a tile's piece in workgroup `run` (of its head): the second, if the tile begins there.
-__device__ __forceinline__ int piece_slot(const Split& s, const Tile& t, int run) { return 2 * run + (t.at >= run * s.len ? 1 : 0); }
 
 // ------------------------------------------------------------------ values as the matrix instructions take them
 
@@ -621,7 +625,8 @@ __device__ __forceinline__ void store4(const float* v, void* p, int64_t i, int t
 
 // Four dims of row r (of its sequence's) of a head of keys, and with the first of them the row's lse.
 __device__ __forceinline__ void write_row(const AttendArgs& a, int first, int head, int r, int d, float4_t f, float most, float sum) {
-    const int token = r / a.group, h = head * a.group + r - token * a.group;
+    uint32_t rest;
+    const int token = (int)kv_divide(r, a.group, a.per_group, rest), h = head * a.group + (int)rest;
     const float v[4] = {f[0], f[1], f[2], f[3]};
     store4(v, a.out, (first + token) * a.ldo + (int64_t)h * a.p.dim + d, a.otype, a.vec);
     if (d == 0 && a.lse)
@@ -648,13 +653,15 @@ struct Shape {
     static constexpr int kKeys = kStaged ? Stage<KT, NB>::kBytes : 0, kVals = kStaged ? Stage<VT, NB>::kBytes : 0;
     // Keys of a block format enter as u 2^-24, their sums begin at -128 2^-24 times the queries' sum.  Values do where the registers hold the sums of their weights beside the others.
     static constexpr bool kBiased = VT != kKvF16 && NB * RT <= 4;
-    static constexpr int kQueries = RT * NB * (2 * 64 + (kStaged ? 16 : 0)) * 16;
+    static constexpr int kQueries = RT * NB * 2 * 64 * 16;
     static constexpr int kWaves = kQueries + 4 * (kKeys + kVals) > kAtLds ? 8 : 4;
     static constexpr int kDepth = kStaged && kWaves == 4 && kQueries + 8 * (kKeys + kVals) <= kAtLds ? 2 : 1;
     static constexpr int kRing = kDepth * (kKeys + kVals);  // bytes a wave
     static constexpr int kRows = 16 * RT, kPitch = 32 * NB + 4;
-    static constexpr int kSums = kWaves / 2 * kRows * (kPitch + 2) * 4;  // of half the waves, at the end
-    static constexpr int kBytes = kQueries + (kWaves * kRing > kSums ? kWaves * kRing : kSums);
+    static constexpr int kSums = kWaves * kRows * (kPitch + 2) * 4;  // of the waves, at the end, in place of all else
+    static constexpr int kOdd = KT == kKvF16 && VT == kKvF16 ? kRows * kAtStep * 4 + 64 * NB : 0;  // bytes a wave: values that are not finite
+    static constexpr int kLoop = kQueries + kWaves * (kRing > kOdd ? kRing : kOdd);
+    static constexpr int kBytes = kLoop > kSums ? kLoop : kSums;
 };
 
 // Resources: the queries' parts lie in LDS, read again each step (two 16-byte reads a block), which leaves the
@@ -670,22 +677,24 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
     // Binary16 keys are read into registers, a step ahead: before the weights, or after the values where the registers
     // do not hold both.
     constexpr bool kEarly = NB < 8;
-    // Queries, then what is on its way, wave by wave; at the end the sums of half the waves, and of binary16 values a
-    // place a wave for odd ones until then.
+    // Queries, then what is on its way, wave by wave; at the end the sums of the waves in their place.
     auto& lq = *(uint32_t(*)[RT][NB][2][64][4])lds;
-    auto& lb = *(float(*)[RT][NB][16][4])(lds + sizeof(lq));  // where a block's sums begin, for the four positions of a lane
-    auto& so = *(float(*)[kWaves / 2][kRows][S::kPitch])(lds + S::kQueries);
-    auto& lm = *(float(*)[kWaves / 2][kRows])(lds + S::kQueries + sizeof(so));
-    auto& ll = *(float(*)[kWaves / 2][kRows])(lds + S::kQueries + sizeof(so) + sizeof(lm));
-    static_assert(kValBlocks || S::kSums / kWaves >= kRows * kAtStep * 4 + kDim * 2, "weights and a position's values");
+    auto& so = *(float(*)[kWaves][kRows][S::kPitch])lds;
+    auto& lm = *(float(*)[kWaves][kRows])(lds + sizeof(so));
+    auto& ll = *(float(*)[kWaves][kRows])(lds + sizeof(so) + sizeof(lm));
+    static_assert(sizeof(so) + sizeof(lm) + sizeof(ll) == S::kSums, "the sums' place");
     int tid = threadIdx.x;
     asm volatile("" : "+v"(tid));  // what depends on it is not kept from one piece to the next
     const int lane = tid & 63, n = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     // The rows of the tile: lane n's, the positions [rlo, rhi) that they see, and the same over all of them.
     const int row0 = tile * kRows, rows = min(kRows, w.n * a.group - row0), cap = a.p.max_pages * a.p.page_size;
+    const auto token_of = [&](int r) {
+        uint32_t rest;
+        return (int)kv_divide(r, a.group, a.per_group, rest);
+    };
     const auto low = [&](int pos) { return a.window > 0 && pos >= a.window ? pos - a.window + 1 : 0; };
-    const int pos0 = w.len - w.n + row0 / a.group, pos1 = w.len - w.n + (row0 + rows - 1) / a.group;
+    const int pos0 = w.len - w.n + token_of(row0), pos1 = w.len - w.n + token_of(row0 + rows - 1);
     const int lo_min = low(pos0), lo_max = low(pos1), hi_min = min(pos0 + 1, cap), hi_max = min(pos1 + 1, cap);
 
     // The queries, 16 threads a row: read before the keys set out, since loads return in order; then scaled, their two
@@ -695,7 +704,7 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
     uint32_t raw[RT][NB][2];
 #pragma unroll
     for (int x = 0; x < RT; ++x) {
-        const int r = min(16 * x + tid / 16, rows - 1), j = tid & 15, tok = (row0 + r) / a.group;
+        const int r = min(16 * x + tid / 16, rows - 1), j = tid & 15, tok = token_of(row0 + r);
         const int64_t at = (w.first + tok) * a.ldq + (int64_t)(head * a.group + row0 + r - tok * a.group) * kDim;
         if (a.qtype == kF32) {
 #pragma unroll
@@ -764,10 +773,6 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
         fetch_keys(0);
         if constexpr (kStaged) {
             fetch_values(0, vals);
-            if (kDepth > 1 && ksteps > 1) {
-                fetch_keys(1);
-                fetch_values(1, vals);
-            }
         }
     }
 
@@ -797,17 +802,12 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
             two_parts(mix, v[b][0] * up, v[b][1] * up, hi, lo);
             lq[x][b][0][16 * (j / 4) + r % 16][j % 4] = hi;
             lq[x][b][1][16 * (j / 4) + r % 16][j % 4] = lo;
-            if constexpr (kKeyBlocks) {
-                const half2_t h = __builtin_bit_cast(half2_t, hi), l = __builtin_bit_cast(half2_t, lo);
-                float sum = ((float)h.x + (float)h.y) + ((float)l.x + (float)l.y);
-                sum += dpp<0xB1>(sum);
-                sum += dpp<0x4E>(sum);
-                sum += dpp<0x141>(sum);
-                sum += dpp<0x140>(sum);
-                if (j < 4) lb[x][b][r % 16][j] = sum * -power(7 - 24);
-            }
         }
         if (j == 0) lc[r] = power(e - 14 + (kKeyBlocks ? 24 : 0));
+    }
+    if (kStaged && kDepth > 1 && ksteps > 1) {
+        fetch_keys(1);
+        fetch_values(1, vals);
     }
     __syncthreads();
 
@@ -819,7 +819,7 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
 #pragma unroll
     for (int x = 0; x < RT; ++x) {
         const int r = 16 * x + n;
-        const int pos = w.len - w.n + (row0 + r) / a.group;
+        const int pos = w.len - w.n + token_of(row0 + r);
         rlo[x] = low(pos);
         rhi[x] = r < rows ? min(pos + 1, cap) : 0;
         c[x] = lc[r];
@@ -833,7 +833,8 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
 #pragma unroll
         for (int b = 0; b < (kBiased ? NB : 1); ++b) weights[x][b] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
     }
-    const half8_t ones = as_half8(0x00800080u, 0x00800080u, 0x00800080u, 0x00800080u);
+    const half8_t bias = as_half8(0x00800080u, 0x00800080u, 0x00800080u, 0x00800080u);    // 128 2^-24
+    const half8_t minus = as_half8(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);  // -128 2^-24
     int least = 1;  // the least of the rows' bounds
     const auto queries = [&](int x, int b, int part) { return __builtin_bit_cast(half8_t, *(const u32x4*)lq[x][b][part][lane]); };
 
@@ -871,11 +872,15 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
 #pragma unroll
                 for (int x = 0; x < RT; ++x) {
                     const half8_t qh = queries(x, b, 0), ql = queries(x, b, 1);
+                    float4_t begin = {0.0f, 0.0f, 0.0f, 0.0f};
+                    if constexpr (kKeyBlocks) {
+                        begin = __builtin_amdgcn_mfma_f32_16x16x32_f16(minus, ql, begin, 0, 0, 0);
+                        begin = __builtin_amdgcn_mfma_f32_16x16x32_f16(minus, qh, begin, 0, 0, 0);
+                    }
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         if constexpr (kKeyBlocks) {
-                            float4_t u = *(const float4_t*)lb[x][b][n];
-                            u = __builtin_amdgcn_mfma_f32_16x16x32_f16(kb[h], ql, u, 0, 0, 0);
+                            float4_t u = __builtin_amdgcn_mfma_f32_16x16x32_f16(kb[h], ql, begin, 0, 0, 0);
                             u = __builtin_amdgcn_mfma_f32_16x16x32_f16(kb[h], qh, u, 0, 0, 0);
 #pragma unroll
                             for (int r = 0; r < 4; ++r) z[x][4 * h + r] = __builtin_fmaf(u[r], keys[h].scale(r, b), z[x][4 * h + r]);
@@ -1036,7 +1041,7 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
                 }
             }
             if (__any(odd)) {
-                float* weight = (float*)(lds + S::kQueries + wave * (S::kSums / kWaves / 16 * 16));
+                float* weight = (float*)(lds + S::kQueries + wave * S::kOdd);
                 uint32_t* row = (uint32_t*)(weight + kRows * kAtStep);
 #pragma unroll
                 for (int x = 0; x < RT; ++x)
@@ -1108,8 +1113,8 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
                 if (t % 2 == 0) {
 #pragma unroll
                     for (int x = 0; x < RT; ++x) {
-                        weights[x][t / 2] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ones, pl[x], weights[x][t / 2], 0, 0, 0);
-                        weights[x][t / 2] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ones, ph[x], weights[x][t / 2], 0, 0, 0);
+                        weights[x][t / 2] = __builtin_amdgcn_mfma_f32_16x16x32_f16(bias, pl[x], weights[x][t / 2], 0, 0, 0);
+                        weights[x][t / 2] = __builtin_amdgcn_mfma_f32_16x16x32_f16(bias, ph[x], weights[x][t / 2], 0, 0, 0);
                     }
                 }
             }
@@ -1128,7 +1133,8 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
         }
     }
 
-    // The waves' results, in base-2 units of the scores: half the waves to the other half through LDS, until two are left, then those.
+    // The waves' results, in base-2 units of the scores, to LDS; then four dims of a row a lane.
+    const int active = min(kWaves, max(s1 - s0, 1));  // waves with a step (one at least: the zeros of none)
 #pragma unroll
     for (int x = 0; x < RT; ++x) {
         l[x] = rows_sum(l[x]) * (kValBlocks ? 1.0f : power(-14));
@@ -1137,46 +1143,35 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) o[x][t] = (kBiased ? o[x][t] - weights[x][kBiased ? t / 2 : 0] : o[x][t]) * back;
     }
-    const auto put = [&](int at) {
-#pragma unroll
-        for (int x = 0; x < RT; ++x) {
-            if (g == 0) {
-                lm[at][16 * x + n] = m[x];
-                ll[at][16 * x + n] = l[x];
-            }
-#pragma unroll
-            for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) so[at][16 * x + n][Values<VT, NB>::dim(t, 4 * g + r)] = o[x][t][r];
-        }
-    };
-#pragma unroll
-    for (int half = kWaves / 2; half >= 2; half /= 2) {
-        __syncthreads();
-        if (wave >= half && wave < 2 * half) put(wave - half);
-        __syncthreads();
-        if (wave >= half) continue;
-#pragma unroll
-        for (int x = 0; x < RT; ++x) {
-            const float other = lm[wave][16 * x + n], most = __builtin_fmaxf(m[x], other), mine = beside(m[x], most), its = beside(other, most);
-            m[x] = most;
-            l[x] = l[x] * mine + ll[wave][16 * x + n] * its;
-#pragma unroll
-            for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) o[x][t][r] = o[x][t][r] * mine + so[wave][16 * x + n][Values<VT, NB>::dim(t, 4 * g + r)] * its;
-        }
-    }
     __syncthreads();
-    if (wave < 2) put(wave);
+#pragma unroll
+    for (int x = 0; x < RT; ++x) {
+        if (wave >= active || 16 * x + n >= rows) continue;
+        if (g == 0) {
+            lm[wave][16 * x + n] = m[x];
+            ll[wave][16 * x + n] = l[x];
+        }
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) so[wave][16 * x + n][Values<VT, NB>::dim(t, 4 * g + r)] = o[x][t][r];
+    }
     __syncthreads();
     const AttendArgs& b = launch_args();
     float* part = b.parts + ((int64_t)slot * b.p.nheads + head) * part_floats(kRows, kDim);
     for (int i = tid; i < rows * (kDim / 4); i += 64 * kWaves) {
         const int r = i / (kDim / 4), d = 4 * (i - r * (kDim / 4));
-        const float most = __builtin_fmaxf(lm[0][r], lm[1][r]), e0 = beside(lm[0][r], most), e1 = beside(lm[1][r], most);
-        const float sum = e0 * ll[0][r] + e1 * ll[1][r];
-        float4_t f = e0 * *(const float4_t*)&so[0][r][d] + e1 * *(const float4_t*)&so[1][r][d];
+        float most = -INFINITY, sum = 0.0f;
+        float4_t f = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int y = 0; y < kWaves; ++y) most = y < active ? __builtin_fmaxf(most, lm[y][r]) : most;
+#pragma unroll
+        for (int y = 0; y < kWaves; ++y) {
+            if (y >= active) break;
+            const float weight = beside(lm[y][r], most);
+            sum += weight * ll[y][r];
+            f += weight * *(const float4_t*)&so[y][r][d];
+        }
         if (slot < 0) {
             f *= sum != 0.0f ? 1.0f / sum : 0.0f;
             write_row(b, w.first, head, row0 + r, d, f, most, sum);
@@ -1190,7 +1185,6 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
     }
 }
 
-
 template <int KT, int VT, int NB, int RT>
 __global__ __launch_bounds__((64 * Shape<KT, VT, NB, RT>::kWaves), 2) void attend_kernel(AttendArgs) {
     const AttendArgs& a = launch_args();
@@ -1198,11 +1192,13 @@ __global__ __launch_bounds__((64 * Shape<KT, VT, NB, RT>::kWaves), 2) void atten
     constexpr int kRows = 16 * RT, kDim = 32 * NB;
     __shared__ __attribute__((aligned(16))) char lds[S::kBytes];
     __shared__ float lc[kRows];
-    const int head = (int)(blockIdx.x % (uint32_t)a.p.nheads);
-    const int run = (int)(blockIdx.x / (uint32_t)a.p.nheads);
+    uint32_t head;
+    const int run = (int)kv_divide(blockIdx.x, a.p.nheads, a.p.per_head, head);
     SeqWork mine;
     const Split split = find_split(a, kRows, mine);
     const int begin = run * split.len, end = min(begin + split.len, split.all);
+    const bool tells = a.pieces && head == 0 && threadIdx.x == 0;
+    if (tells) a.pieces[2 * run].count = a.pieces[2 * run + 1].count = 0;
     for (int at = begin; at < end;) {
         if (at > begin && !a.plan) mine = lane_work(a, threadIdx.x & 63, kRows);  // (not kept beside the sums)
         const Tile tl = find_tile(a, split, at, kRows, mine);
@@ -1210,8 +1206,14 @@ __global__ __launch_bounds__((64 * Shape<KT, VT, NB, RT>::kWaves), 2) void atten
         const int piece = at - tl.at, units = min(end - tl.at, tl.live) - piece;
         at = tl.at + tl.units;
         if (units <= 0) continue;
-        attend_piece<KT, VT, NB, RT>(w, tl.tile, piece << split.shift, units << split.shift, lds, lc, head,
-                                     units == tl.live ? -1 : piece_slot(split, tl, run));
+        int slot = -1;
+        if (units != tl.live) {
+            // The second of the two, if the tile begins here.
+            const int from = tl.at / split.len;
+            slot = 2 * run + (run == from ? 1 : 0);
+            if (tells) a.pieces[slot] = Piece{(tl.at + tl.live - 1) / split.len - from + 1, run - from, w.first, tl.tile << 6 | min(kRows, w.n * a.group - tl.tile * kRows)};
+        }
+        attend_piece<KT, VT, NB, RT>(w, tl.tile, piece << split.shift, units << split.shift, lds, lc, (int)head, slot);
         __syncthreads();
     }
 }

@@ -53,19 +53,19 @@ __global__ __launch_bounds__(1024) void attend_plan_kernel(AttendArgs a, int row
 
 // The pieces of a tile joined, in their order, by as many workgroups as it has pieces: they share the tile's groups of
 // four dims.  A group's pieces go to E lanes of a wave, each every E-th of them, lanes of neighbouring groups
-// beside each other.  Bound: two loads one after the other (the sequences, the pieces), 4-5 us.
+// beside each other.  Bound: two loads one after the other (what the pass told, the pieces).
 template <int E>
-__device__ __forceinline__ void join(const AttendArgs& a, const Split& split, const Tile& t, int from, int pieces, int mine, int head, int tile_rows) {
-    const int dim = a.p.dim, row0 = t.tile * tile_rows, rows = min(tile_rows, t.w.n * a.group - row0), quads = rows * (dim / 4);
+__device__ __forceinline__ void join(const AttendArgs& a, const Piece& t, int run, int head, int tile_rows) {
+    const int dim = a.p.dim, row0 = (t.rows >> 6) * tile_rows, rows = t.rows & 63, quads = rows * (dim / 4), from = run - t.mine;
     const int lane = threadIdx.x & 63, turn = lane / (64 / E);
     const int64_t size = part_floats(tile_rows, dim);
-    for (int u = (mine * 4 + (int)(threadIdx.x >> 6)) * (64 / E); u < quads; u += pieces * 4 * (64 / E)) {
+    for (int u = (t.mine * 4 + (int)(threadIdx.x >> 6)) * (64 / E); u < quads; u += t.count * 4 * (64 / E)) {
         const int at = min(u + lane % (64 / E), quads - 1), r = at / (dim / 4), d = 4 * (at - r * (dim / 4));
         float most = -INFINITY, sum = 0.0f;
         float4_t f = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 4
-        for (int i = turn; i < pieces; i += E) {
-            const float* p = a.parts + ((int64_t)piece_slot(split, t, from + i) * a.p.nheads + head) * size;
+        for (int i = turn; i < t.count; i += E) {
+            const float* p = a.parts + ((int64_t)(2 * (from + i) + (i ? 0 : 1)) * a.p.nheads + head) * size;
             const float m = p[r], l = p[tile_rows + r];
             const float4_t o = *(const float4_t*)(p + 2 * tile_rows + r * dim + d);
             const float now = __builtin_fmaxf(most, m), old = beside(most, now), fresh = beside(m, now);
@@ -84,24 +84,20 @@ __device__ __forceinline__ void join(const AttendArgs& a, const Split& split, co
         }
         if (turn == 0 && u + lane < quads) {
             f *= sum != 0.0f ? 1.0f / sum : 0.0f;
-            write_row(a, t.w.first, head, row0 + r, d, f, most, sum);
+            write_row(a, t.first, head, row0 + r, d, f, most, sum);
         }
     }
 }
 
+// blockIdx.y: the workgroup's piece of a tile that began before it, or of one that begins there.
 __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, int tile_rows) {
-    const int head = (int)(blockIdx.x % (uint32_t)a.p.nheads), run = (int)(blockIdx.x / (uint32_t)a.p.nheads);
-    SeqWork mine;
-    const Split split = find_split(a, tile_rows, mine);
-    // The tile that goes on from the workgroup before, or the one that begins here and goes on.
-    const int begin = run * split.len, end = begin + split.len;
-    if (blockIdx.y ? end >= split.all : !run || begin >= split.all) return;
-    const Tile t = find_tile(a, split, blockIdx.y ? end - 1 : begin, tile_rows, mine);
-    if (blockIdx.y ? t.at < begin || t.at + t.live <= end : t.at >= begin || t.at + t.live <= begin) return;
-    const int from = t.at / split.len, pieces = (t.at + t.live - 1) / split.len - from + 1;
-    if (pieces <= 4) join<1>(a, split, t, from, pieces, run - from, head, tile_rows);
-    else if (pieces <= 64) join<8>(a, split, t, from, pieces, run - from, head, tile_rows);
-    else join<16>(a, split, t, from, pieces, run - from, head, tile_rows);
+    uint32_t head;
+    const int run = (int)kv_divide(blockIdx.x, a.p.nheads, a.p.per_head, head);
+    const Piece t = a.pieces[2 * run + blockIdx.y];
+    if (t.count == 0) return;
+    if (t.count <= 4) join<1>(a, t, run, (int)head, tile_rows);
+    else if (t.count <= 64) join<8>(a, t, run, (int)head, tile_rows);
+    else join<16>(a, t, run, (int)head, tile_rows);
 }
 
 }  // namespace qmm
@@ -122,8 +118,8 @@ struct AttendShape {
     int rt;          // 16-row tiles a workgroup
     int target;      // workgroups a head of keys, at most
     bool split;      // a tile can have more than one piece
-    size_t bytes;    // of the workspace: pieces, then the plan
-    size_t plan;     // its offset
+    size_t bytes;    // of the workspace: pieces, what is told of them, the plan
+    size_t told, plan;  // their offsets
 };
 
 int attend_shape(AttendShape& s, const qmm_kv_cache* c, const int32_t* pages, int64_t ldpages, int64_t max_pages,
@@ -142,7 +138,8 @@ int attend_shape(AttendShape& s, const qmm_kv_cache* c, const int32_t* pages, in
     s.target = (int)std::max(std::min((int64_t)(kAtTarget / c->nheads), line), (int64_t)1);
     s.split = steps > kAtLeast || tiles > s.target;
     // (sized for 32 rows where a call of other proportions would take them)
-    s.plan = s.split ? (size_t)(2 * s.target * c->nheads * part_floats(wide ? 32 : 16, c->head_dim) * 4 + 15) & ~(size_t)15 : 0;
+    s.told = s.split ? (size_t)(2 * s.target * c->nheads * part_floats(wide ? 32 : 16, c->head_dim) * 4) : 0;
+    s.plan = s.told + (s.split ? 2 * s.target * sizeof(Piece) : 0);
     s.bytes = s.plan + (nseq > kAtInline ? (size_t)(nseq + 4) * 4 : 0);
     s.bytes = s.bytes < 16 ? 16 : s.bytes;
     return QMM_OK;
@@ -176,6 +173,7 @@ extern "C" int qmm_kv_attend(const qmm_kv_cache* c, const int32_t* pages, int64_
     a.out = out;
     a.lse = lse;
     a.parts = (float*)ws;
+    a.pieces = s.split ? (Piece*)((char*)ws + s.told) : nullptr;
     a.plan = nseq > kAtInline ? (const int32_t*)((char*)ws + s.plan) : nullptr;
     a.ldq = ldq;
     a.ldo = ldo;
@@ -184,6 +182,7 @@ extern "C" int qmm_kv_attend(const qmm_kv_cache* c, const int32_t* pages, int64_
     a.p = s.p;
     a.nheads = nheads;
     a.group = nheads / c->nheads;
+    a.per_group = kv_per(a.group);
     a.qtype = qtype;
     a.otype = otype;
     a.scale = (float)((double)scale * 1.4426950408889634);
