@@ -452,8 +452,6 @@ struct Values {
         const char* p = rows + (uint32_t)(4 * g * Side<TYPE, NB>::kFactor + n * kBytes);
 #pragma unroll
         for (int r = 0; r < 4; ++r) load_bytes<kBytes>(w[4 * half + r], p + r * Side<TYPE, NB>::kFactor);
-        if constexpr (TYPE != kKvF16)
-            load_bytes<8 * NB>(d[half], rows + scales + (uint32_t)(4 * g * (2 * NB)));
     }
     __device__ __forceinline__ void read(int lane, const char* lds) {
         const int n = lane & 15, g = lane >> 4;
@@ -646,16 +644,19 @@ struct Nothing {
 };
 
 // How a pair of formats, a width and a number of row tiles are run: waves of a workgroup, whether keys and values pass
-// through LDS on their way (block formats do, if the keys are one), and how many steps ahead they set out.
+// through LDS on their way (block formats do), and how many steps ahead they set out.  Binary16 keys are read into
+// registers, a step ahead: before the weights, or after the values where the registers do not hold both.
 template <int KT, int VT, int NB, int RT>
 struct Shape {
     static constexpr bool kStaged = KT != kKvF16;
-    static constexpr int kKeys = kStaged ? Stage<KT, NB>::kBytes : 0, kVals = kStaged ? Stage<VT, NB>::kBytes : 0;
+    static constexpr int kKeys = kStaged ? Stage<KT, NB>::kBytes : 0, kVals = VT != kKvF16 ? Stage<VT, NB>::kBytes : 0;
     // Keys of a block format enter as u 2^-24, their sums begin at -128 2^-24 times the queries' sum.  Values do where the registers hold the sums of their weights beside the others.
     static constexpr bool kBiased = VT != kKvF16 && NB * RT <= 4;
     static constexpr int kQueries = RT * NB * 2 * 64 * 16;
     static constexpr int kWaves = kQueries + 4 * (kKeys + kVals) > kAtLds ? 8 : 4;
-    static constexpr int kDepth = kStaged && kWaves == 4 && kQueries + 8 * (kKeys + kVals) <= kAtLds ? 2 : 1;
+    static constexpr bool kTwo = kWaves == 4 && kQueries + 8 * (kKeys + kVals) <= kAtLds;
+    static constexpr bool kEarly = !kStaged && (VT == kKvF16 ? NB < 8 : NB * RT <= 4) && kTwo;
+    static constexpr int kDepth = kTwo && (kStaged || kEarly) ? 2 : 1;
     static constexpr int kRing = kDepth * (kKeys + kVals);  // bytes a wave
     static constexpr int kRows = 16 * RT, kPitch = 32 * NB + 4;
     static constexpr int kSums = kWaves * kRows * (kPitch + 2) * 4;  // of the waves, at the end, in place of all else
@@ -674,9 +675,7 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
     using S = Shape<KT, VT, NB, RT>;
     constexpr int kRows = 16 * RT, kDim = 32 * NB, kTiles = 2 * NB, kWaves = S::kWaves, kDepth = S::kDepth;
     constexpr bool kKeyBlocks = KT != kKvF16, kValBlocks = VT != kKvF16, kStaged = S::kStaged, kBiased = S::kBiased;
-    // Binary16 keys are read into registers, a step ahead: before the weights, or after the values where the registers
-    // do not hold both.
-    constexpr bool kEarly = NB < 8;
+    constexpr bool kEarly = S::kEarly;
     // Queries, then what is on its way, wave by wave; at the end the sums of the waves in their place.
     auto& lq = *(uint32_t(*)[RT][NB][2][64][4])lds;
     auto& so = *(float(*)[kWaves][kRows][S::kPitch])lds;
@@ -748,7 +747,7 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
     };
     char* const ring = lds + S::kQueries + wave * S::kRing;
     const std::conditional_t<kStaged, Stage<KT, NB>, Nothing> kstage(lane);
-    const std::conditional_t<kStaged, Stage<VT, NB>, Nothing> vstage(lane);
+    const std::conditional_t<kValBlocks, Stage<VT, NB>, Nothing> vstage(lane);
     Keys<KT, NB> keys[2];
     const auto fetch_keys = [&](int k) {
 #pragma unroll
@@ -758,11 +757,22 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
             else keys[h].load(lane, rows_of(krows, i), lane_of(kfar, i));
         }
     };
+    // Of binary16 the next step's; after the last anything, so that this step's do not stay in registers through it.
+    const auto next_keys = [&](int k) {
+        if (k < ksteps) {
+            fetch_keys(k);
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (uint32_t& word : keys[h].w) asm("" : "=v"(word));
+        }
+    };
     const auto fetch_values = [&](int k, Values<VT, NB>& vals) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int i = 2 * (k - block) + h;
-            if constexpr (kStaged) vstage.fetch(lane, ring + kDepth * S::kKeys + k % kDepth * S::kVals, h, rows_of(vrows, i), lane_of(vfar, i));
+            if constexpr (kValBlocks) vstage.fetch(lane, ring + kDepth * S::kKeys + k % kDepth * S::kVals, h, rows_of(vrows, i), lane_of(vfar, i));
             else vals.load(lane, h, rows_of(vrows, i), lane_of(vfar, i));
         }
     };
@@ -770,10 +780,10 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
     if (ksteps > 0) {
         read_pages(0);
         if constexpr (kStaged) arrived<0>();  // the queries too: a wait for them further on would wait for what sets out now
-        fetch_keys(0);
-        if constexpr (kStaged) {
-            fetch_values(0, vals);
-        }
+        // (values first where the compiler waits for the keys: they are there when the keys are)
+        if constexpr (kStaged) fetch_keys(0);
+        if constexpr (kValBlocks) fetch_values(0, vals);
+        if constexpr (!kStaged) fetch_keys(0);
     }
 
 #pragma unroll
@@ -848,6 +858,8 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
             else arrived<Stage<VT, NB>::kLoads>();
 #pragma unroll
             for (int h = 0; h < 2; ++h) keys[h].read(lane, h, ring + k % kDepth * S::kKeys);
+        } else if constexpr (kValBlocks) {
+            arrived<0>();
         } else {
             fetch_values(k, vals);
         }
@@ -902,8 +914,12 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
         if constexpr (kStaged) {
             taken();
             if (k + kDepth < ksteps) fetch_keys(k + kDepth);
-        } else if (kEarly && k + 1 < ksteps) {
-            fetch_keys(k + 1);
+        } else if constexpr (kEarly) {
+            if (kValBlocks && k + 1 < ksteps) {
+                taken();
+                fetch_values(k + 1, vals);
+            }
+            next_keys(k + 1);
         }
         // Positions that some row of the tile does not see: their scores go, whatever they are.  (The empty asm keeps
         // this a branch that steps in the middle of a cache skip.)
@@ -964,6 +980,8 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
             if (k + kDepth < ksteps) arrived<kDepth * kK + (kDepth - 1) * kV>();
             else if (kDepth > 1 && k + 1 < ksteps) arrived<kK + kV>();
             else arrived<0>();
+        }
+        if constexpr (kValBlocks) {
             vals.read(lane, ring + kDepth * S::kKeys + k % kDepth * S::kVals);
         }
         if constexpr (kValBlocks) {
@@ -987,19 +1005,14 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
                 }
 #pragma unroll
                 for (int x = 0; x < RT; ++x) above |= most[x] >= bound[x];
-            } else if constexpr (kStaged) {
+            } else {
                 // (the sixteen lanes with the same scales share them)
                 above = Stage<VT, NB>::largest_part(ring + kDepth * S::kKeys + k % kDepth * S::kVals, n, g) >= least;
-            } else {
-#pragma unroll
-                for (int x = 0; x < RT; ++x) most[x] = x ? most[0] : vals.template largest<false>(0);
-#pragma unroll
-                for (int x = 0; x < RT; ++x) above |= most[x] >= bound[x];
             }
             vals.keep_words();
             if (__any(above)) {
                 int now = 0x10000;
-                if (kStaged && !masked) {
+                if (!masked) {
 #pragma unroll
                     for (int x = 0; x < RT; ++x) most[x] = x ? most[0] : vals.template largest<false>(0);
                 }
@@ -1128,8 +1141,12 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
         if constexpr (kStaged) {
             taken();
             if (k + kDepth < ksteps) fetch_values(k + kDepth, vals);
-        } else if (!kEarly && k + 1 < ksteps) {
-            fetch_keys(k + 1);
+        } else if constexpr (!kEarly) {
+            if (kValBlocks && k + 1 < ksteps) {
+                taken();
+                fetch_values(k + 1, vals);
+            }
+            next_keys(k + 1);
         }
     }
 
