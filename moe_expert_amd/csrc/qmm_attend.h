@@ -49,9 +49,10 @@ struct AttendArgs {
     int nheads, group, qtype, otype;  // group: heads of queries a head of keys
     float scale;                      // times log2(e)
     int window;                       // 0: none
-    int target, least;                // workgroups a head of keys, steps that a tile counts for at least
+    int target, one, least;           // workgroups a head of keys, of one for every CU;  steps that a tile counts for at least
+    int shift;                        // a unit of the split is 2^shift steps: no line has more than 2^29 units
     int vec;                          // out: groups of four values are aligned
-    uint32_t per_group;               // kv_per(group)
+    uint32_t per_group, per_target;  // kv_per() of them
 };
 
 // The kernel's argument where it is needed: read again from its segment rather than kept in scalar registers, of which
@@ -63,6 +64,18 @@ __device__ __forceinline__ const AttendArgs& launch_args() {
 }
 
 // ------------------------------------------------------------------ what a workgroup does
+
+// Quotients by n > 0 of numbers in [0, 2^31), exact: the reciprocal is within 2^-44 of its value, and (v + 1/2) / n no
+// nearer to a whole number than 1 / (2 n).
+struct Per {
+    double per;
+    __device__ __forceinline__ explicit Per(int n) {
+        const double r = (double)__builtin_amdgcn_rcpf((float)n);
+        per = r * __builtin_fma(-(double)n, r, 2.0);
+    }
+    __device__ __forceinline__ int down(int v) const { return (int)(((double)v + 0.5) * per); }
+    __device__ __forceinline__ int up(int v) const { return v > 0 ? down(v - 1) + 1 : 0; }
+};
 
 // Sequence s as the split sees it.
 struct SeqWork {
@@ -102,51 +115,48 @@ __device__ __forceinline__ SeqWork lane_work(const AttendArgs& a, int s, int row
 // than the equal share of the steps, tiles take whole lengths: a workgroup has one piece then, and pays once for what
 // it does beside its steps (kAtCost steps of its time, about).
 constexpr int kAtCost = 12;
+constexpr int kAtWaves = 4;
 struct Split {
-    int shift;      // a unit is 2^shift steps (0, but for lines of more than 2^30 steps)
     int len, all;   // units of a workgroup, and all
     bool whole;     // tiles take whole lengths
 };
 
 // Units of a tile that hold steps (one if there are none, for the zeros), and its units.
-__device__ __forceinline__ int live_units(int steps, int shift) { return max(1, (steps + (1 << shift) - 1) >> shift); }
+__device__ __forceinline__ int live_units(const AttendArgs& a, int steps) { return max(1, (steps + (1 << a.shift) - 1) >> a.shift); }
+__device__ __forceinline__ int least_units(const AttendArgs& a) { return max(a.least >> a.shift, 1); }
+__device__ __forceinline__ int line_units(const AttendArgs& a, int steps) { return max(live_units(a, steps), least_units(a)); }
 __device__ __forceinline__ int tile_units(const AttendArgs& a, int steps, const Split& s) {
-    const int live = live_units(steps, s.shift);
-    return s.whole ? (live + s.len - 1) / s.len * s.len : max(live, a.least >> s.shift);
+    const int live = live_units(a, steps);
+    return s.whole ? Per(s.len).up(live) * s.len : max(live, least_units(a));
 }
 
-// From the sums over the sequences of tiles times steps (or the least) and of tokens.  Offsets that decrease give more
-// tokens than there are: nothing is done then.
-__device__ __forceinline__ int line_shift(int64_t work) {
-    int shift = 0;
-    while (work >> shift > 1 << 29) ++shift;
-    return shift;
-}
-__device__ __forceinline__ int share(const AttendArgs& a, int units, int shift, int lengths) {
-    return max((units + lengths - 1) / lengths, max(a.least >> shift, 1));
-}
-// units: of all tiles, counted for the line; lengths(len): how many whole lengths all tiles take.
+// units, tiles, tokens: of all sequences (line_units() of each tile); lengths(len): how many whole lengths all tiles
+// take.  Offsets that decrease give more tokens than there are: nothing is done then.
 template <class F>
-__device__ __forceinline__ Split line_split(const AttendArgs& a, int shift, int units, int tiles, int64_t tokens, F lengths) {
+__device__ __forceinline__ Split line_split(const AttendArgs& a, int units, int tiles, int64_t tokens, F lengths) {
     Split s;
-    s.shift = shift;
-    const int even = share(a, units, shift, a.target);
-    for (int i = 0; i < 2; ++i) {
-        // the equal share, then one that leaves half a length a tile
-        const int left = a.target - tiles / 2;
-        if (i && left <= 0) break;
-        s.len = i ? share(a, units, shift, left) : even;
-        if (s.len > even + (kAtCost >> shift)) break;
-        const int count = lengths(s.len);
-        if (count <= a.target) {
-            s.whole = true;
-            s.all = tokens > a.p.ntok ? 0 : count * s.len;
-            return s;
-        }
+    const int target = a.target, step = max(kAtWaves >> a.shift, 1);
+    const auto rounded = [&](int len) { return max((len + step - 1) & -step, step); };  // as many steps for every wave
+    uint32_t rest;
+    const int share = (int)kv_divide(units, target, a.per_target, rest) + (rest ? 1 : 0);
+    int even = rounded(share), count = lengths(even);
+    if (even < 2 * step && count > a.one) {
+        even = 2 * step;
+        count = lengths(even);
     }
-    s.whole = false;
+    s.whole = true;
     s.len = even;
-    s.all = tokens > a.p.ntok ? 0 : units;
+    if (count > target && target > tiles / 2) {
+        // not the equal share, but one that leaves half a length a tile
+        const int left = target - tiles / 2;
+        s.len = rounded(Per(left).up(units));
+        count = s.len > even + (kAtCost >> a.shift) ? count : lengths(s.len);
+    }
+    if (count > target) {
+        s.whole = false;
+        s.len = max(share, least_units(a));
+    }
+    s.all = tokens > a.p.ntok ? 0 : s.whole ? count * s.len : units;
     return s;
 }
 
@@ -159,34 +169,23 @@ struct Tile {
 // The split, by every wave for itself; w: the lane's sequence of the first 64, for find_tile.
 __device__ __forceinline__ Split find_split(const AttendArgs& a, int rows, SeqWork& w) {
     const int lane = threadIdx.x & 63, nseq = a.p.nseq;
-    Split s;
-    if (a.plan) {
-        s.shift = a.plan[0];
-        s.len = a.plan[1];
-        s.all = a.plan[2];
-        s.whole = false;
-        return s;
-    }
-    int64_t work = 0;
-    int tokens = 0, tiles = 0;
+    if (a.plan) return Split{a.plan[0], a.plan[1], false};
+    int units = 0, tokens = 0, tiles = 0;
     for (int j = (nseq - 1) & ~63; j >= 0; j -= 64) {
         w = lane_work(a, j + lane, rows);
-        const int64_t mine = (int64_t)max(w.steps, a.least) * w.tiles;  // below 2^49 in all: two sums that fit 32 bits
-        work += ((int64_t)wave_total((int)(mine >> 24)) << 24) + wave_total((int)(mine & 0xFFFFFF));
+        units += wave_total(w.tiles * line_units(a, w.steps));
         tokens += wave_total(w.n);
         tiles += wave_total(w.tiles);
     }
-    const int shift = line_shift(work);
-    const auto sum = [&](auto value) {
+    return line_split(a, units, tiles, tokens, [&](int len) {
         int all = 0;
+        const Per per(len);
         for (int j = 0; j < nseq; j += 64) {
-            const SeqWork v = j || nseq > 64 ? lane_work(a, j + lane, rows) : w;
-            all += wave_total(v.tiles * value(live_units(v.steps, shift)));
+            const SeqWork v = j ? lane_work(a, j + lane, rows) : w;
+            all += wave_total(v.tiles * per.up(live_units(a, v.steps)));
         }
         return all;
-    };
-    const int units = shift ? sum([&](int live) { return max(live, a.least >> shift); }) : (int)work;
-    return line_split(a, shift, units, tiles, tokens, [&](int len) { return sum([&](int live) { return (live + len - 1) / len; }); });
+    });
 }
 
 // The tile that unit `at` of the line belongs to; w: the lane's sequence of the first 64.
@@ -195,7 +194,7 @@ __device__ __forceinline__ Tile find_tile(const AttendArgs& a, const Split& s, i
     Tile t;
     int before = 0;
     if (a.plan) {
-        const int32_t* units = a.plan + 3;  // before each sequence, and all
+        const int32_t* units = a.plan + 2;  // before each sequence, and all
         const int stride = (nseq + 63) / 64;
         int seq = stride * __popcll(__ballot(units[min((lane + 1) * stride, nseq)] <= at));
         const int end = min(seq + stride, nseq);
@@ -223,9 +222,9 @@ __device__ __forceinline__ Tile find_tile(const AttendArgs& a, const Split& s, i
             before += total;
         }
     }
-    t.live = live_units(t.w.steps, s.shift);
+    t.live = live_units(a, t.w.steps);
     t.units = tile_units(a, t.w.steps, s);
-    t.tile = (at - before) / t.units;
+    t.tile = t.w.tiles > 1 ? Per(t.units).down(at - before) : 0;
     t.at = before + t.tile * t.units;
     return t;
 }
@@ -1226,11 +1225,12 @@ __global__ __launch_bounds__((64 * Shape<KT, VT, NB, RT>::kWaves), 2) void atten
         int slot = -1;
         if (units != tl.live) {
             // The second of the two, if the tile begins here.
-            const int from = tl.at / split.len;
+            const Per per(split.len);
+            const int from = per.down(tl.at);
             slot = 2 * run + (run == from ? 1 : 0);
-            if (tells) a.pieces[slot] = Piece{(tl.at + tl.live - 1) / split.len - from + 1, run - from, w.first, tl.tile << 6 | min(kRows, w.n * a.group - tl.tile * kRows)};
+            if (tells) a.pieces[slot] = Piece{per.down(tl.at + tl.live - 1) - from + 1, run - from, w.first, tl.tile << 6 | min(kRows, w.n * a.group - tl.tile * kRows)};
         }
-        attend_piece<KT, VT, NB, RT>(w, tl.tile, piece << split.shift, units << split.shift, lds, lc, (int)head, slot);
+        attend_piece<KT, VT, NB, RT>(w, tl.tile, piece << a.shift, units << a.shift, lds, lc, (int)head, slot);
         __syncthreads();
     }
 }

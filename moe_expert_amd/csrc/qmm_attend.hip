@@ -4,50 +4,35 @@
 
 namespace qmm {
 
-// The split of more sequences than a wave looks through: shift, length, all, then the units before each sequence.
+// The split of more sequences than a wave looks through: length, all, then the units before each sequence.
 __global__ __launch_bounds__(1024) void attend_plan_kernel(AttendArgs a, int rows, int32_t* plan) {
-    __shared__ int64_t work[16], tokens[16];
-    __shared__ int units[16];
+    __shared__ int tokens[16], units[16];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, nseq = a.p.nseq;
-    int64_t sum = 0, all = 0;
-    for (int s = threadIdx.x; s - lane < nseq; s += 1024) {
-        const SeqWork w = lane_work(a, s, rows);
-        const int64_t mine = (int64_t)max(w.steps, a.least) * w.tiles;
-        sum += ((int64_t)wave_total((int)(mine >> 24)) << 24) + wave_total((int)(mine & 0xFFFFFF));
-        all += wave_total(w.n);
-    }
-    if (lane == 0) {
-        work[wave] = sum;
-        tokens[wave] = all;
-    }
-    __syncthreads();
-    sum = all = 0;
-    for (int i = 0; i < 16; ++i) {
-        sum += work[i];
-        all += tokens[i];
-    }
-    Split split{line_shift(sum), 0, 0, false};
+    int64_t all = 0;
     int before = 0;
     for (int s0 = 0; s0 < nseq; s0 += 1024) {
         const int s = s0 + threadIdx.x;
         const SeqWork w = lane_work(a, s, rows);
-        const int mine = w.tiles * tile_units(a, w.steps, split), upto = wave_scan(mine);
+        const int mine = w.tiles * line_units(a, w.steps), upto = wave_scan(mine), n = wave_total(w.n);
         __syncthreads();
-        if (lane == 63) units[wave] = upto;
+        if (lane == 63) {
+            units[wave] = upto;
+            tokens[wave] = n;
+        }
         __syncthreads();
         int off = before;
         for (int i = 0; i < 16; ++i) {
             off += i < wave ? units[i] : 0;
             before += units[i];
+            all += tokens[i];
         }
-        if (s < nseq) plan[3 + s] = off + upto - mine;
+        if (s < nseq) plan[2 + s] = off + upto - mine;
     }
-    split = line_split(a, split.shift, before, 0, all, [&](int) { return a.target + 1; });
+    const Split split = line_split(a, before, 0, all, [&](int) { return 0x7FFFFFFF; });
     if (threadIdx.x == 0) {
-        plan[0] = split.shift;
-        plan[1] = split.len;
-        plan[2] = split.all;
-        plan[3 + nseq] = before;
+        plan[0] = split.len;
+        plan[1] = split.all;
+        plan[2 + nseq] = before;
     }
 }
 
@@ -111,12 +96,13 @@ using namespace qmm;
 namespace {
 
 constexpr int kAtTarget = 512;  // workgroups: two for every CU, what runs at once
-constexpr int kAtLeast = 8;     // steps that a tile counts for at least, two for each wave
+constexpr int kAtLeast = 8;     // steps that a tile counts for at least on the line
 
 struct AttendShape {
     KvPlace p;
     int rt;          // 16-row tiles a workgroup
     int target;      // workgroups a head of keys, at most
+    int shift;       // 2^shift steps are a unit of the split
     bool split;      // a tile can have more than one piece
     size_t bytes;    // of the workspace: pieces, what is told of them, the plan
     size_t told, plan;  // their offsets
@@ -134,9 +120,10 @@ int attend_shape(AttendShape& s, const qmm_kv_cache* c, const int32_t* pages, in
     const int64_t rows = 16 * s.rt, tiles = std::min(nseq + ntok * group / rows, ntok * ((group + rows - 1) / rows));
     // At most this many steps a tile (a walk may begin 15 positions early), and so workgroups with a length of the line.
     const int64_t steps = (max_pages * c->page_size + kAtStep - 1) / kAtStep + 1;
-    const int64_t line = tiles * ((std::max(steps, (int64_t)kAtLeast) + kAtLeast - 1) / kAtLeast);
+    const int64_t line = tiles * ((steps + kAtWaves - 1) / kAtWaves);
     s.target = (int)std::max(std::min((int64_t)(kAtTarget / c->nheads), line), (int64_t)1);
-    s.split = steps > kAtLeast || tiles > s.target;
+    for (s.shift = 0; (tiles * std::max(steps, (int64_t)kAtLeast)) >> s.shift > 1 << 29;) ++s.shift;
+    s.split = steps > kAtWaves || tiles > s.target;
     // (sized for 32 rows where a call of other proportions would take them)
     s.told = s.split ? (size_t)(2 * s.target * c->nheads * part_floats(wide ? 32 : 16, c->head_dim) * 4) : 0;
     s.plan = s.told + (s.split ? 2 * s.target * sizeof(Piece) : 0);
@@ -188,6 +175,9 @@ extern "C" int qmm_kv_attend(const qmm_kv_cache* c, const int32_t* pages, int64_
     a.scale = (float)((double)scale * 1.4426950408889634);
     a.window = (int)std::min(window, (int64_t)0x7FFFFFFF);  // more than any position
     a.target = s.target;
+    a.one = std::max(kAtTarget / 2 / c->nheads, 1);
+    a.shift = s.shift;
+    a.per_target = kv_per(a.target);
     a.least = kAtLeast;
     a.vec = fours(out, ldo, otype);
     const hipStream_t st = as_stream(stream);
