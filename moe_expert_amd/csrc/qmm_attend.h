@@ -776,9 +776,10 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
         }
     };
     Values<VT, NB> vals;
+    // Waves without a step look pages up too: the queries are there then whatever way the compiler follows, and it puts
+    // no wait for them further on, which would wait for the keys and values that set out now.
+    read_pages(0);
     if (ksteps > 0) {
-        read_pages(0);
-        if constexpr (kStaged) arrived<0>();  // the queries too: a wait for them further on would wait for what sets out now
         // (values first where the compiler waits for the keys: they are there when the keys are)
         if constexpr (kStaged) fetch_keys(0);
         if constexpr (kValBlocks) fetch_values(0, vals);
