@@ -436,6 +436,8 @@ struct Keys {
 };
 
 __device__ __forceinline__ bool not_finite(uint32_t half) { return (half & 0x7C00u) == 0x7C00u; }
+// Bits 15 and 31: whether each of two halves is not finite.  (Many of them are joined without a compare each.)
+__device__ __forceinline__ uint32_t odd_halves(uint32_t v) { return ((v & 0x7C007C00u) + 0x04000400u) & 0x80008000u; }
 
 // The values of 32 positions: lane (n, g) holds, of the positions 4g .. 4g+3 of both halves, the dims that
 // row n of the 2 NB operands V^T takes: tile (b, i) dim 32b + 16i + n (binary16: tile j dim 2 NB n + j).
@@ -477,8 +479,8 @@ struct Values {
                 uint32_t v = d[h][i] & 0x7FFF7FFFu;
                 if constexpr (MASKED) {
                     const int x = 4 * h + 2 * i / NB, y = 4 * h + (2 * i + 1) / NB;
-                    if (x == y) v = seen >> x & 1 ? v : 0u;
-                    else v = (seen >> x & 1 ? v & 0xFFFFu : 0u) | (seen >> y & 1 ? v & 0xFFFF0000u : 0u);
+                    const uint32_t a = (uint32_t)((int)((uint32_t)seen << (31 - x)) >> 31), b = (uint32_t)((int)((uint32_t)seen << (31 - y)) >> 31);
+                    v &= x == y ? a : (a & 0xFFFFu) | (b & 0xFFFF0000u);
                 }
                 most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2, v));
             }
@@ -486,20 +488,23 @@ struct Values {
     }
     // Scales that are not finite: whether there are any, the blocks (bits) where a position seen has one, and without them.
     __device__ __forceinline__ bool any_odd() const {
-        bool odd = false;
+        uint32_t odd = 0;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int i = 0; i < 2 * NB; ++i) odd |= not_finite(d[h][i]) || not_finite(d[h][i] >> 16);
-        return odd;
+            for (int i = 0; i < 2 * NB; ++i) odd |= odd_halves(d[h][i]);
+        return odd != 0;
     }
     __device__ __forceinline__ int odd_blocks(int seen) const {
         int blocks = 0;
 #pragma unroll
-        for (int x = 0; x < 8; ++x)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int b = 0; b < NB; ++b)
-                blocks |= seen >> x & 1 && not_finite(__builtin_bit_cast(uint16_t, scale(x, b))) ? 1 << b : 0;
+            for (int i = 0; i < 2 * NB; ++i) {
+                const uint32_t odd = odd_halves(d[h][i]);
+                blocks |= (int)(odd >> 15 & (uint32_t)seen >> (4 * h + 2 * i / NB) & 1) << (2 * i % NB);
+                blocks |= (int)(odd >> 31 & (uint32_t)seen >> (4 * h + (2 * i + 1) / NB) & 1) << ((2 * i + 1) % NB);
+            }
         return blocks;
     }
     // The scales as they are loaded, two a register, also past a branch that may change them.
@@ -850,6 +855,8 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
 
     for (int k = 0; k < ksteps; ++k) {
         const int j0 = start + kAtStep * kWaves * k;
+        int there = lane;  // where registers are short, the addresses in LDS are found anew rather than kept
+        if constexpr (NB * RT >= 6) asm volatile("" : "+v"(there));
         if (k - block == 30) read_pages(k);
         const bool exist[2] = {!(missing >> (2 * (k - block)) & 1), !(missing >> (2 * (k - block) + 1) & 1)};
         if constexpr (kStaged) {
@@ -857,7 +864,7 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
             if (kDepth > 1 && k + 1 < ksteps) arrived<2 * Stage<VT, NB>::kLoads + Stage<KT, NB>::kLoads>();
             else arrived<Stage<VT, NB>::kLoads>();
 #pragma unroll
-            for (int h = 0; h < 2; ++h) keys[h].read(lane, h, ring + k % kDepth * S::kKeys);
+            for (int h = 0; h < 2; ++h) keys[h].read(there, h, ring + k % kDepth * S::kKeys);
         } else if constexpr (kValBlocks) {
             arrived<0>();
         } else {
@@ -982,7 +989,7 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
             else arrived<0>();
         }
         if constexpr (kValBlocks) {
-            vals.read(lane, ring + kDepth * S::kKeys + k % kDepth * S::kVals);
+            vals.read(there, ring + kDepth * S::kKeys + k % kDepth * S::kVals);
         }
         if constexpr (kValBlocks) {
             bool above = false;
@@ -1007,7 +1014,7 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
                 for (int x = 0; x < RT; ++x) above |= most[x] >= bound[x];
             } else {
                 // (the sixteen lanes with the same scales share them)
-                above = Stage<VT, NB>::largest_part(ring + kDepth * S::kKeys + k % kDepth * S::kVals, n, g) >= least;
+                above = Stage<VT, NB>::largest_part(ring + kDepth * S::kKeys + k % kDepth * S::kVals, there & 15, there >> 4) >= least;
             }
             vals.keep_words();
             if (__any(above)) {
@@ -1042,7 +1049,7 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
             asm volatile("");
             // Places that no row sees count as zeros.  Infinities and NaN that some rows see and others do not
             // must not meet the others' zeros in the products: they are added one position at a time, and left out there.
-            bool odd = false;
+            uint32_t odd = 0;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const int j = j0 + 16 * (i >> 2) + 4 * g + (i & 3);
@@ -1050,10 +1057,10 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
 #pragma unroll
                 for (int e = 0; e < Values<VT, NB>::kWords; ++e) {
                     vals.w[i][e] = some ? vals.w[i][e] : 0u;
-                    odd |= not_finite(vals.w[i][e]) || not_finite(vals.w[i][e] >> 16);
+                    odd |= odd_halves(vals.w[i][e]);
                 }
             }
-            if (__any(odd)) {
+            if (__any(odd != 0)) {
                 float* weight = (float*)(lds + S::kQueries + wave * S::kOdd);
                 uint32_t* row = (uint32_t*)(weight + kRows * kAtStep);
 #pragma unroll
