@@ -762,7 +762,8 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
         vfar = (size - place) * Side<VT, NB>::kFactor + place * Side<VT, NB>::kScale;
     };
     const auto rows_of = [&](uint64_t rows, int i) {
-        return (const char*)((uint64_t)(uint32_t)lane_of((int)(rows >> 32), i) << 32 | (uint32_t)lane_of((int)rows, i));
+        const uint64_t at = (uint64_t)(uint32_t)lane_of((int)(rows >> 32), i) << 32 | (uint32_t)lane_of((int)rows, i);
+        return (const char*)(const __attribute__((address_space(1))) char*)at;  // (global: loads that LDS does not wait for)
     };
     char* const ring = lds + S::kQueries + wave * S::kRing;
     const std::conditional_t<kStaged, Stage<KT, NB>, Nothing> kstage(lane);
