@@ -116,9 +116,22 @@ __device__ __forceinline__ SeqWork lane_work(const AttendArgs& a, int s, int row
 // it does beside its steps (kAtCost steps of its time, about).
 constexpr int kAtCost = 12;
 constexpr int kAtWaves = 4;
+
+// Of two workgroups on a CU the one that came first is served first and ends first (32 x 8192 q8_0: after 38.7 us, the
+// other after 48.3), so where lengths are long the workgroups take the line in pairs, one of the first half and one
+// of the second, and the first of a pair takes kAtMore sixteenths of a length more.
+constexpr int kAtLong = 16, kAtMore = 3;
 struct Split {
-    int len, all;   // units of a workgroup, and all
-    bool whole;     // tiles take whole lengths
+    int pair, first;  // units of two workgroups, and of the first of them
+    int all;          // of the line
+    int whole;        // units that a tile takes a multiple of, or 0
+    bool paired;      // workgroups of the first and the second half in turn
+    // The place on the line of a workgroup, counted along it, and which of them a unit belongs to.
+    __device__ __forceinline__ int begin(int run) const { return (run >> 1) * pair + (run & 1 ? first : 0); }
+    __device__ __forceinline__ int run_of(const Per& per, int unit) const {
+        const int p = per.down(unit);
+        return 2 * p + (unit - p * pair >= first ? 1 : 0);
+    }
 };
 
 // Units of a tile that hold steps (one if there are none, for the zeros), and its units.
@@ -127,7 +140,7 @@ __device__ __forceinline__ int least_units(const AttendArgs& a) { return max(a.l
 __device__ __forceinline__ int line_units(const AttendArgs& a, int steps) { return max(live_units(a, steps), least_units(a)); }
 __device__ __forceinline__ int tile_units(const AttendArgs& a, int steps, const Split& s) {
     const int live = live_units(a, steps);
-    return s.whole ? Per(s.len).up(live) * s.len : max(live, least_units(a));
+    return s.whole ? Per(s.whole).up(live) * s.whole : max(live, least_units(a));
 }
 
 // units, tiles, tokens: of all sequences (line_units() of each tile); lengths(len): how many whole lengths all tiles
@@ -144,19 +157,28 @@ __device__ __forceinline__ Split line_split(const AttendArgs& a, int units, int 
         even = 2 * step;
         count = lengths(even);
     }
-    s.whole = true;
-    s.len = even;
-    if (count > target && target > tiles / 2) {
-        // not the equal share, but one that leaves half a length a tile
-        const int left = target - tiles / 2;
-        s.len = rounded(Per(left).up(units));
-        count = s.len > even + (kAtCost >> a.shift) ? count : lengths(s.len);
+    int len = even;
+    bool whole = true;
+    s.paired = even >= kAtLong >> a.shift && target > a.one;
+    const int pairs = s.paired ? lengths(2 * even) : 0;
+    if (s.paired && 2 * pairs <= target) {
+        count = pairs;
+        s.whole = 2 * even;
+    } else {
+        if (count > target && target > tiles / 2) {
+            // not the equal share, but one that leaves half a length a tile
+            const int left = target - tiles / 2;
+            len = rounded(Per(left).up(units));
+            count = len > even + (kAtCost >> a.shift) ? count : lengths(len);
+        }
+        whole = count <= target;
+        if (!whole) len = max(share, least_units(a));
+        s.paired = s.paired && !whole;
+        s.whole = whole ? len : 0;
     }
-    if (count > target) {
-        s.whole = false;
-        s.len = max(share, least_units(a));
-    }
-    s.all = tokens > a.p.ntok ? 0 : s.whole ? count * s.len : units;
+    s.pair = 2 * len;
+    s.first = s.paired ? len + ((len * kAtMore / 16 + step - 1) & -step) : len;
+    s.all = tokens > a.p.ntok ? 0 : whole ? count * s.whole : units;
     return s;
 }
 
@@ -169,7 +191,7 @@ struct Tile {
 // The split, by every wave for itself; w: the lane's sequence of the first 64, for find_tile.
 __device__ __forceinline__ Split find_split(const AttendArgs& a, int rows, SeqWork& w) {
     const int lane = threadIdx.x & 63, nseq = a.p.nseq;
-    if (a.plan) return Split{a.plan[0], a.plan[1], false};
+    if (a.plan) return Split{a.plan[0], a.plan[1], a.plan[2], 0, a.plan[1] * 2 != a.plan[0]};
     int units = 0, tokens = 0, tiles = 0;
     for (int j = (nseq - 1) & ~63; j >= 0; j -= 64) {
         w = lane_work(a, j + lane, rows);
@@ -194,7 +216,7 @@ __device__ __forceinline__ Tile find_tile(const AttendArgs& a, const Split& s, i
     Tile t;
     int before = 0;
     if (a.plan) {
-        const int32_t* units = a.plan + 2;  // before each sequence, and all
+        const int32_t* units = a.plan + 3;  // before each sequence, and all
         const int stride = (nseq + 63) / 64;
         int seq = stride * __popcll(__ballot(units[min((lane + 1) * stride, nseq)] <= at));
         const int end = min(seq + stride, nseq);
@@ -1233,10 +1255,14 @@ __global__ __launch_bounds__((64 * Shape<KT, VT, NB, RT>::kWaves), 2) void atten
     __shared__ __attribute__((aligned(16))) char lds[S::kBytes];
     __shared__ float lc[kRows];
     uint32_t head;
-    const int run = (int)kv_divide(blockIdx.x, a.p.nheads, a.p.per_head, head);
+    int run = (int)kv_divide(blockIdx.x, a.p.nheads, a.p.per_head, head);
     SeqWork mine;
     const Split split = find_split(a, kRows, mine);
-    const int begin = run * split.len, end = min(begin + split.len, split.all);
+    if (split.paired) {
+        const int half = (a.target + 1) / 2;
+        run = run < half ? 2 * run : 2 * (run - half) + 1;
+    }
+    const int begin = split.begin(run), end = min(split.begin(run + 1), split.all);
     const bool tells = a.pieces && head == 0 && threadIdx.x == 0;
     if (tells) a.pieces[2 * run].count = a.pieces[2 * run + 1].count = 0;
     for (int at = begin; at < end;) {
@@ -1249,10 +1275,10 @@ __global__ __launch_bounds__((64 * Shape<KT, VT, NB, RT>::kWaves), 2) void atten
         int slot = -1;
         if (units != tl.live) {
             // The second of the two, if the tile begins here.
-            const Per per(split.len);
-            const int from = per.down(tl.at);
+            const Per per(split.pair);
+            const int from = split.run_of(per, tl.at);
             slot = 2 * run + (run == from ? 1 : 0);
-            if (tells) a.pieces[slot] = Piece{per.down(tl.at + tl.live - 1) - from + 1, run - from, w.first, tl.tile << 6 | min(kRows, w.n * a.group - tl.tile * kRows)};
+            if (tells) a.pieces[slot] = Piece{split.run_of(per, tl.at + tl.live - 1) - from + 1, run - from, w.first, tl.tile << 6 | min(kRows, w.n * a.group - tl.tile * kRows)};
         }
         attend_piece<KT, VT, NB, RT>(w, tl.tile, piece << a.shift, units << a.shift, lds, lc, (int)head, slot);
         __syncthreads();

@@ -4,7 +4,7 @@
 
 namespace qmm {
 
-// The split of more sequences than a wave looks through: length, all, then the units before each sequence.
+// The split of more sequences than a wave looks through: lengths, all, then the units before each sequence.
 __global__ __launch_bounds__(1024) void attend_plan_kernel(AttendArgs a, int rows, int32_t* plan) {
     __shared__ int tokens[16], units[16];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, nseq = a.p.nseq;
@@ -26,13 +26,14 @@ __global__ __launch_bounds__(1024) void attend_plan_kernel(AttendArgs a, int row
             before += units[i];
             all += tokens[i];
         }
-        if (s < nseq) plan[2 + s] = off + upto - mine;
+        if (s < nseq) plan[3 + s] = off + upto - mine;
     }
-    const Split split = line_split(a, before, 0, all, [&](int) { return 0x7FFFFFFF; });
+    const Split split = line_split(a, before, 0, all, [&](int) { return 0x3FFFFFFF; });
     if (threadIdx.x == 0) {
-        plan[0] = split.len;
-        plan[1] = split.all;
-        plan[2 + nseq] = before;
+        plan[0] = split.pair;
+        plan[1] = split.first;
+        plan[2] = split.all;
+        plan[3 + nseq] = before;
     }
 }
 
