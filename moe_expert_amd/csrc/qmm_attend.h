@@ -397,11 +397,11 @@ __device__ __forceinline__ void load_bytes(uint32_t* w, const char* p) {
     __builtin_memcpy(w, p, N);
 }
 
-// Two biased bytes u = q + 128, which perm laid into the low bytes of two halves, are u 2^-24 as binary16 values.  As
-// they are (BIASED), what 128 in their place would give is taken from the sums; or (u - 128) 2^-10.
-template <bool BIASED>
+// Two biased bytes u = q + 128, which perm laid into the low bytes of two halves, are u 2^-24 as binary16 values: to
+// q 2^-10.  (Keys enter as they are, and what 128 in their place would give is where their sums begin.  For values that
+// costs digits: the sums of a long context's weights times 128 are far above those of its values.  8 sequences of 4096
+// positions, q8_0, were 9e-6 off so, and 2e-7 like this.)
 __device__ __forceinline__ uint32_t value_pair(uint32_t x) {
-    if constexpr (BIASED) return x;
     const half2_t scale = {(_Float16)16384.0f, (_Float16)16384.0f}, bias = {(_Float16)-0.125f, (_Float16)-0.125f};
     return __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(__builtin_bit_cast(half2_t, x), scale, bias));
 }
@@ -579,7 +579,6 @@ struct Values {
                 }
             }
     }
-    template <bool BIASED>
     __device__ static __forceinline__ half8_t tile(const Ready& r, int t) {
         uint32_t o[4];
 #pragma unroll
@@ -587,11 +586,11 @@ struct Values {
             if constexpr (TYPE == kKvF16) {
                 o[m] = perm(r.a[2 * m + 1][t / 2], r.a[2 * m][t / 2], t & 1 ? 0x07060302u : 0x05040100u);
             } else if constexpr (TYPE == kKvQ8) {
-                o[m] = value_pair<BIASED>(perm(r.a[2 * m + 1][t / 4], r.a[2 * m][t / 4], pair_sel(t % 4, t % 4 + 4)));
+                o[m] = value_pair(perm(r.a[2 * m + 1][t / 4], r.a[2 * m][t / 4], pair_sel(t % 4, t % 4 + 4)));
             } else {
                 const int b = t / 2, i = b / 4, shared = kBytes % 4 == 2 && i == kWords - 1 ? 2 : 0;
                 const uint32_t lo = t & 1 ? r.b[2 * m][i] : r.a[2 * m][i], hi = t & 1 ? r.b[2 * m + 1][i] : r.a[2 * m + 1][i];
-                o[m] = value_pair<BIASED>(perm(hi, lo, pair_sel(b % 4, b % 4 + 4 + shared)));
+                o[m] = value_pair(perm(hi, lo, pair_sel(b % 4, b % 4 + 4 + shared)));
             }
         }
         return as_half8(o[0], o[1], o[2], o[3]);
@@ -691,8 +690,6 @@ template <int KT, int VT, int NB, int RT>
 struct Shape {
     static constexpr bool kStaged = KT != kKvF16;
     static constexpr int kKeys = kStaged ? Stage<KT, NB>::kBytes : 0, kVals = VT != kKvF16 ? Stage<VT, NB>::kBytes : 0;
-    // Keys of a block format enter as u 2^-24, their sums begin at -128 2^-24 times the queries' sum.  Values do where the registers hold the sums of their weights beside the others.
-    static constexpr bool kBiased = VT != kKvF16 && NB * RT <= 4;
     static constexpr int kQueries = RT * NB * 2 * 64 * 16;
     static constexpr int kWaves = kQueries + 4 * (kKeys + kVals) > kAtLds ? 8 : 4;
     static constexpr bool kTwo = kWaves == 4 && kQueries + 8 * (kKeys + kVals) <= kAtLds;
@@ -715,7 +712,7 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
     const AttendArgs& a = launch_args();
     using S = Shape<KT, VT, NB, RT>;
     constexpr int kRows = 16 * RT, kDim = 32 * NB, kTiles = 2 * NB, kWaves = S::kWaves, kDepth = S::kDepth;
-    constexpr bool kKeyBlocks = KT != kKvF16, kValBlocks = VT != kKvF16, kStaged = S::kStaged, kBiased = S::kBiased;
+    constexpr bool kKeyBlocks = KT != kKvF16, kValBlocks = VT != kKvF16, kStaged = S::kStaged;
     constexpr bool kEarly = S::kEarly;
     // Queries, then what is on its way, wave by wave; at the end the sums of the waves in their place.
     auto& lq = *(uint32_t(*)[RT][NB][2][64][4])lds;
@@ -866,7 +863,7 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
 
     int rlo[RT], rhi[RT];
     float c[RT];  // scores are c times the sums of the scaled operands
-    float4_t o[RT][kTiles], weights[RT][kBiased ? NB : 1];  // weights: 128 2^-24 times the sums of a block's
+    float4_t o[RT][kTiles];
     float m[RT], l[RT], limit[RT], fold[RT];
     int bound[RT];  // the binary16 bits of limit, a power of two above the scales of values that the row has seen
 #pragma unroll
@@ -883,10 +880,7 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
         bound[x] = 1;
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) o[x][t] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int b = 0; b < (kBiased ? NB : 1); ++b) weights[x][b] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
     }
-    const half8_t bias = as_half8(0x00800080u, 0x00800080u, 0x00800080u, 0x00800080u);    // 128 2^-24
     const half8_t minus = as_half8(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);  // -128 2^-24
     int least = 1;  // the least of the rows' bounds
     const auto queries = [&](int x, int b, int part) { return __builtin_bit_cast(half8_t, *(const u32x4*)lq[x][b][part][lane]); };
@@ -1002,10 +996,6 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
                 l[x] *= shrink;
 #pragma unroll
                 for (int t = 0; t < kTiles; ++t) o[x][t] *= shrink;
-                if constexpr (kBiased) {
-#pragma unroll
-                    for (int b = 0; b < NB; ++b) weights[x][b] *= shrink;
-                }
             }
         }
         // Weights: of binary16 values times 2^14; of blocks' to be multiplied by the scales and a power of two that
@@ -1071,10 +1061,6 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
                     bound[x] = to > 65536.0f ? 0x10000 : (int)f2h(to);
 #pragma unroll
                     for (int t = 0; t < kTiles; ++t) o[x][t] *= shrink;
-                    if constexpr (kBiased) {
-#pragma unroll
-                        for (int b = 0; b < NB; ++b) weights[x][b] *= shrink;
-                    }
                     now = min(now, bound[x]);
                 }
                 now = min(now, dpp_i<0xB1>(now));
@@ -1167,16 +1153,7 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
                     pl[x] = as_half8(lo[0], lo[1], lo[2], lo[3]);
                 }
             }
-            if constexpr (kBiased) {
-                if (t % 2 == 0) {
-#pragma unroll
-                    for (int x = 0; x < RT; ++x) {
-                        weights[x][t / 2] = __builtin_amdgcn_mfma_f32_16x16x32_f16(bias, pl[x], weights[x][t / 2], 0, 0, 0);
-                        weights[x][t / 2] = __builtin_amdgcn_mfma_f32_16x16x32_f16(bias, ph[x], weights[x][t / 2], 0, 0, 0);
-                    }
-                }
-            }
-            const half8_t v = Values<VT, NB>::template tile<kBiased>(ready, t);
+            const half8_t v = Values<VT, NB>::tile(ready, t);
 #pragma unroll
             for (int x = 0; x < RT; ++x) {
                 o[x][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, pl[x], o[x][t], 0, 0, 0);
@@ -1201,9 +1178,9 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
     for (int x = 0; x < RT; ++x) {
         l[x] = rows_sum(l[x]) * (kValBlocks ? 1.0f : power(-14));
         m[x] *= c[x];
-        const float back = kValBlocks ? limit[x] * power((kBiased ? 24 : 10) - 14) : power(-14);
+        const float back = kValBlocks ? limit[x] * power(10 - 14) : power(-14);
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t) o[x][t] = (kBiased ? o[x][t] - weights[x][kBiased ? t / 2 : 0] : o[x][t]) * back;
+        for (int t = 0; t < kTiles; ++t) o[x][t] *= back;
     }
     __syncthreads();
 #pragma unroll
