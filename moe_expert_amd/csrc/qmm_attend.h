@@ -398,10 +398,10 @@ __device__ __forceinline__ void load_bytes(uint32_t* w, const char* p) {
 }
 
 // Two biased bytes u = q + 128, which perm laid into the low bytes of two halves, are u 2^-24 as binary16 values: to
-// q 2^-10.  (Keys enter as they are, and what 128 in their place would give is where their sums begin.  For values that
-// costs digits: the sums of a long context's weights times 128 are far above those of its values.  8 sequences of 4096
-// positions, q8_0, were 9e-6 off so, and 2e-7 like this.)
-__device__ __forceinline__ uint32_t value_pair(uint32_t x) {
+// q 2^-10.  (They could enter the products as they are, and what 128 in their place gives be taken from the sums.  That
+// is no faster, the matrix instructions wait for the others, and costs digits: 128 times a long context's weights is
+// far above the sum of its values.  8 sequences of 4096 positions, q8_0, were 9e-6 off so, and are 2e-7.)
+__device__ __forceinline__ uint32_t byte_pair(uint32_t x) {
     const half2_t scale = {(_Float16)16384.0f, (_Float16)16384.0f}, bias = {(_Float16)-0.125f, (_Float16)-0.125f};
     return __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(__builtin_bit_cast(half2_t, x), scale, bias));
 }
@@ -458,10 +458,10 @@ struct Keys {
         for (int m = 0; m < 4; ++m) {
             if constexpr (TYPE == kKvQ8) {
                 const int at = (m * NB + b) * 2;
-                x[m] = perm(r.a[at / 4], r.a[at / 4], pair_sel(at % 4, at % 4 + 1));
+                x[m] = byte_pair(perm(r.a[at / 4], r.a[at / 4], pair_sel(at % 4, at % 4 + 1)));
             } else {
                 const int at = m * NB + b;
-                x[m] = perm(r.b[at / 4], r.a[at / 4], pair_sel(at % 4, at % 4 + 4));
+                x[m] = byte_pair(perm(r.b[at / 4], r.a[at / 4], pair_sel(at % 4, at % 4 + 4)));
             }
         }
         return as_half8(x[0], x[1], x[2], x[3]);
@@ -586,11 +586,11 @@ struct Values {
             if constexpr (TYPE == kKvF16) {
                 o[m] = perm(r.a[2 * m + 1][t / 2], r.a[2 * m][t / 2], t & 1 ? 0x07060302u : 0x05040100u);
             } else if constexpr (TYPE == kKvQ8) {
-                o[m] = value_pair(perm(r.a[2 * m + 1][t / 4], r.a[2 * m][t / 4], pair_sel(t % 4, t % 4 + 4)));
+                o[m] = byte_pair(perm(r.a[2 * m + 1][t / 4], r.a[2 * m][t / 4], pair_sel(t % 4, t % 4 + 4)));
             } else {
                 const int b = t / 2, i = b / 4, shared = kBytes % 4 == 2 && i == kWords - 1 ? 2 : 0;
                 const uint32_t lo = t & 1 ? r.b[2 * m][i] : r.a[2 * m][i], hi = t & 1 ? r.b[2 * m + 1][i] : r.a[2 * m + 1][i];
-                o[m] = value_pair(perm(hi, lo, pair_sel(b % 4, b % 4 + 4 + shared)));
+                o[m] = byte_pair(perm(hi, lo, pair_sel(b % 4, b % 4 + 4 + shared)));
             }
         }
         return as_half8(o[0], o[1], o[2], o[3]);
@@ -853,7 +853,7 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
             lq[x][b][0][16 * (j / 4) + r % 16][j % 4] = hi;
             lq[x][b][1][16 * (j / 4) + r % 16][j % 4] = lo;
         }
-        if (j == 0) lc[r] = power(e - 14 + (kKeyBlocks ? 24 : 0));
+        if (j == 0) lc[r] = power(e - 14 + (kKeyBlocks ? 10 : 0));
     }
     if (kStaged && kDepth > 1 && ksteps > 1) {
         fetch_keys(1);
@@ -881,7 +881,6 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) o[x][t] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
     }
-    const half8_t minus = as_half8(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);  // -128 2^-24
     int least = 1;  // the least of the rows' bounds
     const auto queries = [&](int x, int b, int part) { return __builtin_bit_cast(half8_t, *(const u32x4*)lq[x][b][part][lane]); };
 
@@ -923,15 +922,10 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
 #pragma unroll
                 for (int x = 0; x < RT; ++x) {
                     const half8_t qh = queries(x, b, 0), ql = queries(x, b, 1);
-                    float4_t begin = {0.0f, 0.0f, 0.0f, 0.0f};
-                    if constexpr (kKeyBlocks) {
-                        begin = __builtin_amdgcn_mfma_f32_16x16x32_f16(minus, ql, begin, 0, 0, 0);
-                        begin = __builtin_amdgcn_mfma_f32_16x16x32_f16(minus, qh, begin, 0, 0, 0);
-                    }
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         if constexpr (kKeyBlocks) {
-                            float4_t u = __builtin_amdgcn_mfma_f32_16x16x32_f16(kb[h], ql, begin, 0, 0, 0);
+                            float4_t u = __builtin_amdgcn_mfma_f32_16x16x32_f16(kb[h], ql, float4_t{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
                             u = __builtin_amdgcn_mfma_f32_16x16x32_f16(kb[h], qh, u, 0, 0, 0);
 #pragma unroll
                             for (int r = 0; r < 4; ++r) z[x][4 * h + r] = __builtin_fmaf(u[r], keys[h].scale(r, b), z[x][4 * h + r]);
