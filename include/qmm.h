@@ -506,7 +506,8 @@ size_t qmm_kv_attend_workspace(const qmm_kv_cache* cache, int64_t ntok, int nhea
  *   cache->vtype holds at most as many bits as cache->ktype (an error of a key enters the exponent).
  *   ws   : qmm_kv_attend_workspace() bytes, 16-byte aligned; nothing in it is kept between calls, and
  *          calls that may overlap in time need one each.
- * Results do not depend on scheduling.
+ * Results do not depend on scheduling.  Offsets that decrease so that sequences have more tokens than ntok in
+ * all: nothing is written.
  * Errors: QMM_EINVAL, QMM_EALIGN, QMM_EUNSUPPORTED, QMM_ESPACE. */
 int qmm_kv_attend(const qmm_kv_cache* cache, const int32_t* pages, int64_t ldpages, int64_t max_pages,
                   const int32_t* lens, const int32_t* seg_off, int nseq, int qtype, const void* q,

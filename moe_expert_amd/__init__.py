@@ -980,7 +980,6 @@ def qmm_kv_read(cache, pages, lens, k=None, v=None, seg_off=None, ntok=None, str
         if isinstance(t, torch.dtype):
             if t not in (_TYPE_OF or _types()):
                 raise ValueError(f"{name}: {t} is not a type that this call writes")
-            # rows of no sequence would be whatever the memory held
             t = outs[i] = _empty(shape, t, dev, stream)
         ct, lds[i] = _rows(t, name, shape, dev)
         if code and ct != code:

@@ -234,6 +234,31 @@ def test_many_sequences():
     Case(lens, new=new, heads=2, kv=1, dim=64, kinds=("f16", "f16")).check()
 
 
+@pytest.mark.parametrize("lens,kv", [([40000], 8), ([50000], 7), ([9000, 30000, 7, 0, 2000], 5), ([12000] * 3, 8), ([3000, 0, 70] * 20, 6)])
+@pytest.mark.parametrize("kinds", [("f16", "q8_0"), ("iq4_nl", "iq4_nl")])
+def test_long_lines(lens, kv, kinds):
+    """Enough steps that workgroups take unequal lengths in turn, of one sequence and of several, whose ends lie in either."""
+    print(f"attend {lens[:5]} {kv} {kinds}", flush=True)
+    Case(lens, kinds=kinds, heads=kv, kv=kv, dim=64, page=64, seed=kv).check()
+
+
+def test_long_line_of_many_sequences():
+    rng = np.random.default_rng(12)
+    lens = [int(x) for x in rng.integers(0, 900, 300)]
+    Case(lens, kinds=("q8_0", "q8_0"), heads=4, kv=2, dim=64, page=32).check()
+
+
+def test_offsets_that_decrease():
+    """More tokens than there are, by offsets that do not stand for any split: nothing is written."""
+    off = np.array([0, 4, 2, 6], np.int32)
+    c = Case([40, 50, 60], off=off, heads=2, kv=1, dim=64)
+    got, lse = c.run()
+    assert (host(got) == 7.0).all() and (host(lse) == 7.0).all()
+    c = Case([40] * 300, off=np.arange(300, -1, -1).astype(np.int32).clip(2), heads=2, kv=1, dim=64)
+    got, lse = c.run()
+    assert np.isfinite(host(got)).all()
+
+
 @pytest.mark.parametrize("pad,offset", [(3, 0), (0, 1), (16, 8), (5, 3)])
 @pytest.mark.parametrize("name", ["f32", "f16"])
 def test_strides(pad, offset, name):

@@ -253,3 +253,49 @@ def test_many_sequences():
     k, v = M.qmm_kv_read(cache, *args, k=dtype("f32"), v=dtype("f32"), seg_off=dev(off), ntok=int(off[-1]))
     assert np.array_equal(host(k), R.stored(x, "iq4_nl").astype(np.float32))
     assert np.array_equal(host(v), R.stored(x, "q8_0").astype(np.float32))
+
+
+def test_streams_and_graphs():
+    """A call on a stream given by handle, and writes with reads behind them in a captured graph whose rows, lengths and
+    pages change between the replays, eager calls of another cache beside them."""
+    import torch
+    rng = np.random.default_rng(8)
+    lens = np.array([40, 7, 100], np.int32)
+    off = dev(np.array([0, 5, 6, 26], np.int32))
+    pages, npages = R.tables(rng, lens, 16, width=9)
+    pages, lens = dev(pages), dev(lens)
+    caches = [M.KvCache.empty(M.QMM_Q8_0, M.QMM_IQ4_NL, npages, 2, 64, 16) for _ in range(2)]
+    x = dev(rng.standard_normal((26, 128)).astype(np.float32))
+    outs = [[torch.empty_like(x) for _ in range(2)] for _ in range(2)]
+
+    def run(i, stream=None):
+        M.qmm_kv_write(caches[i], pages, lens, x, x, seg_off=off, stream=stream)
+        M.qmm_kv_read(caches[i], pages, lens, k=outs[i][0], v=outs[i][1], seg_off=off, stream=stream)
+
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    run(0)
+    run(1, side.cuda_stream)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(*outs)) and torch.equal(caches[0].k, caches[1].k)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run(0)
+    for step in range(4):
+        x.normal_()
+        lens.copy_(dev(np.array([40 - step, 7 + 3 * step, 100 - 20 * step], np.int32)))
+        pages.copy_(pages.roll(step, 1))
+        g.replay()
+        run(1)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(*outs))
+        assert torch.equal(caches[0].k, caches[1].k) and torch.equal(caches[0].v, caches[1].v)
+
+
+def test_many_rows():
+    """More rows than workgroups fit at once, so that the keys and values of a row are one workgroup's."""
+    rng = np.random.default_rng(9)
+    new = [1500, 1, 700, 0, 900]
+    off = np.concatenate([[0], np.cumsum(new)])
+    x = (rng.standard_normal((off[-1], 6 * 64)) * np.exp(rng.standard_normal(6 * 64))).astype(np.float32)
+    check(("q8_0", "iq4_nl"), x, [1600, 1, 705, 3, 900], off, 64, 64, 6)
