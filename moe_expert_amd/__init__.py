@@ -31,6 +31,7 @@ QMM_FLAG_DEBUG_INTERMEDIATES = 1
 QMM_TYPE_F32, QMM_TYPE_F16, QMM_TYPE_BF16 = 1, 2, 3
 QMM_SCORE_SOFTMAX, QMM_SCORE_SIGMOID = 0, 1
 QMM_ROUTE_RENORM = 1
+QMM_ESPACE = -5
 BLOCK_VALUES = {QMM_Q8_0: 32, QMM_IQ4_NL: 32, QMM_CB3: 256, QMM_F16: 1}
 BLOCK_BYTES = {QMM_Q8_0: 34, QMM_IQ4_NL: 18, QMM_CB3: 110, QMM_F16: 2}
 Q8_1_BYTES = 36
@@ -960,10 +961,11 @@ def qmm_kv_read(cache, pages, lens, k=None, v=None, seg_off=None, ntok=None, str
     each sequence); None for what is not wanted.  Positions that do not exist give rows of zeros; rows of
     no sequence are left alone.  Returns (k, v)."""
     import torch
-    dev = cache.device
-    for t in (k, v):
-        if t is not None and not isinstance(t, torch.dtype):
+    dtype, dev = torch.dtype, cache.device
+    for t in (v, k):
+        if t is not None and not isinstance(t, dtype):
             ntok = _matrix(t, "k and v", "[ntok, nheads * head_dim] or a dtype")[0]
+            break
     if ntok is None:
         if seg_off is not None:
             raise ValueError("ntok is required for new tensors of ragged sequences")
@@ -971,23 +973,29 @@ def qmm_kv_read(cache, pages, lens, k=None, v=None, seg_off=None, ntok=None, str
     if ntok < 0:
         raise ValueError("ntok must not be negative")
     nseq, width, ldp = _kv_sequences(cache, pages, lens, seg_off, ntok)
-    shape, code, lds, outs = (ntok, cache.width), 0, [0, 0], [k, v]
-    if k is None and v is None:
-        raise ValueError("k or v is required")
-    for i, (t, name) in enumerate(((k, "k"), (v, "v"))):
-        if t is None:
-            continue
-        if isinstance(t, torch.dtype):
-            if t not in (_TYPE_OF or _types()):
-                raise ValueError(f"{name}: {t} is not a type that this call writes")
-            t = outs[i] = _empty(shape, t, dev, stream)
-        ct, lds[i] = _rows(t, name, shape, dev)
-        if code and ct != code:
+    kt = vt = ldk = ldv = 0
+    if k is not None:
+        if isinstance(k, dtype):
+            k = _kv_rows_of(k, "k", (ntok, cache.width), dev, stream)
+        kt, ldk = _rows(k, "k", (ntok, cache.width), dev)
+    if v is not None:
+        if isinstance(v, dtype):
+            v = _kv_rows_of(v, "v", (ntok, cache.width), dev, stream)
+        vt, ldv = _rows(v, "v", (ntok, cache.width), dev)
+        if kt and vt != kt:
             raise ValueError("k and v must have the same dtype")
-        code = ct
-    _call("qmm_kv_read", dev, stream, cache._ref, pages.data_ptr(), ldp, width, lens.data_ptr(), _addr(seg_off), nseq, code,
-          _addr(outs[0]), lds[0], _addr(outs[1]), lds[1], ntok)
-    return tuple(outs)
+    if not kt and not vt:
+        raise ValueError("k or v is required")
+    _call("qmm_kv_read", dev, stream, cache._ref, pages.data_ptr(), ldp, width, lens.data_ptr(), _addr(seg_off), nseq, kt or vt,
+          _addr(k), ldk, _addr(v), ldv, ntok)
+    return k, v
+
+
+def _kv_rows_of(dtype, name, shape, device, stream):
+    """A new tensor that a read fills."""
+    if dtype not in (_TYPE_OF or _types()):
+        raise ValueError(f"{name}: {dtype} is not a type that this call writes")
+    return _empty(shape, dtype, device, stream)
 
 
 def qmm_kv_attend_workspace(cache, ntok, nheads, nseq, max_pages):
@@ -1025,8 +1033,19 @@ def qmm_kv_attend(q, cache, pages, lens, seg_off=None, scale=None, window=0, out
         _flat(lse, "lse", torch.float32, ntok * nheads, dev)
     if not 0 <= window <= 0x7FFFFFFFFFFFFFFF:
         raise ValueError("window must not be negative")
-    ws = _scratch(ws, qmm_kv_attend_workspace(cache, ntok, nheads, nseq, maxp), dev, stream)
-    _call("qmm_kv_attend", dev, stream, cache._ref, pages.data_ptr(), ldp, maxp, lens.data_ptr(), _addr(seg_off), nseq, qt,
-          q.data_ptr(), ldq, ntok, nheads, dim ** -0.5 if scale is None else scale, window, ot, out.data_ptr(), ldo, _addr(lse),
-          ws.data_ptr(), ws.numel())
+    own = ws is None
+    if own:
+        ws = _scratch(None, qmm_kv_attend_workspace(cache, ntok, nheads, nseq, maxp), dev, stream)
+    else:
+        _flat(ws, "ws", torch.uint8, 16, dev)
+    try:
+        _call("qmm_kv_attend", dev, stream, cache._ref, pages.data_ptr(), ldp, maxp, lens.data_ptr(), _addr(seg_off), nseq, qt,
+              q.data_ptr(), ldq, ntok, nheads, dim ** -0.5 if scale is None else scale, window, ot, out.data_ptr(), ldo, _addr(lse),
+              ws.data_ptr(), ws.numel())
+    except QmmError as e:
+        if e.status != QMM_ESPACE or own:
+            raise
+        # (the library knows how much it needs: asked for the message alone, a call costs a microsecond)
+        _flat(ws, "ws", torch.uint8, qmm_kv_attend_workspace(cache, ntok, nheads, nseq, maxp), dev)
+        raise
     return out, lse

@@ -39,7 +39,7 @@ __global__ __launch_bounds__(1024) void attend_plan_kernel(AttendArgs a, int row
 
 // The pieces of a tile joined, in their order, by as many workgroups as it has pieces: they share the tile's groups of
 // four dims.  A group's pieces go to E lanes of a wave, each every E-th of them, lanes of neighbouring groups
-// beside each other.  Bound: two loads one after the other (what the pass told, the pieces).
+// beside each other.  Bound: two loads one after the other (what the pass told, the pieces): 4 us, 2.5 at least.
 template <int E>
 __device__ __forceinline__ void join(const AttendArgs& a, const Piece& t, int run, int head, int tile_rows) {
     const int dim = a.p.dim, row0 = (t.rows >> 6) * tile_rows, rows = t.rows & 63, quads = rows * (dim / 4), from = run - t.mine;

@@ -248,6 +248,16 @@ def test_long_line_of_many_sequences():
     Case(lens, kinds=("q8_0", "q8_0"), heads=4, kv=2, dim=64, page=32).check()
 
 
+def test_workspace_too_small():
+    import torch
+    c = Case([400, 90], heads=4, kv=2, dim=64)
+    need = M.qmm_kv_attend_workspace(c.cache(), 2, 4, 2, c.pages.shape[1])
+    for n in (16, need - 1):
+        with pytest.raises(ValueError, match="ws must be"):
+            c.run(ws=torch.empty(n, dtype=torch.uint8, device="cuda"))
+    c.compare(*c.run(ws=torch.empty(need, dtype=torch.uint8, device="cuda")), c.want(), "f32")
+
+
 def test_offsets_that_decrease():
     """More tokens than there are, by offsets that do not stand for any split: nothing is written."""
     off = np.array([0, 4, 2, 6], np.int32)
