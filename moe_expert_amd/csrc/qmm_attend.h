@@ -35,7 +35,9 @@ typedef float float4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kAtLds = 80 * 1024 - 512;  // bytes of LDS of a workgroup of which two share a CU
 constexpr int kAtStep = 32;      // positions a step
-constexpr int kAtInline = 256;   // sequences that a workgroup plans by itself; beyond, a launch of its own
+// Sequences that a workgroup plans by itself; beyond, a launch of its own (128 of up to 1000 positions: 32.4 us, with the
+// launch 33.1; 256: 52.2, 48.4).
+constexpr int kAtInline = 128;
 
 // What a workgroup leaves of a tile that goes on beyond it: the tile's pieces (0: none) and which of them, and its rows.
 struct Piece {
@@ -119,7 +121,7 @@ __device__ __forceinline__ SeqWork lane_work(const AttendArgs& a, int s, int row
 //
 // Where the pieces of a length c, every tile cut by itself, are no more than the workgroups, and c is not much longer
 // than the equal share of the steps, tiles take whole lengths: a workgroup has one piece then, and pays once for what
-// it does beside its steps (kAtCost steps of its time, about).
+// it does beside its steps (kAtCost steps of its time, about; 32 of up to 4096: 24.1 us, 28.7 without).
 //
 // A length is a multiple of a step for each of four waves: one where the pieces then are no more than the CUs (1 x 1024
 // q8_0: 10.9 us, with two 13.0), else two (16 x 4 tokens, 192 wide, a window of 1000: 21.5 us, with one 23.4).
