@@ -75,19 +75,23 @@ __device__ __forceinline__ void join(const AttendArgs& a, const Piece& t, int ru
     }
 }
 
-// blockIdx.y: the workgroup's piece of a tile that began before it, or of one that begins there.
+// The workgroup's piece of a tile that began before it, then of one that begins there (seldom both).
 __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, int tile_rows) {
     uint32_t head;
     const int run = (int)kv_divide(blockIdx.x, a.p.nheads, a.p.per_head, head);
-    const Piece t = a.pieces[2 * run + blockIdx.y];
-    if (t.count == 0) return;
-    // As few pieces a lane as leave a lane to every group at once (32 x 256 wide, 16 rows: 28 us, with 8 lanes a group 31).
-    const int room = 256 * t.count, quads = (t.rows & 63) * (a.p.dim / 4);
-    if (t.count >= 16 && room >= 16 * quads) join<16>(a, t, run, (int)head, tile_rows);
-    else if (t.count >= 8 && room >= 8 * quads) join<8>(a, t, run, (int)head, tile_rows);
-    else if (t.count >= 4 && room >= 4 * quads) join<4>(a, t, run, (int)head, tile_rows);
-    else if (room >= 2 * quads) join<2>(a, t, run, (int)head, tile_rows);
-    else join<1>(a, t, run, (int)head, tile_rows);
+    const Piece both[2] = {a.pieces[2 * run], a.pieces[2 * run + 1]};
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) {
+        const Piece t = i ? both[1] : both[0];
+        if (t.count == 0) continue;
+        // As few pieces a lane as leave a lane to every group at once (32 x 256 wide, 16 rows: 28 us, with 8 lanes a group 31).
+        const int room = 256 * t.count, quads = (t.rows & 63) * (a.p.dim / 4);
+        if (t.count >= 16 && room >= 16 * quads) join<16>(a, t, run, (int)head, tile_rows);
+        else if (t.count >= 8 && room >= 8 * quads) join<8>(a, t, run, (int)head, tile_rows);
+        else if (t.count >= 4 && room >= 4 * quads) join<4>(a, t, run, (int)head, tile_rows);
+        else if (room >= 2 * quads) join<2>(a, t, run, (int)head, tile_rows);
+        else join<1>(a, t, run, (int)head, tile_rows);
+    }
 }
 
 }  // namespace qmm
@@ -193,6 +197,6 @@ extern "C" int qmm_kv_attend(const qmm_kv_cache* c, const int32_t* pages, int64_
     if (c->ktype == QMM_F16) attend_f16(a, grid, s.rt, st);
     else if (c->ktype == QMM_Q8_0) attend_q8(a, grid, s.rt, st);
     else attend_iq4(a, grid, s.rt, st);
-    if (s.split) hipLaunchKernelGGL(attend_join_kernel, dim3(grid, 2), dim3(256), 0, st, a, 16 * s.rt);
+    if (s.split) hipLaunchKernelGGL(attend_join_kernel, dim3(grid), dim3(256), 0, st, a, 16 * s.rt);
     return launch_status();
 }
