@@ -16,9 +16,9 @@
 // binary16 parts, 2^-22 of the value in all, after a power of two a row that puts the largest near 2^14, so the second
 // part keeps 2^-24 2^-14 of it.  One part alone would cost 2^-11, the error of a binary16 output.
 //
-// Bounds.  Binary16: the cache's bytes (32 sequences of 8192 positions, 4 heads of 128: 99 us, 5.4 TB/s).  Block formats:
+// Bounds.  Binary16: the cache's bytes (32 sequences of 8192 positions, 4 heads of 128: 98 us, 5.5 TB/s).  Block formats:
 // the vector instructions of a step, some 380 for 32 positions of q8_0 and 590 of iq4_nl at 128 wide, most of them to unpack
-// the bytes and to scale and cut the weights once a block (64 us, 4.4 TB/s; 60 us, 2.5 TB/s); the matrix units are
+// the bytes and to scale and cut the weights once a block (63 us, 4.5 TB/s; 62 us, 2.4 TB/s); the matrix units are
 // busy an eighth of the time.  Few positions: one load after the other (arguments, lengths, pages, keys), 5 us until
 // the first step, 1 us behind the last, and the join's launch.
 #pragma once
