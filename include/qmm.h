@@ -488,7 +488,7 @@ int qmm_kv_read(const qmm_kv_cache* cache, const int32_t* pages, int64_t ldpages
                 const int32_t* lens, const int32_t* seg_off, int nseq, int otype, void* k, int64_t ldk,
                 void* v, int64_t ldv, int64_t ntok, void* stream);
 
-/* Workspace bytes qmm_kv_attend needs (host); 0 for sizes it does not take. */
+/* Workspace bytes qmm_kv_attend needs (host), enough for calls of smaller sizes too; 0 for sizes it does not take. */
 size_t qmm_kv_attend_workspace(const qmm_kv_cache* cache, int64_t ntok, int nheads, int nseq,
                                int64_t max_pages);
 

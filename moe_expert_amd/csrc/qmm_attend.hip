@@ -128,16 +128,22 @@ int attend_shape(AttendShape& s, const qmm_kv_cache* c, const int32_t* pages, in
     // by 16; 8 tokens of 5, binary16: 42, 68).  Two tiles of wider heads do not fit the registers.
     const bool wide = c->head_dim <= 128;
     s.rt = wide && nseq && group * ((ntok + nseq - 1) / nseq) > 16 ? 2 : 1;
-    const int64_t rows = 16 * s.rt, tiles = std::min(nseq + ntok * group / rows, ntok * ((group + rows - 1) / rows));
     // At most this many steps a tile (a walk may begin 15 positions early), and so workgroups with a length of the line.
     const int64_t steps = (max_pages * c->page_size + kAtStep - 1) / kAtStep + 1;
-    const int64_t line = tiles * ((steps + kAtWaves - 1) / kAtWaves);
-    s.target = (int)std::max(std::min((int64_t)(kAtTarget / c->nheads), line), (int64_t)1);
+    const auto tiles_of = [&](int64_t rows) { return std::min(nseq + ntok * group / rows, ntok * ((group + rows - 1) / rows)); };
+    const auto target_of = [&](int64_t tiles) {
+        return (int)std::max(std::min((int64_t)(kAtTarget / c->nheads), tiles * ((steps + kAtWaves - 1) / kAtWaves)), (int64_t)1);
+    };
+    const int64_t tiles = tiles_of(16 * s.rt), most = tiles_of(16);
+    s.target = target_of(tiles);
     for (s.shift = 0; (tiles * std::max(steps, (int64_t)kAtLeast)) >> s.shift > 1 << 29;) ++s.shift;
     s.split = steps > kAtWaves || tiles > s.target;
-    // (sized for 32 rows where a call of other proportions would take them)
-    s.told = s.split ? (size_t)(2 * s.target * c->nheads * part_floats(wide ? 32 : 16, c->head_dim) * 4) : 0;
-    s.plan = s.told + (s.split ? 2 * s.target * sizeof(Piece) : 0);
+    // The size for tiles of 16 rows, which are more, and of 32, which are larger: what is enough for a call is enough for
+    // smaller ones, of whatever proportions.
+    const int room = target_of(most);
+    const bool pieces = steps > kAtWaves || most > room;
+    s.told = pieces ? (size_t)(2 * room * c->nheads * part_floats(wide ? 32 : 16, c->head_dim) * 4) : 0;
+    s.plan = s.told + (pieces ? 2 * room * sizeof(Piece) : 0);
     s.bytes = s.plan + (nseq > kAtInline ? (size_t)(nseq + 4) * 4 : 0);
     s.bytes = s.bytes < 16 ? 16 : s.bytes;
     return QMM_OK;

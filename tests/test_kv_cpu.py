@@ -98,6 +98,16 @@ def test_attend(kw, expect):
     assert M.lib().qmm_kv_attend(*a.values()) == expect
 
 
+@pytest.mark.parametrize("heads,dim", [(1, 64), (3, 128), (4, 256), (8, 96)])
+def test_workspace_is_enough_for_smaller_calls(heads, dim):
+    cache = struct(nheads=heads, head_dim=dim, kstride=1 << 30, vstride=1 << 30)
+    need = np.array([[[[M.lib().qmm_kv_attend_workspace(C.addressof(cache), n, heads * g, s, p) for p in (1, 2, 5, 40, 3000)]
+                       for s in (1, 2, 3, 7, 40, 127, 128, 129, 300)] for n in (1, 2, 3, 5, 16, 17, 40, 300, 1000)] for g in (1, 2, 5, 8, 16, 40)])
+    assert (need >= 16).all()
+    for axis in range(4):
+        assert (np.diff(need, axis=axis) >= 0).all(), f"axis {axis}"
+
+
 def test_attend_formats():
     """Values of more bits than the keys are declined."""
     order = [M.QMM_IQ4_NL, M.QMM_Q8_0, M.QMM_F16]
