@@ -125,8 +125,13 @@ __device__ __forceinline__ SeqWork lane_work(const AttendArgs& a, int s, int row
 //
 // A length is a multiple of a step for each of four waves: one where the pieces then are no more than the CUs (1 x 1024
 // q8_0: 10.9 us, with two 13.0), else two (16 x 4 tokens, 192 wide, a window of 1000: 21.5 us, with one 23.4).
+//
+// Where a table holds up to kAtShort steps and the tiles fill the CUs by themselves, or half as many, and there are no
+// more tiles than workgroups, nothing is split, which saves the join's launch (64 x 512 q8_0: 14.9 us, split 18.4;
+// 16 x 256: 9.6, 10.5; but 16 x 512, a quarter of the CUs: 13.6, split 11.4).
 constexpr int kAtCost = 12;
 constexpr int kAtWaves = 4;
+constexpr int kAtShort = 18;
 
 // Of two workgroups on a CU the one that came first is served first and ends first (32 x 8192 q8_0: after 38.7 us, the
 // other after 48.3), so where lengths are long the workgroups take the line in pairs, one of the first half and one
@@ -158,6 +163,8 @@ __device__ __forceinline__ int tile_units(const AttendArgs& a, int steps, const 
 // take.  Offsets that decrease give more tokens than there are: nothing is done then.
 template <class F>
 __device__ __forceinline__ Split line_split(const AttendArgs& a, int units, int tiles, int64_t tokens, F lengths) {
+    if (!a.pieces && !a.plan)  // a workgroup a tile
+        return Split{2 * kAtShort, kAtShort, tokens > a.p.ntok ? 0 : tiles * kAtShort, kAtShort, false};
     Split s;
     const int target = a.target, step = max(kAtWaves >> a.shift, 1);
     const auto rounded = [&](int len) { return max((len + step - 1) & -step, step); };  // as many steps for every wave

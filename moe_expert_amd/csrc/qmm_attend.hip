@@ -137,7 +137,9 @@ int attend_shape(AttendShape& s, const qmm_kv_cache* c, const int32_t* pages, in
     const int64_t tiles = tiles_of(16 * s.rt), most = tiles_of(16);
     s.target = target_of(tiles);
     for (s.shift = 0; (tiles * std::max(steps, (int64_t)kAtLeast)) >> s.shift > 1 << 29;) ++s.shift;
-    s.split = steps > kAtWaves || tiles > s.target;
+    const int whole = nseq > kAtInline ? kAtWaves : tiles * c->nheads >= kAtTarget / 2 ? kAtShort : kAtShort / 2;
+    s.split = steps > whole || tiles > s.target;
+    if (!s.split) s.target = (int)std::max(tiles, (int64_t)1);
     // The size for tiles of 16 rows, which are more, and of 32, which are larger: what is enough for a call is enough for
     // smaller ones, of whatever proportions.
     const int room = target_of(most);

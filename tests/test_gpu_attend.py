@@ -84,6 +84,16 @@ def test_formats(dim, kinds):
     Case([1, 2, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129, 300], kinds=kinds, dim=dim, heads=10, kv=2, seed=dim).check()
 
 
+@pytest.mark.parametrize("dim", [64, 96, 128, 192, 256])
+@pytest.mark.parametrize("kinds", PAIRS)
+def test_formats_in_pieces(dim, kinds):
+    """The same behind tables wide enough that sequences may be split, and on both sides of that."""
+    print(f"attend in pieces {dim} {kinds}", flush=True)
+    Case([1, 33, 130, 300, 512, 515, 639], kinds=kinds, dim=dim, heads=10, kv=2, seed=dim, width=40).check()
+    for width in (16, 18, 34, 36):
+        Case([16 * width, 16 * width - 15, 3], kinds=kinds, dim=dim, heads=10, kv=2, seed=width, width=width).check()
+
+
 @pytest.mark.parametrize("name", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("out", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("kinds", [("f16", "f16"), ("q8_0", "iq4_nl")])
