@@ -387,6 +387,30 @@ def test_streams_and_graphs():
             assert torch.equal(out, o) and torch.equal(lse, l)
 
 
+@pytest.mark.parametrize("nseq,longest", [(150, 700), (40, 200), (3, 200)])
+def test_graph_of_other_lengths(nseq, longest):
+    """Captured calls that plan in a launch of their own, and that do not split: lengths and tables change between the replays."""
+    import torch
+    rng = np.random.default_rng(nseq)
+    c = Case([int(x) for x in rng.integers(0, longest, nseq)], kinds=("q8_0", "iq4_nl"), heads=4, kv=2, dim=64, page=32)
+    cache = c.cache()
+    pages, lens, _ = c.args()
+    out, lse = torch.empty_like(c.q), torch.empty(nseq, 4, device="cuda")
+    ws = torch.empty(M.qmm_kv_attend_workspace(cache, nseq, 4, nseq, pages.shape[1]), dtype=torch.uint8, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        M.qmm_kv_attend(c.q, cache, pages, lens, out=out, lse=lse, ws=ws)
+    for step in range(4):
+        lens.copy_(lens.roll(1) - step)
+        pages.copy_(pages.roll(step, 0))
+        ws.fill_(255 * (step % 2))
+        g.replay()
+        want = M.qmm_kv_attend(c.q, cache, pages, lens, lse=True)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
 def test_written_then_attended():
     """A request's life: its prompt written and attended, then tokens one and three at a time, against the
     attention over the values as they were stored."""
