@@ -104,7 +104,11 @@ using namespace qmm;
 
 namespace {
 
-constexpr int kAtTarget = 512;  // workgroups: two for every CU, what runs at once
+constexpr int kAtCus = 256;
+// Workgroups run two on a CU, but for keys and values of q8_0 that are 256 wide, whose eight waves take the LDS of a whole
+// one (8 x 4096: 25 us, split for two a CU, one after the other, 33; 64 of up to 1500: 39, 34).
+static_assert(Shape<kKvQ8, kKvQ8, 8, 1>::kWaves == 8 && Shape<kKvQ8, kKvIq4, 8, 1>::kWaves == 4 && Shape<kKvF16, kKvQ8, 8, 1>::kWaves == 4 &&
+              Shape<kKvQ8, kKvQ8, 6, 1>::kWaves == 4 && Shape<kKvQ8, kKvQ8, 4, 2>::kWaves == 4, "as attend_shape counts them");
 constexpr int kAtLeast = 8;     // steps that a tile counts for at least on the line
 
 struct AttendShape {
@@ -129,15 +133,16 @@ int attend_shape(AttendShape& s, const qmm_kv_cache* c, const int32_t* pages, in
     const bool wide = c->head_dim <= 128;
     s.rt = wide && nseq && group * ((ntok + nseq - 1) / nseq) > 16 ? 2 : 1;
     // At most this many steps a tile (a walk may begin 15 positions early), and so workgroups with a length of the line.
+    const bool alone = c->ktype == QMM_Q8_0 && c->vtype == QMM_Q8_0 && c->head_dim == 256;
     const int64_t steps = (max_pages * c->page_size + kAtStep - 1) / kAtStep + 1;
     const auto tiles_of = [&](int64_t rows) { return std::min(nseq + ntok * group / rows, ntok * ((group + rows - 1) / rows)); };
     const auto target_of = [&](int64_t tiles) {
-        return (int)std::max(std::min((int64_t)(kAtTarget / c->nheads), tiles * ((steps + kAtWaves - 1) / kAtWaves)), (int64_t)1);
+        return (int)std::max(std::min((int64_t)((alone ? 1 : 2) * kAtCus / c->nheads), tiles * ((steps + kAtWaves - 1) / kAtWaves)), (int64_t)1);
     };
     const int64_t tiles = tiles_of(16 * s.rt), most = tiles_of(16);
     s.target = target_of(tiles);
     for (s.shift = 0; (tiles * std::max(steps, (int64_t)kAtLeast)) >> s.shift > 1 << 29;) ++s.shift;
-    const int whole = nseq > kAtInline ? kAtWaves : tiles * c->nheads >= kAtTarget / 2 ? kAtShort : kAtShort / 2;
+    const int whole = nseq > kAtInline ? kAtWaves : tiles * c->nheads >= kAtCus ? kAtShort : kAtShort / 2;
     s.split = steps > whole || tiles > s.target;
     if (!s.split) s.target = (int)std::max(tiles, (int64_t)1);
     // The size for tiles of 16 rows, which are more, and of 32, which are larger: what is enough for a call is enough for
@@ -194,7 +199,7 @@ extern "C" int qmm_kv_attend(const qmm_kv_cache* c, const int32_t* pages, int64_
     a.scale = (float)((double)scale * 1.4426950408889634);
     a.window = (int)std::min(window, (int64_t)0x7FFFFFFF);  // more than any position
     a.target = s.target;
-    a.one = std::max(kAtTarget / 2 / c->nheads, 1);
+    a.one = std::max(kAtCus / c->nheads, 1);
     a.shift = s.shift;
     a.per_target = kv_per(a.target);
     a.least = kAtLeast;
