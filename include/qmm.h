@@ -496,10 +496,12 @@ size_t qmm_kv_attend_workspace(const qmm_kv_cache* cache, int64_t ntok, int nhea
  * token t of sequence s at position p, head h, and the cache's head h / (nheads / cache->nheads):
  *   z_j = scale * sum_c q[t][h][c] * key_j[c],   j <= p, j > p - window if window > 0, j existing
  *   out[t][h] = sum_j exp(z_j - max z) * value_j / sum_j exp(z_j - max z),   lse[t][h] = log sum_j exp(z_j)
- * with binary32 scores, statistics and sums.  No j (a token before position 0, an empty sequence, missing
- * pages): out 0, lse -inf.  Positions a token does not see have no effect on it, whatever they hold.  A
- * row of q that is not finite gives NaN in its own outputs.  Meant for up to some tens of tokens a sequence
- * (any count is right: each 16 or 32 rows of queries read the cache once).
+ * with binary32 scores, statistics and sums; query values and weights are kept to 2^-22 of themselves, or to 2^-38 of
+ * the row's largest (query value; weight, times the largest scale seen of the block where values are blocks).  No j
+ * (a token before position 0, an empty sequence, missing pages): out 0, lse -inf.  Positions a token does not see have no
+ * effect on it, whatever they hold.  A row of q that is not finite gives NaN in its own outputs.  Blocks of values seen
+ * with a scale that is not finite give NaN in their own dims.  Meant for up to some tens of tokens a sequence (any
+ * count is right: each 16 or 32 rows of queries read the cache once).
  *   q    : qtype [ntok][ldq], rows of nheads * head_dim values.   nheads : a multiple of cache->nheads, at
  *          most 1024.   scale : finite.   window : >= 0.
  *   out  : otype [ntok][ldo], must not overlap q.   lse : float [ntok][nheads] or NULL.

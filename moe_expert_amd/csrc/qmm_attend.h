@@ -10,11 +10,14 @@
 // the contraction runs over positions in the order (g, half, 0..3), so no weight moves between lanes, and every
 // statistic of a row belongs to its lane.
 //
-// Nothing is rounded on the way that binary32 would keep: a block's integers are exact in binary16 (as
-// (u - 128) 2^-10 of the biased byte u), its scale joins behind the products of the keys (one instruction a
-// score and block) and before those of the values, into the weights; queries and weights enter in two
-// binary16 parts, 2^-22 of the value in all, after a power of two a row that puts the largest near 2^14, so the second
-// part keeps 2^-24 2^-14 of it.  One part alone would cost 2^-11, the error of a binary16 output.
+// What is rounded beside binary32's own: queries and weights, which enter the products in two binary16 parts, 2^-22 of the
+// value in all but no finer than 2^-25 after a power of two that puts the row's largest near 2^14, 2^-39 of that.  One part
+// alone would cost 2^-11, the error of a binary16 output; more parts, to keep 2^-22 of a weight far below the row's
+// largest, half as many instructions again.  A block's integers are exact in binary16 (as (u - 128) 2^-10 of the biased
+// byte u), its scale joins behind the products of the keys (one instruction a score and block) and before those of the values,
+// into the weights: there each block of the head has a power of two of its own, or one block's large scales would push
+// another's weights to where the second part ends (blocks 2^-13 apart, most of the weight on a position whose values are
+// zero: 7 times the bound of the binary32 sums with one power for all, a hundredth of it so).
 //
 // Bounds.  Binary16: the cache's bytes (32 sequences of 8192 positions, 4 heads of 128: 98 us, 5.5 TB/s).  Block formats:
 // the vector instructions of a step, some 380 for 32 positions of q8_0 and 590 of iq4_nl at 128 wide, most of them to unpack
@@ -32,6 +35,7 @@ namespace qmm {
 typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
 typedef float float2_t __attribute__((ext_vector_type(2)));
 typedef float float4_t __attribute__((ext_vector_type(4)));
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kAtLds = 80 * 1024 - 512;  // bytes of LDS of a workgroup of which two share a CU
 constexpr int kAtStep = 32;      // positions a step
@@ -304,6 +308,23 @@ __device__ __forceinline__ void to_lds(char* lds, const char* base, uint32_t off
     }
 }
 
+// Orders LDS accesses of the lanes of a wave, which run in step.
+__device__ __forceinline__ void wave_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// Bits 15 and 31: whether each of two halves is not finite.  (Many of them are joined without a compare each.)
+__device__ __forceinline__ uint32_t odd_halves(uint32_t v) { return ((v & 0x7C007C00u) + 0x04000400u) & 0x80008000u; }
+
+// The least of the 16 lanes of a row, both halves apart.
+__device__ __forceinline__ u16x2 min16_pair(u16x2 v) {
+    v = __builtin_elementwise_min(v, __builtin_bit_cast(u16x2, dpp_i<0xB1>(__builtin_bit_cast(int, v))));
+    v = __builtin_elementwise_min(v, __builtin_bit_cast(u16x2, dpp_i<0x4E>(__builtin_bit_cast(int, v))));
+    v = __builtin_elementwise_min(v, __builtin_bit_cast(u16x2, dpp_i<0x141>(__builtin_bit_cast(int, v))));
+    return __builtin_elementwise_min(v, __builtin_bit_cast(u16x2, dpp_i<0x140>(__builtin_bit_cast(int, v))));
+}
+
 // 32 positions of a block format, as they lie in a page: the factors of both 16-position halves, then their scales,
 // copied by the wave itself 16 bytes a lane without passing registers, so that whole steps are on their way
 // while one is worked on.  A piece of 16 bytes keeps its row and goes, where a row is a power of two of them, to
@@ -381,17 +402,43 @@ struct Stage {
     __device__ static __forceinline__ void scales(uint32_t* d, const char* lds, int h, int g) {
         __builtin_memcpy(d, __builtin_assume_aligned(lds + kScales + (32 * h + 8 * g) * NB, 8), 8 * NB);
     }
-    // The binary16 bits of the largest magnitude among the scales of positions 4g .. 4g+3 that a lane's place n
-    // among 16 falls to.
-    __device__ static __forceinline__ int largest_part(const char* lds, int n, int g) {
-        uint32_t most = 0;
+    // Of the 4 NB dwords of scales of positions 4g .. 4g+3 of both halves the ones that a lane's place n among 16 falls to,
+    // and whether one holds a magnitude whose binary16 bits are more than `most`, one for each of the two blocks that it is of.
+    static constexpr int kParts = (4 * NB + 15) / 16;
+    __device__ static __forceinline__ int part(int n, int i) { return min(n + 16 * i, 4 * NB - 1); }
+    __device__ static __forceinline__ bool above(const char* lds, int n, int g, const u16x2 (&most)[kParts]) {
+        bool any = false;
 #pragma unroll
-        for (int i = 0; i < (4 * NB + 15) / 16; ++i) {
-            const int j = min(n + 16 * i, 4 * NB - 1);
+        for (int i = 0; i < kParts; ++i) {
+            const int j = part(n, i);
             const uint32_t v = *(const uint32_t*)(lds + kScales + (32 * (j / (2 * NB)) + 8 * g) * NB + 4 * (j % (2 * NB))) & 0x7FFF7FFFu;
-            most = max(most, max(v >> 16, v & 0xFFFFu));
+            const u16x2 larger = __builtin_elementwise_max(__builtin_bit_cast(u16x2, v), most[i]);
+            any |= __builtin_bit_cast(uint32_t, larger) != __builtin_bit_cast(uint32_t, most[i]);
         }
-        return (int)most;
+        return any;
+    }
+    // The step's scales without those that are not finite, by the whole wave.
+    __device__ static __forceinline__ void keep_finite(char* lds, int lane) {
+        uint32_t* w = (uint32_t*)(lds + kScales);
+        for (int i = lane; i < 16 * NB; i += 64) w[i] &= ~((odd_halves(w[i]) >> 15) * 0xFFFFu);
+        wave_fence();
+    }
+    // What is compared there: the least of the rows' (of the lanes n) values for blocks 2i and 2i + 1 in v[i].
+    __device__ static __forceinline__ void share(int n, u16x2 (&v)[(NB + 1) / 2], u16x2 (&most)[kParts]) {
+#pragma unroll
+        for (u16x2& w : v) w = min16_pair(w);
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) {
+            const int first = 2 * part(n, i) % NB;  // of the blocks
+            if constexpr (NB % 2 == 0) {
+                most[i] = v[0];
+#pragma unroll
+                for (int b = 1; b < NB / 2; ++b) most[i] = first == 2 * b ? v[b] : most[i];
+            } else {
+                static_assert(NB % 2 == 0 || NB == 3, "blocks (0, 1), (2, 0), (1, 2)");
+                most[i] = first == 0 ? v[0] : first == 2 ? u16x2{v[1].x, v[0].x} : u16x2{v[0].y, v[1].x};
+            }
+        }
     }
 };
 
@@ -496,8 +543,6 @@ struct Keys {
 };
 
 __device__ __forceinline__ bool not_finite(uint32_t half) { return (half & 0x7C00u) == 0x7C00u; }
-// Bits 15 and 31: whether each of two halves is not finite.  (Many of them are joined without a compare each.)
-__device__ __forceinline__ uint32_t odd_halves(uint32_t v) { return ((v & 0x7C007C00u) + 0x04000400u) & 0x80008000u; }
 
 // The values of 32 positions: lane (n, g) holds, of the positions 4g .. 4g+3 of both halves, the dims that
 // row n of the 2 NB operands V^T takes: tile (b, i) dim 32b + 16i + n (binary16: tile j dim 2 NB n + j).
@@ -520,52 +565,42 @@ struct Values {
         for (int h = 0; h < 2; ++h) {
 #pragma unroll
             for (int r = 0; r < 4; ++r) Stage<TYPE, NB>::template read<kBytes>(w[4 * h + r], lds, 16 * h + 4 * g + r, n * kBytes);
-            Stage<TYPE, NB>::scales(d[h], lds, h, g);
         }
+        read_scales(lane, lds);
+    }
+    __device__ __forceinline__ void read_scales(int lane, const char* lds) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) Stage<TYPE, NB>::scales(d[h], lds, h, lane >> 4);
     }
     __device__ __forceinline__ _Float16 scale(int x, int b) const {
         const int i = (x & 3) * NB + b;
         return __builtin_bit_cast(half2_t, d[x >> 2][i / 2])[i & 1];
     }
-    // The binary16 bits of the largest magnitude among the scales, of all positions or of those seen.
-    template <bool MASKED>
-    __device__ __forceinline__ int largest(int seen) const {
-        typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
-        u16x2 most = {0, 0};
+    // The binary16 bits of the largest magnitude among each block's scales at the positions seen, blocks 2i and 2i + 1 in
+    // most[i].
+    static constexpr int kPairs = (NB + 1) / 2;
+    __device__ __forceinline__ void largest(int seen, u16x2 (&most)[kPairs]) const {
+        constexpr int kTurn = NB % 2 ? NB : NB / 2;  // dwords until their two blocks are the same again
+        u16x2 of[kTurn];
+#pragma unroll
+        for (int i = 0; i < kTurn; ++i) of[i] = u16x2{0, 0};
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int i = 0; i < 2 * NB; ++i) {
-                uint32_t v = d[h][i] & 0x7FFF7FFFu;
-                if constexpr (MASKED) {
-                    const int x = 4 * h + 2 * i / NB, y = 4 * h + (2 * i + 1) / NB;
-                    const uint32_t a = (uint32_t)((int)((uint32_t)seen << (31 - x)) >> 31), b = (uint32_t)((int)((uint32_t)seen << (31 - y)) >> 31);
-                    v &= x == y ? a : (a & 0xFFFFu) | (b & 0xFFFF0000u);
-                }
-                most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2, v));
+                const int x = 4 * h + 2 * i / NB, y = 4 * h + (2 * i + 1) / NB;
+                const uint32_t a = (uint32_t)((int)((uint32_t)seen << (31 - x)) >> 31), b = (uint32_t)((int)((uint32_t)seen << (31 - y)) >> 31);
+                const uint32_t v = d[h][i] & 0x7FFF7FFFu & (x == y ? a : (a & 0xFFFFu) | (b & 0xFFFF0000u));
+                of[i % kTurn] = __builtin_elementwise_max(of[i % kTurn], __builtin_bit_cast(u16x2, v));
             }
-        return max((int)most.x, (int)most.y);
-    }
-    // Scales that are not finite: whether there are any, the blocks (bits) where a position seen has one, and without them.
-    __device__ __forceinline__ bool any_odd() const {
-        uint32_t odd = 0;
+        if constexpr (NB % 2 == 0) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int i = 0; i < 2 * NB; ++i) odd |= odd_halves(d[h][i]);
-        return odd != 0;
-    }
-    __device__ __forceinline__ int odd_blocks(int seen) const {
-        int blocks = 0;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int i = 0; i < 2 * NB; ++i) {
-                const uint32_t odd = odd_halves(d[h][i]);
-                blocks |= (int)(odd >> 15 & (uint32_t)seen >> (4 * h + 2 * i / NB) & 1) << (2 * i % NB);
-                blocks |= (int)(odd >> 31 & (uint32_t)seen >> (4 * h + (2 * i + 1) / NB) & 1) << ((2 * i + 1) % NB);
-            }
-        return blocks;
+            for (int i = 0; i < kPairs; ++i) most[i] = of[i];
+        } else {
+            static_assert(NB % 2 == 0 || NB == 3, "blocks (0, 1), (2, 0), (1, 2)");
+            most[0] = __builtin_elementwise_max(of[0], u16x2{of[1].y, of[2].x});
+            most[1] = u16x2{of[1].x > of[2].y ? of[1].x : of[2].y, 0};
+        }
     }
     // The scales as they are loaded, two a register, also past a branch that may change them.
     __device__ __forceinline__ void keep_words() {
@@ -573,15 +608,6 @@ struct Values {
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int i = 0; i < 2 * NB; ++i) asm("" : "+v"(d[h][i]));
-    }
-    __device__ __forceinline__ void drop_odd() {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int i = 0; i < 2 * NB; ++i) {
-                const uint32_t v = d[h][i];
-                d[h][i] = (not_finite(v) ? 0u : v & 0xFFFFu) | (not_finite(v >> 16) ? 0u : v & 0xFFFF0000u);
-            }
     }
     // Biased bytes; of iq4_nl the levels, where two half dwords of neighbouring positions share a lookup.
     struct Ready {
@@ -627,8 +653,10 @@ struct Values {
 struct Mix {
     float minus, zero;
     __device__ __forceinline__ Mix() : minus(-1.0f), zero(0.0f) { asm("" : "+s"(minus), "+s"(zero)); }
-    __device__ __forceinline__ float product(float x, _Float16 h) const { return __builtin_fmaf((float)h, x, zero); }
     __device__ __forceinline__ float rest(float x, _Float16 h) const { return __builtin_fmaf((float)h, minus, x); }
+    // A product with a factor h, rounded to binary16, and what that leaves, the same way (v_fma_mixlo_f16, v_fma_mixhi_f16).
+    __device__ __forceinline__ _Float16 high(float x, _Float16 h) const { return (_Float16)__builtin_fmaf((float)h, x, zero); }
+    __device__ __forceinline__ _Float16 low(float x, _Float16 h, _Float16 high) const { return (_Float16)__builtin_fmaf((float)h, x, -(float)high); }
 };
 
 // Two binary16 parts of pairs of values: the nearest, and the nearest of what is left.
@@ -637,6 +665,32 @@ __device__ __forceinline__ void two_parts(const Mix& mix, float x, float y, uint
     const float2_t rest = {mix.rest(x, h.x), mix.rest(y, h.y)};
     hi = __builtin_bit_cast(uint32_t, h);
     lo = __builtin_bit_cast(uint32_t, __builtin_convertvector(rest, half2_t));
+}
+
+// The same of eight values' products with factors, by v_fma_mixlo_f16 and v_fma_mixhi_f16: four instructions a pair, where
+// products and the parts above are six.  (The empty asm keeps the compiler from rounding the two of a pair together.  All
+// pairs at once: what takes the half that an instruction leaves waits for one more.)
+template <class F>
+__device__ __forceinline__ void scaled_parts(const Mix& mix, const float (&u)[8], F factor, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
+    _Float16 part[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        part[i] = mix.high(u[2 * i], factor(2 * i));
+        asm("" : "+v"(part[i]));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        hi[i] = __builtin_bit_cast(uint32_t, half2_t{part[i], mix.high(u[2 * i + 1], factor(2 * i + 1))});
+        asm("" : "+v"(hi[i]));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        part[i] = mix.low(u[2 * i], factor(2 * i), __builtin_bit_cast(half2_t, hi[i]).x);
+        asm("" : "+v"(part[i]));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        lo[i] = __builtin_bit_cast(uint32_t, half2_t{part[i], mix.low(u[2 * i + 1], factor(2 * i + 1), __builtin_bit_cast(half2_t, hi[i]).y)});
 }
 
 // Maximum and sum over the lanes n, n + 16, n + 32, n + 48.
@@ -657,10 +711,21 @@ __device__ __forceinline__ float rows_sum(float v) {
     return __builtin_bit_cast(float, (int)r[0]) + __builtin_bit_cast(float, (int)r[1]);
 }
 
-// Orders LDS accesses of the lanes of a wave, which run in step.
-__device__ __forceinline__ void wave_fence() {
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
+__device__ __forceinline__ u16x2 rows_max16(u16x2 v) {
+    const int x = __builtin_bit_cast(int, v);
+    auto r = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    v = __builtin_elementwise_max(__builtin_bit_cast(u16x2, (int)r[0]), __builtin_bit_cast(u16x2, (int)r[1]));
+    const int y = __builtin_bit_cast(int, v);
+    r = __builtin_amdgcn_permlane32_swap(y, y, false, false);
+    return __builtin_elementwise_max(__builtin_bit_cast(u16x2, (int)r[0]), __builtin_bit_cast(u16x2, (int)r[1]));
+}
+
+// A row's fold of a block of values, a power of two: its weights times the block's scales times the fold are what is cut into
+// binary16 parts.  The largest scale that the row has seen of the block has a product in [2^13, 2^15) with it.  2^e / fold:
+constexpr uint32_t kFoldMost = (127u + 38u) << 23;  // (the least scale is 2^-24)
+template <int E>
+__device__ __forceinline__ float over(uint32_t fold) {
+    return __builtin_bit_cast(float, ((127u + E + 127u) << 23) - fold);
 }
 
 __device__ __forceinline__ int rows_or(int v) {
@@ -888,24 +953,30 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
     int rlo[RT], rhi[RT];
     float c[RT];  // scores are c times the sums of the scaled operands
     float4_t o[RT][kTiles];
-    float m[RT], l[RT], limit[RT], fold[RT];
-    int bound[RT];  // the binary16 bits of limit, a power of two above the scales of values that the row has seen
+    float m[RT], l[RT];
+    // The folds of the blocks of values, the upper halves of two binary32 a dword; and for each of the lane's parts of a step's
+    // scales the binary16 bits up to which there is room under every row's.
+    constexpr int kPairs = Values<VT, NB>::kPairs;
+    uint32_t fold[RT][kPairs];
+    constexpr int kParts = (4 * NB + 15) / 16;
+    u16x2 room[kParts];
 #pragma unroll
     for (int x = 0; x < RT; ++x) {
         const int r = 16 * x + n;
-        const int pos = w.len - w.n + token_of(row0 + r);
+        const int pos = w.len - w.n + token_of(row0 + min(r, rows - 1));  // (a row that does not exist sees what the last one does)
         rlo[x] = low(pos);
-        rhi[x] = r < rows ? min(pos + 1, cap) : 0;
+        rhi[x] = min(pos + 1, cap);
         c[x] = lc[r];
         m[x] = -INFINITY;
         l[x] = 0.0f;
-        limit[x] = power(-24);
-        fold[x] = power(14 + 24);
-        bound[x] = 1;
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) fold[x][i] = 0x10001u * (kFoldMost >> 16);
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) o[x][t] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
     }
-    int least = 1;  // the least of the rows' bounds
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) room[i] = u16x2{0, 0};
+    const auto fold_bits = [&](int x, int b) { return b & 1 ? fold[x][b / 2] & 0xFFFF0000u : fold[x][b / 2] << 16; };
     const auto queries = [&](int x, int b, int part) { return __builtin_bit_cast(half8_t, *(const u32x4*)lq[x][b][part][lane]); };
 
     for (int k = 0; k < ksteps; ++k) {
@@ -981,7 +1052,7 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
         // Positions that some row of the tile does not see: their scores go, whatever they are.  (The empty asm keeps
         // this a branch that steps in the middle of a cache skip.)
         const bool masked = j0 < lo_max || j0 + kAtStep > hi_min || !exist[0] || !exist[1];
-        int seen[RT], most[RT];  // bit i of seen: position i of z
+        int seen[RT];  // bit i: position i of z
         if (masked) {
             asm volatile("");
 #pragma unroll
@@ -1038,55 +1109,65 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
             vals.read(there, ring + kDepth * S::kKeys + k % kDepth * S::kVals);
         }
         if constexpr (kValBlocks) {
-            bool above = false;
             vals.keep_words();
-            if (masked) {
+            char* const scales = ring + kDepth * S::kKeys + k % kDepth * S::kVals;
+            // Scales that some row's folds leave no room for, seen or not: seldom after the first step.
+            if (__any(Stage<VT, NB>::above(scales, there & 15, there >> 4, room))) {
                 asm volatile("");
-#pragma unroll
-                for (int x = 0; x < RT; ++x) most[x] = vals.template largest<true>(seen[x]);
-                // A scale that is not finite must not meet the weight 0 of a row that does not see it: it is left
-                // out, and makes its block NaN in the rows that do.
-                if (__any(vals.any_odd())) {
-#pragma unroll
-                    for (int x = 0; x < RT; ++x) {
-                        const int blocks = rows_or(vals.odd_blocks(seen[x]));
-#pragma unroll
-                        for (int t = 0; t < kTiles; ++t)
-                            if (blocks >> (t / 2) & 1) o[x][t] = float4_t{NAN, NAN, NAN, NAN};
-                    }
-                    vals.drop_odd();
-                }
-#pragma unroll
-                for (int x = 0; x < RT; ++x) above |= most[x] >= bound[x];
-            } else {
-                // (the sixteen lanes with the same scales share them)
-                above = Stage<VT, NB>::largest_part(ring + kDepth * S::kKeys + k % kDepth * S::kVals, there & 15, there >> 4) >= least;
-            }
-            vals.keep_words();
-            if (__any(above)) {
-                int now = 0x10000;
                 if (!masked) {
 #pragma unroll
-                    for (int x = 0; x < RT; ++x) most[x] = x ? most[0] : vals.template largest<false>(0);
+                    for (int x = 0; x < RT; ++x) seen[x] = 0xFF;
                 }
+                // A scale that is not finite must not meet the weight 0 of a row that does not see it: it is left
+                // out, and makes its block NaN in the rows that do.
+                u16x2 finite[kParts];
+                int odd[RT] = {};
+#pragma unroll
+                for (int i = 0; i < kParts; ++i) finite[i] = u16x2{0x7BFF, 0x7BFF};
+                if (__any(Stage<VT, NB>::above(scales, there & 15, there >> 4, finite))) {
+#pragma unroll
+                    for (int x = 0; x < RT; ++x) {
+                        u16x2 most[kPairs];
+                        vals.largest(seen[x], most);
+#pragma unroll
+                        for (int i = 0; i < kPairs; ++i) most[i] = rows_max16(most[i]);
+#pragma unroll
+                        for (int b = 0; b < NB; ++b) odd[x] |= most[b / 2][b % 2] >= 0x7C00 ? 1 << b : 0;
+                    }
+                    Stage<VT, NB>::keep_finite(scales, there);
+                    vals.read_scales(there, scales);
+                }
+                u16x2 least[kPairs];
+#pragma unroll
+                for (int i = 0; i < kPairs; ++i) least[i] = u16x2{0x7BFF, 0x7BFF};
 #pragma unroll
                 for (int x = 0; x < RT; ++x) {
-                    const float d = rows_max(__builtin_fabsf(h2f(min(most[x], 0x7C00))));  // (an infinity, NaN: 2^17)
-                    const int e = max(min((int)(__builtin_bit_cast(uint32_t, d) >> 23) - 126, 17), -24);
-                    const float to = __builtin_fmaxf(limit[x], power(e)), shrink = limit[x] * (1.0f / to);
-                    limit[x] = to;
-                    fold[x] = 16384.0f / to;
-                    bound[x] = to > 65536.0f ? 0x10000 : (int)f2h(to);
+                    u16x2 most[kPairs];
+                    vals.largest(seen[x], most);
 #pragma unroll
-                    for (int t = 0; t < kTiles; ++t) o[x][t] *= shrink;
-                    now = min(now, bound[x]);
+                    for (int i = 0; i < kPairs; ++i) {
+                        const u16x2 d = rows_max16(most[i]);
+                        uint32_t now[2];
+                        float up[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            // (a zero's is beyond kFoldMost)
+                            const uint32_t scale = __builtin_bit_cast(uint32_t, h2f(d[e]));
+                            now[e] = min(((127u + 13u + 127u) << 23) - (scale & 0x7F800000u), fold_bits(x, 2 * i + e));
+                            up[e] = odd[x] >> (2 * i + e) & 1 ? NAN : __builtin_bit_cast(float, now[e] - fold_bits(x, 2 * i + e) + (127u << 23));
+                            if (2 * i + e < NB) {
+                                o[x][2 * (2 * i + e)] *= up[e];
+                                o[x][2 * (2 * i + e) + 1] *= up[e];
+                            }
+                        }
+                        fold[x][i] = now[0] >> 16 | now[1];
+                        const u16x2 limit = __builtin_bit_cast(u16x2, __builtin_convertvector((float2_t{over<15>(now[0]), over<15>(now[1])}), half2_t));
+                        least[i] = __builtin_elementwise_min(least[i], limit - u16x2{1, 1});
+                    }
                 }
-                now = min(now, dpp_i<0xB1>(now));
-                now = min(now, dpp_i<0x4E>(now));
-                now = min(now, dpp_i<0x141>(now));
-                now = min(now, dpp_i<0x140>(now));
-                least = __builtin_amdgcn_readfirstlane(now);
+                Stage<VT, NB>::share(there & 15, least, room);
             }
+            vals.keep_words();
         } else if (masked) {
             asm volatile("");
             // Places that no row sees count as zeros.  Infinities and NaN that some rows see and others do not
@@ -1140,12 +1221,6 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
                     }
             }
         }
-        if constexpr (kValBlocks) {
-#pragma unroll
-            for (int x = 0; x < RT; ++x)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) z[x][i] *= fold[x];
-        }
         // The sums of values.
         typename Values<VT, NB>::Ready ready;
         vals.ready(ready);
@@ -1157,15 +1232,15 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
 #pragma unroll
                 for (int x = 0; x < RT; ++x) {
                     uint32_t hi[4], lo[4];
+                    if constexpr (kValBlocks) {
+                        const float f = __builtin_bit_cast(float, fold_bits(x, t / 2));
+                        float u[8];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float u[2];
+                        for (int i = 0; i < 8; ++i) u[i] = z[x][i] * f;
+                        scaled_parts(mix, u, [&](int i) { return vals.scale(i, t / 2); }, hi, lo);
+                    } else {
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            u[e] = z[x][2 * i + e];
-                            if constexpr (kValBlocks) u[e] = mix.product(u[e], vals.scale(2 * i + e, t / 2));
-                        }
-                        two_parts(mix, u[0], u[1], hi[i], lo[i]);
+                        for (int i = 0; i < 4; ++i) two_parts(mix, z[x][2 * i], z[x][2 * i + 1], hi[i], lo[i]);
                     }
                     ph[x] = as_half8(hi[0], hi[1], hi[2], hi[3]);
                     pl[x] = as_half8(lo[0], lo[1], lo[2], lo[3]);
@@ -1196,9 +1271,8 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
     for (int x = 0; x < RT; ++x) {
         l[x] = rows_sum(l[x]) * (kValBlocks ? 1.0f : power(-14));
         m[x] *= c[x];
-        const float back = kValBlocks ? limit[x] * power(10 - 14) : power(-14);
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t) o[x][t] *= back;
+        for (int t = 0; t < kTiles; ++t) o[x][t] *= kValBlocks ? over<10>(fold_bits(x, t / 2)) : power(-14);
     }
     __syncthreads();
 #pragma unroll
