@@ -316,6 +316,8 @@ __device__ __forceinline__ void wave_fence() {
 
 // Bits 15 and 31: whether each of two halves is not finite.  (Many of them are joined without a compare each.)
 __device__ __forceinline__ uint32_t odd_halves(uint32_t v) { return ((v & 0x7C007C00u) + 0x04000400u) & 0x80008000u; }
+// The halves that are finite, zeros for the others.
+__device__ __forceinline__ uint32_t finite_halves(uint32_t v) { return v & ~((odd_halves(v) >> 15) * 0xFFFFu); }
 
 // The least of the 16 lanes of a row, both halves apart.
 __device__ __forceinline__ u16x2 min16_pair(u16x2 v) {
@@ -420,7 +422,7 @@ struct Stage {
     // The step's scales without those that are not finite, by the whole wave.
     __device__ static __forceinline__ void keep_finite(char* lds, int lane) {
         uint32_t* w = (uint32_t*)(lds + kScales);
-        for (int i = lane; i < 16 * NB; i += 64) w[i] &= ~((odd_halves(w[i]) >> 15) * 0xFFFFu);
+        for (int i = lane; i < 16 * NB; i += 64) w[i] = finite_halves(w[i]);
         wave_fence();
     }
     // What is compared there: the least of the rows' (of the lanes n) values for blocks 2i and 2i + 1 in v[i].
@@ -1032,10 +1034,40 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
                 }
             }
             if constexpr (!kKeyBlocks) {
+                bool odd = false;
 #pragma unroll
                 for (int x = 0; x < RT; ++x)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) z[x][i] = s[x][i / 4][i & 3] + t[x][i / 4][i & 3];
+                    for (int i = 0; i < 8; ++i) {
+                        z[x][i] = s[x][i / 4][i & 3] + t[x][i / 4][i & 3];
+                        if (i & 1) odd |= __builtin_isunordered(z[x][i - 1], z[x][i]);
+                    }
+                // A key's infinity times the second part of a query's value, zero or of the other sign, would make NaN of the
+                // infinity that the first part gives: there the second parts meet the finite values alone.  (The keys are read
+                // again, so that they need no registers here where they are finite.)
+                if (__any(odd)) {
+                    fetch_keys(k);
+                    keys[0].ready(ready[0]);
+                    keys[1].ready(ready[1]);
+#pragma unroll
+                    for (int x = 0; x < RT; ++x)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            float4_t u = {0.0f, 0.0f, 0.0f, 0.0f}, v = u;
+#pragma unroll
+                            for (int b = 0; b < NB; ++b) {
+                                const half8_t kb = Keys<KT, NB>::block(ready[h], b);
+                                u32x4 f = __builtin_bit_cast(u32x4, kb);
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) f[e] = finite_halves(f[e]);
+                                u = __builtin_amdgcn_mfma_f32_16x16x32_f16(kb, queries(x, b, 0), u, 0, 0, 0);
+                                v = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, f), queries(x, b, 1), v, 0, 0, 0);
+                                __builtin_amdgcn_sched_barrier(0);
+                            }
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) z[x][4 * h + r] = u[r] + v[r];
+                        }
+                }
             }
         }
         __builtin_amdgcn_sched_barrier(0);
