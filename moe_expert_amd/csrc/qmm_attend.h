@@ -546,6 +546,15 @@ struct Keys {
 
 __device__ __forceinline__ bool not_finite(uint32_t half) { return (half & 0x7C00u) == 0x7C00u; }
 
+__device__ __forceinline__ u16x2 rows_max16(u16x2 v) {
+    const int x = __builtin_bit_cast(int, v);
+    auto r = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    v = __builtin_elementwise_max(__builtin_bit_cast(u16x2, (int)r[0]), __builtin_bit_cast(u16x2, (int)r[1]));
+    const int y = __builtin_bit_cast(int, v);
+    r = __builtin_amdgcn_permlane32_swap(y, y, false, false);
+    return __builtin_elementwise_max(__builtin_bit_cast(u16x2, (int)r[0]), __builtin_bit_cast(u16x2, (int)r[1]));
+}
+
 // The values of 32 positions: lane (n, g) holds, of the positions 4g .. 4g+3 of both halves, the dims that
 // row n of the 2 NB operands V^T takes: tile (b, i) dim 32b + 16i + n (binary16: tile j dim 2 NB n + j).
 template <int TYPE, int NB>
@@ -578,9 +587,10 @@ struct Values {
         const int i = (x & 3) * NB + b;
         return __builtin_bit_cast(half2_t, d[x >> 2][i / 2])[i & 1];
     }
-    // The binary16 bits of the largest magnitude among each block's scales at the positions seen, blocks 2i and 2i + 1 in
-    // most[i].
+    // The binary16 bits of the largest magnitude among each block's scales, of all positions or of those seen, blocks 2i and
+    // 2i + 1 in most[i]; by all lanes of a row.
     static constexpr int kPairs = (NB + 1) / 2;
+    template <bool MASKED>
     __device__ __forceinline__ void largest(int seen, u16x2 (&most)[kPairs]) const {
         constexpr int kTurn = NB % 2 ? NB : NB / 2;  // dwords until their two blocks are the same again
         u16x2 of[kTurn];
@@ -590,9 +600,12 @@ struct Values {
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int i = 0; i < 2 * NB; ++i) {
-                const int x = 4 * h + 2 * i / NB, y = 4 * h + (2 * i + 1) / NB;
-                const uint32_t a = (uint32_t)((int)((uint32_t)seen << (31 - x)) >> 31), b = (uint32_t)((int)((uint32_t)seen << (31 - y)) >> 31);
-                const uint32_t v = d[h][i] & 0x7FFF7FFFu & (x == y ? a : (a & 0xFFFFu) | (b & 0xFFFF0000u));
+                uint32_t v = d[h][i] & 0x7FFF7FFFu;
+                if constexpr (MASKED) {
+                    const int x = 4 * h + 2 * i / NB, y = 4 * h + (2 * i + 1) / NB;
+                    const uint32_t a = (uint32_t)((int)((uint32_t)seen << (31 - x)) >> 31), b = (uint32_t)((int)((uint32_t)seen << (31 - y)) >> 31);
+                    v &= x == y ? a : (a & 0xFFFFu) | (b & 0xFFFF0000u);
+                }
                 of[i % kTurn] = __builtin_elementwise_max(of[i % kTurn], __builtin_bit_cast(u16x2, v));
             }
         if constexpr (NB % 2 == 0) {
@@ -603,6 +616,8 @@ struct Values {
             most[0] = __builtin_elementwise_max(of[0], u16x2{of[1].y, of[2].x});
             most[1] = u16x2{of[1].x > of[2].y ? of[1].x : of[2].y, 0};
         }
+#pragma unroll
+        for (u16x2& v : most) v = rows_max16(v);
     }
     // The scales as they are loaded, two a register, also past a branch that may change them.
     __device__ __forceinline__ void keep_words() {
@@ -711,15 +726,6 @@ __device__ __forceinline__ float rows_sum(float v) {
     const int y = __builtin_bit_cast(int, v);
     r = __builtin_amdgcn_permlane32_swap(y, y, false, false);
     return __builtin_bit_cast(float, (int)r[0]) + __builtin_bit_cast(float, (int)r[1]);
-}
-
-__device__ __forceinline__ u16x2 rows_max16(u16x2 v) {
-    const int x = __builtin_bit_cast(int, v);
-    auto r = __builtin_amdgcn_permlane16_swap(x, x, false, false);
-    v = __builtin_elementwise_max(__builtin_bit_cast(u16x2, (int)r[0]), __builtin_bit_cast(u16x2, (int)r[1]));
-    const int y = __builtin_bit_cast(int, v);
-    r = __builtin_amdgcn_permlane32_swap(y, y, false, false);
-    return __builtin_elementwise_max(__builtin_bit_cast(u16x2, (int)r[0]), __builtin_bit_cast(u16x2, (int)r[1]));
 }
 
 // A row's fold of a block of values, a power of two: its weights times the block's scales times the fold are what is cut into
@@ -1146,10 +1152,21 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
             // Scales that some row's folds leave no room for, seen or not: seldom after the first step.
             if (__any(Stage<VT, NB>::above(scales, there & 15, there >> 4, room))) {
                 asm volatile("");
-                if (!masked) {
+                vals.keep_words();  // (read again at the end: the registers go to the sums)
+                const auto largest = [&](u16x2(&most)[RT][kPairs]) {
 #pragma unroll
-                    for (int x = 0; x < RT; ++x) seen[x] = 0xFF;
-                }
+                    for (int x = 0; x < RT; ++x) {
+                        if (masked) {
+                            vals.template largest<true>(seen[x], most[x]);
+                        } else if (x == 0) {
+                            vals.template largest<false>(0, most[0]);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < kPairs; ++i) most[x][i] = most[0][i];
+                        }
+                    }
+                };
+                u16x2 most[RT][kPairs];
                 // A scale that is not finite must not meet the weight 0 of a row that does not see it: it is left
                 // out, and makes its block NaN in the rows that do.
                 u16x2 finite[kParts];
@@ -1157,28 +1174,23 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
 #pragma unroll
                 for (int i = 0; i < kParts; ++i) finite[i] = u16x2{0x7BFF, 0x7BFF};
                 if (__any(Stage<VT, NB>::above(scales, there & 15, there >> 4, finite))) {
+                    largest(most);
 #pragma unroll
-                    for (int x = 0; x < RT; ++x) {
-                        u16x2 most[kPairs];
-                        vals.largest(seen[x], most);
+                    for (int x = 0; x < RT; ++x)
 #pragma unroll
-                        for (int i = 0; i < kPairs; ++i) most[i] = rows_max16(most[i]);
-#pragma unroll
-                        for (int b = 0; b < NB; ++b) odd[x] |= most[b / 2][b % 2] >= 0x7C00 ? 1 << b : 0;
-                    }
+                        for (int b = 0; b < NB; ++b) odd[x] |= most[x][b / 2][b % 2] >= 0x7C00 ? 1 << b : 0;
                     Stage<VT, NB>::keep_finite(scales, there);
                     vals.read_scales(there, scales);
                 }
+                largest(most);
                 u16x2 least[kPairs];
 #pragma unroll
                 for (int i = 0; i < kPairs; ++i) least[i] = u16x2{0x7BFF, 0x7BFF};
 #pragma unroll
                 for (int x = 0; x < RT; ++x) {
-                    u16x2 most[kPairs];
-                    vals.largest(seen[x], most);
 #pragma unroll
                     for (int i = 0; i < kPairs; ++i) {
-                        const u16x2 d = rows_max16(most[i]);
+                        const u16x2 d = most[x][i];
                         uint32_t now[2];
                         float up[2];
 #pragma unroll
@@ -1198,6 +1210,9 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
                     }
                 }
                 Stage<VT, NB>::share(there & 15, least, room);
+                asm volatile("" ::: "memory");
+                vals.read_scales(there, scales);
+                vals.keep_words();
             }
             vals.keep_words();
         } else if (masked) {
