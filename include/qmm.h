@@ -499,8 +499,10 @@ size_t qmm_kv_attend_workspace(const qmm_kv_cache* cache, int64_t ntok, int nhea
  * with binary32 scores, statistics and sums; query values and weights are kept to 2^-22 of themselves, or to 2^-38 of
  * the row's largest (query value; weight, times the largest scale seen of the block where values are blocks).  No j
  * (a token before position 0, an empty sequence, missing pages): out 0, lse -inf.  Positions a token does not see have no
- * effect on it, whatever they hold.  A row of q that is not finite gives NaN in its own outputs.  Blocks of values seen
- * with a scale that is not finite give NaN in their own dims.  Meant for up to some tens of tokens a sequence (any
+ * effect on it, whatever they hold.  A row of q that is not finite gives NaN in its own outputs.  Infinities and NaN that it
+ * sees in a binary16 cache count as the formulas say: a score of -inf has the weight 0, an infinite value gives its
+ * infinity, or NaN beside the opposite one or at a weight of 0.  A block whose scale is not finite adds scale * (the sum of
+ * its integers' products) to a score, and makes its own dims of the values NaN.  Meant for up to some tens of tokens a sequence (any
  * count is right: each 16 or 32 rows of queries read the cache once).
  *   q    : qtype [ntok][ldq], rows of nheads * head_dim values.   nheads : a multiple of cache->nheads, at
  *          most 1024.   scale : finite.   window : >= 0.

@@ -619,6 +619,16 @@ struct Values {
 #pragma unroll
         for (u16x2& v : most) v = rows_max16(v);
     }
+    // Whether a binary16 value is not finite: its product with zero is a NaN then, one instruction a dword.
+    __device__ __forceinline__ bool any_odd() const {
+        const half2_t zero = {0, 0};
+        half2_t sum[2] = {zero, zero};
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) sum[x & 1] = __builtin_elementwise_fma(__builtin_bit_cast(half2_t, w[x][i]), zero, sum[x & 1]);
+        return odd_halves(__builtin_bit_cast(uint32_t, sum[0] + sum[1])) != 0;
+    }
     // The scales as they are loaded, two a register, also past a branch that may change them.
     __device__ __forceinline__ void keep_words() {
 #pragma unroll
@@ -1215,22 +1225,25 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
                 vals.keep_words();
             }
             vals.keep_words();
-        } else if (masked) {
-            asm volatile("");
-            // Places that no row sees count as zeros.  Infinities and NaN that some rows see and others do not
-            // must not meet the others' zeros in the products: they are added one position at a time, and left out there.
-            uint32_t odd = 0;
+        } else {
+            // Places that no row sees count as zeros.  Infinities and NaN must not meet the zeros of rows that do not see
+            // them in the products, nor a weight's second part, zero or of the other sign: they are added one position at a
+            // time, and left out there.
+            if (masked) {
+                asm volatile("");
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int j = j0 + 16 * (i >> 2) + 4 * g + (i & 3);
-                const bool some = exist[i >> 2] && j >= lo_min && j < hi_max;
+                for (int i = 0; i < 8; ++i) {
+                    const int j = j0 + 16 * (i >> 2) + 4 * g + (i & 3);
+                    const bool some = exist[i >> 2] && j >= lo_min && j < hi_max;
 #pragma unroll
-                for (int e = 0; e < Values<VT, NB>::kWords; ++e) {
-                    vals.w[i][e] = some ? vals.w[i][e] : 0u;
-                    odd |= odd_halves(vals.w[i][e]);
+                    for (int e = 0; e < Values<VT, NB>::kWords; ++e) vals.w[i][e] = some ? vals.w[i][e] : 0u;
                 }
             }
-            if (__any(odd != 0)) {
+            if (__any(vals.any_odd())) {
+                if (!masked) {
+#pragma unroll
+                    for (int x = 0; x < RT; ++x) seen[x] = 0xFF;
+                }
                 float* weight = (float*)(lds + S::kQueries + wave * S::kOdd);
                 uint32_t* row = (uint32_t*)(weight + kRows * kAtStep);
 #pragma unroll
@@ -1262,10 +1275,7 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
 #pragma unroll
-                    for (int e = 0; e < Values<VT, NB>::kWords; ++e) {
-                        const uint32_t v = vals.w[i][e];
-                        vals.w[i][e] = (not_finite(v) ? 0u : v & 0xFFFFu) | (not_finite(v >> 16) ? 0u : v & 0xFFFF0000u);
-                    }
+                    for (int e = 0; e < Values<VT, NB>::kWords; ++e) vals.w[i][e] = finite_halves(vals.w[i][e]);
             }
         }
         // The sums of values.

@@ -70,6 +70,35 @@ def test_keys_of_both_infinities():
                 assert not (s == -np.inf).any() and np.isnan(got).all() and np.isnan(lse).all()
 
 
+@pytest.mark.parametrize("dim,heads,kv", [(64, 40, 2), (96, 5, 1), (128, 10, 2), (192, 3, 1), (256, 2, 2)])
+def test_infinite_values(dim, heads, kv):
+    """An infinite value gives its infinity to the rows that see it, two opposite ones and NaN give NaN, wherever they
+    lie; other dims keep every bit."""
+    n = 260
+    for where in (0, 3, 100, 131, n - 1):
+        for first, second, want in ((np.inf, None, np.inf), (-np.inf, None, -np.inf), (np.inf, np.inf, np.inf), (np.inf, -np.inf, np.nan),
+                                    (np.nan, None, np.nan), (-np.inf, np.nan, np.nan)):
+            print(f"infinite value {dim} {heads} {where} {first} {second}", flush=True)
+            c = Case([n, 20], new=[2, 1], kinds=("f16", "f16"), heads=heads, kv=kv, dim=dim, page=16, seed=where)
+            clean, lse = (host(t) for t in c.run())
+            put = [(where, first)] + ([] if second is None else [((where + 37) % (n - 1), second)])
+            for j, value in put:
+                c.raw[1][c.pages[0, j // 16], :, j % 16, 9] = value
+            got, lse2 = (host(t) for t in c.run())
+            assert np.array_equal(lse, lse2)
+            got, clean = got.reshape(3, heads, dim), clean.reshape(3, heads, dim)
+            other = np.arange(dim) != 9
+            assert np.array_equal(got[:, :, other], clean[:, :, other]) and np.array_equal(got[2], clean[2])
+            for t in range(2):
+                seen = [value for j, value in put if j <= n - 2 + t]
+                if len(seen) == len(put):
+                    assert np.array_equal(got[t, :, 9], np.full(heads, want), equal_nan=True)
+                elif not seen:
+                    assert np.array_equal(got[t], clean[t])
+                else:
+                    assert np.array_equal(got[t, :, 9], np.full(heads, seen[0]), equal_nan=True)
+
+
 @pytest.mark.parametrize("window", [0, 50])
 def test_written_infinities(window):
     """Values beyond binary16 that a write makes infinities of, keys and values of one position, a long sequence."""
