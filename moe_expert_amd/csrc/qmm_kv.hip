@@ -238,7 +238,13 @@ struct KvRead {
     uint32_t f[NB] = {}, scales[(NB + 1) / 2] = {};
     __device__ __forceinline__ void load(const KvRows& a, int which, const KvRow& row, const KvSpot& spot) {
         const int type = a.side[which].type, n = row.n;
-        if (spot.page < 0) return;
+        if (spot.page < 0) {
+            // +0 of every format: a scale of zero times the level 1, where index 0 is -127
+            if (type == kKvIq4)
+#pragma unroll
+                for (int i = 0; i < NB; ++i) f[i] = 0x88888888u;
+            return;
+        }
         const char* chunk = kv_chunk(a.side[which], a.p, spot.page, row.h);
         if (type == kKvF16) {
             __builtin_memcpy(f, __builtin_assume_aligned(chunk + spot.place * (64 * NB) + 4 * NB * n, 4), 4 * NB);
