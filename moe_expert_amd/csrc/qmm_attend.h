@@ -164,11 +164,13 @@ __device__ __forceinline__ int tile_units(const AttendArgs& a, int steps, const 
 }
 
 // units, tiles, tokens: of all sequences (line_units() of each tile); lengths(len): how many whole lengths all tiles
-// take.  Offsets that decrease give more tokens than there are: nothing is done then.
+// take.  Offsets that decrease give more tokens than there are, of which units and tiles may not hold the count: nothing is
+// done then.
 template <class F>
 __device__ __forceinline__ Split line_split(const AttendArgs& a, int units, int tiles, int64_t tokens, F lengths) {
+    if (tokens > a.p.ntok) return Split{2, 1, 0, 0, false};
     if (!a.pieces && !a.plan)  // a workgroup a tile
-        return Split{2 * kAtShort, kAtShort, tokens > a.p.ntok ? 0 : tiles * kAtShort, kAtShort, false};
+        return Split{2 * kAtShort, kAtShort, tiles * kAtShort, kAtShort, false};
     Split s;
     const int target = a.target, step = max(kAtWaves >> a.shift, 1);
     const auto rounded = [&](int len) { return max((len + step - 1) & -step, step); };  // as many steps for every wave
@@ -205,7 +207,7 @@ __device__ __forceinline__ Split line_split(const AttendArgs& a, int units, int 
     }
     s.pair = 2 * len;
     s.first = s.paired ? len + ((len * kAtMore / 16 + step - 1) & -step) : len;
-    s.all = tokens > a.p.ntok ? 0 : whole ? count * s.whole : units;
+    s.all = whole ? count * s.whole : units;
     return s;
 }
 
