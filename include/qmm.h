@@ -502,8 +502,8 @@ size_t qmm_kv_attend_workspace(const qmm_kv_cache* cache, int64_t ntok, int nhea
  * effect on it, whatever they hold.  A row of q that is not finite gives NaN in its own outputs.  Infinities and NaN that it
  * sees in a binary16 cache count as the formulas say: a score of -inf has the weight 0, an infinite value gives its
  * infinity, or NaN beside the opposite one or at a weight of 0.  A block whose scale is not finite adds scale * (the sum of
- * its integers' products) to a score, and makes its own dims of the values NaN.  Meant for up to some tens of tokens a sequence (any
- * count is right: each 16 or 32 rows of queries read the cache once).
+ * its integers' products) to a score, and makes its own dims of the values NaN.  Nothing but scores of -inf: as no j.  Meant
+ * for up to some tens of tokens a sequence (any count is right: each 16 or 32 rows of queries read the cache once).
  *   q    : qtype [ntok][ldq], rows of nheads * head_dim values.   nheads : a multiple of cache->nheads, at
  *          most 1024.   scale : finite.   window : >= 0.
  *   out  : otype [ntok][ldo], must not overlap q.   lse : float [ntok][nheads] or NULL.

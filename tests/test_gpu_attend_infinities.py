@@ -124,3 +124,16 @@ def test_written_infinities(window):
     assert np.isnan(got[:, 6]).all()
     assert (np.abs(got - o)[:, other] <= (bound + np.abs(o) * R.U)[:, other]).all()
     assert (np.abs(lse2 - l) <= lbound).all()
+
+
+def test_nothing_but_infinities():
+    """Every score of a row -inf: as a row that sees no position."""
+    for n in (1, 70, 300):
+        c = Case([n], kinds=("f16", "f16"), heads=2, kv=1, dim=64, page=16)
+        q = host(c.q)
+        q[0, 5], q[0, 64 + 5] = 1.0, -1.0
+        c.q = dev(q)
+        c.raw[0][:, :, :, 5] = -np.inf
+        got, lse = (host(t) for t in c.run())
+        assert (got[0, :64] == 0).all() and np.isneginf(lse[0, 0])
+        assert np.isnan(got[0, 64:]).all() and np.isnan(lse[0, 1])

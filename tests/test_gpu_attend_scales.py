@@ -150,3 +150,28 @@ def test_scales_that_a_row_does_not_see(kinds):
             assert torch.equal(got[:3], clean[:3]) and torch.equal(lse, lse2)
             other = got[3].view(6, 4, 32)[:, [0, 2, 3]]
             assert torch.isfinite(other).all() and torch.equal(other, clean[3].view(6, 4, 32)[:, [0, 2, 3]])
+
+
+@pytest.mark.parametrize("odd", [np.inf, -np.inf, np.nan])
+@pytest.mark.parametrize("kinds", [("q8_0", "q8_0"), ("q8_0", "iq4_nl"), ("iq4_nl", "iq4_nl")])
+def test_key_scale_that_is_not_finite(kinds, odd):
+    """It counts times the sum of its block's products: a score of -inf, without weight, or a row of NaN."""
+    for n, where in ((40, 39), (300, 0), (300, 140)):
+        c = Case([n], kinds=kinds, heads=8, kv=1, dim=96, page=16, seed=where)
+        q = host(c.q).reshape(8, 96).astype(np.float64)
+        pg, at = c.pages[0, where // 16], where % 16
+        s = scales_of(c, 0)
+        sums = q[:, 32:64] @ (c.val[0][pg, 0, at, 32:64] / float(s[pg, 0, at, 1]))
+        assert (np.abs(sums) > 1).all()
+        s[pg, 0, at, 1] = odd
+        got, lse = (host(t) for t in c.run())
+        got = got.reshape(8, 96)
+        gone = sums * odd < 0
+        assert np.isnan(got[~gone]).all() and np.isnan(lse[0, ~gone]).all()
+        key = c.val[0][pg, 0, at]
+        for h in np.flatnonzero(gone):
+            key[:] = -120.0 / c.scale * q[h] / np.square(q[h]).sum()
+            o, l, bound, lbound, _ = c.want()
+            rows = slice(96 * h, 96 * h + 96)
+            assert (np.abs(got[h] - o[0, rows]) <= (bound + np.abs(o) * R.U)[0, rows]).all()
+            assert abs(lse[0, h] - l[0, h]) <= lbound[0, h]
