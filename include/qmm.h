@@ -506,7 +506,7 @@ size_t qmm_kv_attend_workspace(const qmm_kv_cache* cache, int64_t ntok, int nhea
  * for up to some tens of tokens a sequence (any count is right: each 16 or 32 rows of queries read the cache once).
  *   q    : qtype [ntok][ldq], rows of nheads * head_dim values.   nheads : a multiple of cache->nheads, at
  *          most 1024.   scale : finite.   window : >= 0.
- *   out  : otype [ntok][ldo], must not overlap q.   lse : float [ntok][nheads] or NULL.
+ *   out  : otype [ntok][ldo], must not overlap q (out == q is refused).   lse : float [ntok][nheads] or NULL.
  *   cache->vtype holds at most as many bits as cache->ktype (an error of a key enters the exponent).
  *   ws   : qmm_kv_attend_workspace() bytes, 16-byte aligned; nothing in it is kept between calls, and
  *          calls that may overlap in time need one each.

@@ -1022,6 +1022,8 @@ def qmm_kv_attend(q, cache, pages, lens, seg_off=None, scale=None, window=0, out
         raise ValueError(f"q must have a multiple of {cache.width} columns")
     nseq, maxp, ldp = _kv_sequences(cache, pages, lens, seg_off, ntok)
     qt, ldq = _rows(q, "q", shape, dev)
+    if out is q:
+        raise ValueError("out must not be q")
     if out is None or isinstance(out, torch.dtype):
         if out is not None and out not in (_TYPE_OF or _types()):
             raise ValueError(f"out: {out} is not a type that this call writes")

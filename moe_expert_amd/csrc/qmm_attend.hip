@@ -178,6 +178,7 @@ extern "C" int qmm_kv_attend(const qmm_kv_cache* c, const int32_t* pages, int64_
     if (!q || !out || !ws) return QMM_EINVAL;
     if (!aligned(q, type_bytes(qtype)) || !aligned(out, type_bytes(otype)) || !aligned(lse, 4) || !aligned(ws, 16)) return QMM_EALIGN;
     if (ws_bytes < s.bytes) return QMM_ESPACE;
+    if (out == q) return QMM_EINVAL;
     const auto fours = [](const void* p, int64_t ld, int type) { return aligned(p, 4 * type_bytes(type)) && ld % 4 == 0; };
     AttendArgs a;
     a.q = q;
