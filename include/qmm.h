@@ -454,7 +454,8 @@ int qmm_lora(int xtype, const void* x, int64_t ldx, int64_t ntok, int64_t k, con
  * t the position lens[s] - (seg_off[s+1] - t).  What the host cannot check is bounded on the device: offsets
  * are clamped to [0, ntok] and have to be non-decreasing, a position below 0, past max_pages or
  * on a page outside [0, npages) does not exist, and tokens of no sequence are left alone.
- *   pages : int32 [nseq][ldpages], ldpages >= max_pages; entries past a sequence's pages are not read.
+ *   pages : int32 [nseq][ldpages], ldpages >= max_pages; entries past a sequence's pages may hold anything (they, and what
+ *           is on a page that they name, may be read, and have no effect).
  *   lens : int32 [nseq].   seg_off : int32 [nseq + 1] or NULL.   (4-byte aligned.)
  *   ntok at most 2^20, ntok * nheads at most 2^27, nseq at most 2^14, max_pages * page_size at most 2^30. */
 typedef struct {
@@ -507,10 +508,12 @@ size_t qmm_kv_attend_workspace(const qmm_kv_cache* cache, int64_t ntok, int nhea
  *   q    : qtype [ntok][ldq], rows of nheads * head_dim values.   nheads : a multiple of cache->nheads, at
  *          most 1024.   scale : finite.   window : >= 0.
  *   out  : otype [ntok][ldo], must not overlap q (out == q is refused).   lse : float [ntok][nheads] or NULL.
- *   cache->vtype holds at most as many bits as cache->ktype (an error of a key enters the exponent).
+ *   cache->vtype holds at most as many bits as cache->ktype (an error of a key enters the exponent): QMM_EUNSUPPORTED
+ *          for others, which qmm_kv_write and qmm_kv_read take.
  *   ws   : qmm_kv_attend_workspace() bytes, 16-byte aligned; nothing in it is kept between calls, and
  *          calls that may overlap in time need one each.
- * Results do not depend on scheduling.  Offsets that decrease so that sequences have more tokens than ntok in
+ * The same call gives the same bits, whatever the scheduling; in their last bits results depend on how the call is
+ * split, which is by nseq, ntok, max_pages and all lengths.  Offsets that decrease so that sequences have more tokens than ntok in
  * all: nothing is written.
  * Errors: QMM_EINVAL, QMM_EALIGN, QMM_EUNSUPPORTED, QMM_ESPACE. */
 int qmm_kv_attend(const qmm_kv_cache* cache, const int32_t* pages, int64_t ldpages, int64_t max_pages,

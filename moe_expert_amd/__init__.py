@@ -852,7 +852,8 @@ class KvCache:
     or uint8 with row = row_bytes(type, head_dim) (a page and head's planes of factors and scales; the
     layout is in include/qmm.h).  Pages may lie apart (a view into a larger allocation: the first
     dimension's stride), what is in a page is contiguous.  page_size is a multiple of 16, head_dim 64,
-    96, 128, 192 or 256.  The object keeps the tensors; it must not outlive a change of their storage."""
+    96, 128, 192 or 256.  Any two formats can be written and read; qmm_kv_attend takes values of at most as many
+    bits as the keys.  The object keeps the tensors; it must not outlive a change of their storage."""
 
     __slots__ = ("ktype", "vtype", "k", "v", "device", "npages", "nheads", "page_size", "head_dim", "width", "_struct", "_ref")
 
@@ -1010,7 +1011,8 @@ def qmm_kv_attend(q, cache, pages, lens, seg_off=None, scale=None, window=0, out
     cache's; head h reads the cache's head h // (nheads / cache.nheads).  pages, lens, seg_off as
     qmm_kv_write; a token at position p sees the positions j <= p, with window > 0 only j > p - window.
     scale: of the products, 1 / sqrt(head_dim) by default.  out: a tensor like q, of any of the types, or
-    a dtype for a new one (default q's; rows of no sequence are left alone); must not be q.  lse: float32
+    a dtype for a new one (default q's; rows of no sequence are left alone); must not be q nor overlap it.  The cache's
+    values must hold at most as many bits as its keys.  lse: float32
     [ntok, nheads] or True for a new one: the log of each row's sum of exponentials.  A row that sees no position
     gives zeros and -inf.  ws: qmm_kv_attend_workspace bytes (a call makes its own by default).
     Returns (out, lse)."""
