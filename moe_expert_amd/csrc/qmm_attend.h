@@ -464,13 +464,6 @@ __device__ __forceinline__ void taken() {
 
 // ------------------------------------------------------------------ operands
 
-// N bytes from an address of any alignment, the last dword filled up with zeros.
-template <int N>
-__device__ __forceinline__ void load_bytes(uint32_t* w, const char* p) {
-    if constexpr (N % 4) w[N / 4] = 0;
-    __builtin_memcpy(w, p, N);
-}
-
 // Two biased bytes u = q + 128, which perm laid into the low bytes of two halves, are u 2^-24 as binary16 values: to
 // q 2^-10.  (They could enter the products as they are, and what 128 in their place gives be taken from the sums.  That
 // is no faster, the matrix instructions wait for the others, and costs digits: 128 times a long context's weights is
@@ -497,16 +490,12 @@ struct Keys {
     uint32_t w[TYPE == kKvF16 ? 4 * NB : kBytes / 4];
     uint32_t d[TYPE == kKvF16 ? 1 : 2 * NB];  // scales [position 4g + r][block], two a dword
 
-    __device__ __forceinline__ void load(int lane, const char* rows, int scales) {
-        const int n = lane & 15, g = lane >> 4;
-        if constexpr (TYPE == kKvF16) {
-            const char* p = rows + (uint32_t)(n * (64 * NB) + 16 * g);
+    // Of binary16, from memory; block formats come through LDS.
+    __device__ __forceinline__ void load(int lane, const char* rows) {
+        static_assert(TYPE == kKvF16, "block formats are staged");
+        const char* p = rows + (uint32_t)((lane & 15) * (64 * NB) + 16 * (lane >> 4));
 #pragma unroll
-            for (int b = 0; b < NB; ++b) __builtin_memcpy(w + 4 * b, __builtin_assume_aligned(p + 64 * b, 16), 16);
-        } else {
-            load_bytes<kBytes>(w, rows + (uint32_t)(n * Side<TYPE, NB>::kFactor + g * kBytes));
-            load_bytes<8 * NB>(d, rows + scales + (uint32_t)(4 * g * (2 * NB)));
-        }
+        for (int b = 0; b < NB; ++b) __builtin_memcpy(w + 4 * b, __builtin_assume_aligned(p + 64 * b, 16), 16);
     }
     __device__ __forceinline__ void read(int lane, int h, const char* lds) {
         const int n = lane & 15, g = lane >> 4;
@@ -566,11 +555,11 @@ struct Values {
     uint32_t w[8][kWords];
     uint32_t d[2][TYPE == kKvF16 ? 1 : 2 * NB];  // scales [half][position 4g + r][block]
 
-    __device__ __forceinline__ void load(int lane, int half, const char* rows, int scales) {
-        const int n = lane & 15, g = lane >> 4;
-        const char* p = rows + (uint32_t)(4 * g * Side<TYPE, NB>::kFactor + n * kBytes);
+    __device__ __forceinline__ void load(int lane, int half, const char* rows) {
+        static_assert(TYPE == kKvF16, "block formats are staged");
+        const char* p = rows + (uint32_t)(4 * (lane >> 4) * Side<TYPE, NB>::kFactor + (lane & 15) * kBytes);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) load_bytes<kBytes>(w[4 * half + r], p + r * Side<TYPE, NB>::kFactor);
+        for (int r = 0; r < 4; ++r) __builtin_memcpy(w[4 * half + r], p + r * Side<TYPE, NB>::kFactor, kBytes);
     }
     __device__ __forceinline__ void read(int lane, const char* lds) {
         const int n = lane & 15, g = lane >> 4;
@@ -748,13 +737,6 @@ __device__ __forceinline__ float over(uint32_t fold) {
     return __builtin_bit_cast(float, ((127u + E + 127u) << 23) - fold);
 }
 
-__device__ __forceinline__ int rows_or(int v) {
-    auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
-    v = (int)r[0] | (int)r[1];
-    r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
-    return (int)r[0] | (int)r[1];
-}
-
 __device__ __forceinline__ void store4(const float* v, void* p, int64_t i, int type, int vec) {
     if (vec && type == kF32) {
         *(float4_t*)((float*)p + i) = float4_t{v[0], v[1], v[2], v[3]};
@@ -902,7 +884,7 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
         for (int h = 0; h < 2; ++h) {
             const int i = 2 * (k - block) + h;
             if constexpr (kStaged) kstage.fetch(lane, ring + k % kDepth * S::kKeys, h, rows_of(krows, i), lane_of(kfar, i));
-            else keys[h].load(lane, rows_of(krows, i), lane_of(kfar, i));
+            else keys[h].load(lane, rows_of(krows, i));
         }
     };
     // Of binary16 the next step's; after the last anything, so that this step's do not stay in registers through it.
@@ -921,7 +903,7 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
         for (int h = 0; h < 2; ++h) {
             const int i = 2 * (k - block) + h;
             if constexpr (kValBlocks) vstage.fetch(lane, ring + kDepth * S::kKeys + k % kDepth * S::kVals, h, rows_of(vrows, i), lane_of(vfar, i));
-            else vals.load(lane, h, rows_of(vrows, i), lane_of(vfar, i));
+            else vals.load(lane, h, rows_of(vrows, i));
         }
     };
     Values<VT, NB> vals;
