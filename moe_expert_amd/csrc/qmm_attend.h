@@ -493,9 +493,16 @@ struct Keys {
     // Of binary16, from memory; block formats come through LDS.
     __device__ __forceinline__ void load(int lane, const char* rows) {
         static_assert(TYPE == kKvF16, "block formats are staged");
-        const char* p = rows + (uint32_t)((lane & 15) * (64 * NB) + 16 * (lane >> 4));
 #pragma unroll
-        for (int b = 0; b < NB; ++b) __builtin_memcpy(w + 4 * b, __builtin_assume_aligned(p + 64 * b, 16), 16);
+        for (int b = 0; b < NB; ++b) {
+            u32x4 v;
+            load_block(v, lane, rows, b);
+            __builtin_memcpy(w + 4 * b, &v, 16);
+        }
+    }
+    __device__ static __forceinline__ void load_block(u32x4& v, int lane, const char* rows, int b) {
+        const char* p = rows + (uint32_t)((lane & 15) * (64 * NB) + 16 * (lane >> 4));
+        __builtin_memcpy(&v, __builtin_assume_aligned(p + 64 * b, 16), 16);
     }
     __device__ __forceinline__ void read(int lane, int h, const char* lds) {
         const int n = lane & 15, g = lane >> 4;
@@ -1044,29 +1051,31 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
                     }
                 // A key's infinity times the second part of a query's value, zero or of the other sign, would make NaN of the
                 // infinity that the first part gives: there the second parts meet the finite values alone.  (The keys are read
-                // again, so that they need no registers here where they are finite.)
+                // again, a block at a time, so that they need no registers here where they are finite.)
                 if (__any(odd)) {
-                    fetch_keys(k);
-                    keys[0].ready(ready[0]);
-                    keys[1].ready(ready[1]);
 #pragma unroll
-                    for (int x = 0; x < RT; ++x)
+                    for (int h = 0; h < 2; ++h) {
+                        const char* rows_h = rows_of(krows, 2 * (k - block) + h);
+                        float4_t u[RT], v[RT];
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            float4_t u = {0.0f, 0.0f, 0.0f, 0.0f}, v = u;
+                        for (int x = 0; x < RT; ++x) u[x] = v[x] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                            for (int b = 0; b < NB; ++b) {
-                                const half8_t kb = Keys<KT, NB>::block(ready[h], b);
-                                u32x4 f = __builtin_bit_cast(u32x4, kb);
+                        for (int b = 0; b < NB; ++b) {
+                            u32x4 kb;
+                            Keys<KT, NB>::load_block(kb, lane, rows_h, b);
+                            const u32x4 fin = {finite_halves(kb.x), finite_halves(kb.y), finite_halves(kb.z), finite_halves(kb.w)};
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) f[e] = finite_halves(f[e]);
-                                u = __builtin_amdgcn_mfma_f32_16x16x32_f16(kb, queries(x, b, 0), u, 0, 0, 0);
-                                v = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, f), queries(x, b, 1), v, 0, 0, 0);
-                                __builtin_amdgcn_sched_barrier(0);
+                            for (int x = 0; x < RT; ++x) {
+                                u[x] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, kb), queries(x, b, 0), u[x], 0, 0, 0);
+                                v[x] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, fin), queries(x, b, 1), v[x], 0, 0, 0);
                             }
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) z[x][4 * h + r] = u[r] + v[r];
+                            __builtin_amdgcn_sched_barrier(0);
                         }
+#pragma unroll
+                        for (int x = 0; x < RT; ++x)
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) z[x][4 * h + r] = u[x][r] + v[x][r];
+                    }
                 }
             }
         }
