@@ -39,8 +39,9 @@ typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kAtLds = 80 * 1024 - 512;  // bytes of LDS of a workgroup of which two share a CU
 constexpr int kAtStep = 32;      // positions a step
-// Sequences that a workgroup plans by itself; beyond, a launch of its own (128 of up to 1000 positions: 32.4 us, with the
-// launch 33.1; 256: 52.2, 48.4).
+// Sequences that a workgroup plans by itself; beyond, a launch of its own (q8_0, 128 of up to 250 positions, which are not
+// split: 13.8 us, with the launch 18.4; of up to 1000: 33.0, 33.7; 256 of up to 250: 32.0, with it 30.2; of up to 1000:
+// 52.2, 49.2).
 constexpr int kAtInline = 128;
 
 // What a workgroup leaves of a tile that goes on beyond it: the tile's pieces (0: none) and which of them, and its rows.
@@ -125,7 +126,8 @@ __device__ __forceinline__ SeqWork lane_work(const AttendArgs& a, int s, int row
 //
 // Where the pieces of a length c, every tile cut by itself, are no more than the workgroups, and c is not much longer
 // than the equal share of the steps, tiles take whole lengths: a workgroup has one piece then, and pays once for what
-// it does beside its steps (kAtCost steps of its time, about; 32 of up to 4096: 24.1 us, 28.7 without).
+// it does beside its steps (kAtCost steps of its time, about: 33 of up to 4096 take 23.5 us, 64 34.3; with 3 28.7 and 38.5, with
+// 40 the same; 40 x 4096 48.0, with 3 46.0).
 //
 // A length is a multiple of a step for each of four waves: one where the pieces then are no more than the CUs (1 x 1024
 // q8_0: 10.9 us, with two 13.0), else two (16 x 4 tokens, 192 wide, a window of 1000: 21.5 us, with one 23.4).
@@ -139,7 +141,9 @@ constexpr int kAtShort = 18;
 
 // Of two workgroups on a CU the one that came first is served first and ends first (32 x 8192 q8_0: after 38.7 us, the
 // other after 48.3), so where lengths are long the workgroups take the line in pairs, one of the first half and one
-// of the second, and the first of a pair takes kAtMore sixteenths of a length more.
+// of the second, and the first of a pair takes kAtMore sixteenths of a length more (1 x 131071 iq4_nl 36.6 us, with 1 37.0, with
+// 5 35.4; 64 x 4096 q8_0 63.2, 64.2, 62.5; others the same).  Long is kAtLong steps (32 of up to 6000, 16 rows, 256 wide iq4_nl:
+// 25.7 us, from 8 on 32.2; 33 x 4096 q8_0 41.8, from 64 on 43.1; but 5 x 4096 17.6, from 8 on 16.5).
 constexpr int kAtLong = 16, kAtMore = 3;
 struct Split {
     int pair, first;  // units of two workgroups, and of the first of them
@@ -182,7 +186,8 @@ __device__ __forceinline__ Split line_split(const AttendArgs& a, int units, int 
         count = lengths(even);
     }
     if (count > a.one && count <= a.one + a.one / 8) {
-        // rather a step more for all than two workgroups for a few CUs (32 multi-query, 256 wide: 27.2 us, 28.3 without)
+        // rather a step more for all than two workgroups for a few CUs (32 of up to 6000, 16 rows, 256 wide iq4_nl: 25.7 us, without
+        // 28.3; up to a third more of them: the same, but 5 x 4096 q8_0 16.1, an eighth 17.6)
         even += step;
         count = lengths(even);
     }
