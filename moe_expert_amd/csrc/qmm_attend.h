@@ -60,7 +60,7 @@ struct AttendArgs {
     KvSide k, v;
     KvPlace p;
     int nheads, group, qtype, otype;  // group: heads of queries a head of keys
-    float scale;                      // times log2(e)
+    float scale;                      // times log2(e) / 4, which is finite for every scale
     int window;                       // 0: none
     int target, one, least;           // workgroups a head of keys, of one for every CU;  steps that a tile counts for at least
     int shift;                        // a unit of the split is 2^shift steps: no line has more than 2^29 units
@@ -956,7 +956,7 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
             lq[x][b][0][16 * (j / 4) + r % 16][j % 4] = hi;
             lq[x][b][1][16 * (j / 4) + r % 16][j % 4] = lo;
         }
-        if (j == 0) lc[r] = power(e - 14 + (kKeyBlocks ? 10 : 0));
+        if (j == 0) lc[r] = power(e - 14 + 2 + (kKeyBlocks ? 10 : 0));
     }
     if (kStaged && kDepth > 1 && ksteps > 1) {
         fetch_keys(1);

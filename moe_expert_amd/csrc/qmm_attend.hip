@@ -197,7 +197,7 @@ extern "C" int qmm_kv_attend(const qmm_kv_cache* c, const int32_t* pages, int64_
     a.per_group = kv_per(a.group);
     a.qtype = qtype;
     a.otype = otype;
-    a.scale = (float)((double)scale * 1.4426950408889634);
+    a.scale = (float)((double)scale * (1.4426950408889634 / 4));
     a.window = (int)std::min(window, (int64_t)0x7FFFFFFF);  // more than any position
     a.target = s.target;
     a.one = std::max(kAtCus / c->nheads, 1);

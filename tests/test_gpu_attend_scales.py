@@ -175,3 +175,12 @@ def test_key_scale_that_is_not_finite(kinds, odd):
             rows = slice(96 * h, 96 * h + 96)
             assert (np.abs(got[h] - o[0, rows]) <= (bound + np.abs(o) * R.U)[0, rows]).all()
             assert abs(lse[0, h] - l[0, h]) <= lbound[0, h]
+
+
+@pytest.mark.parametrize("kinds", [("f16", "f16"), ("q8_0", "iq4_nl")])
+def test_largest_scale(kinds):
+    """The largest factors that are finite, against queries of zero and ones so small that scores are ordinary."""
+    for scale, q in ((3.3e38, 0.0), (-3.3e38, 0.0), (3.0e38, 1e-38), (2.0 ** 127, 2.0 ** -126)):
+        c = Case([90], kinds=kinds, heads=4, kv=2, dim=64, page=16, qscale=q)
+        c.scale = scale
+        c.check()
