@@ -172,9 +172,9 @@ __device__ __forceinline__ int tile_units(const AttendArgs& a, int steps, const 
 // done then.
 template <class F>
 __device__ __forceinline__ Split line_split(const AttendArgs& a, int units, int tiles, int64_t tokens, F lengths) {
-    if (tokens > a.p.ntok) return Split{2, 1, 0, 0, false};
+    const bool many = tokens > a.p.ntok;
     if (!a.pieces && !a.plan)  // a workgroup a tile
-        return Split{2 * kAtShort, kAtShort, tiles * kAtShort, kAtShort, false};
+        return Split{2 * kAtShort, kAtShort, many ? 0 : tiles * kAtShort, kAtShort, false};
     Split s;
     const int target = a.target, step = max(kAtWaves >> a.shift, 1);
     const auto rounded = [&](int len) { return max((len + step - 1) & -step, step); };  // as many steps for every wave
@@ -212,7 +212,8 @@ __device__ __forceinline__ Split line_split(const AttendArgs& a, int units, int 
     }
     s.pair = 2 * len;
     s.first = s.paired ? len + ((len * kAtMore / 16 + step - 1) & -step) : len;
-    s.all = whole ? count * s.whole : units;
+    s.all = many ? 0 : whole ? count * s.whole : units;
+    if (many) s.pair = s.first = 0;  // (nobody's place is below 0)
     return s;
 }
 
@@ -411,19 +412,22 @@ struct Stage {
     __device__ static __forceinline__ void scales(uint32_t* d, const char* lds, int h, int g) {
         __builtin_memcpy(d, __builtin_assume_aligned(lds + kScales + (32 * h + 8 * g) * NB, 8), 8 * NB);
     }
-    // Of the 4 NB dwords of scales of positions 4g .. 4g+3 of both halves the ones that a lane's place n among 16 falls to,
-    // and whether one holds a magnitude whose binary16 bits are more than `most`, one for each of the two blocks that it is of.
+    // Of the 4 NB dwords of scales of positions 4g .. 4g+3 of both halves the magnitudes of the ones that a lane's place n among
+    // 16 falls to, each of two blocks; and whether one of them has binary16 bits of more than `most`.
     static constexpr int kParts = (4 * NB + 15) / 16;
     __device__ static __forceinline__ int part(int n, int i) { return min(n + 16 * i, 4 * NB - 1); }
-    __device__ static __forceinline__ bool above(const char* lds, int n, int g, const u16x2 (&most)[kParts]) {
-        bool any = false;
+    __device__ static __forceinline__ void parts(const char* lds, int n, int g, u16x2 (&v)[kParts]) {
 #pragma unroll
         for (int i = 0; i < kParts; ++i) {
             const int j = part(n, i);
-            const uint32_t v = *(const uint32_t*)(lds + kScales + (32 * (j / (2 * NB)) + 8 * g) * NB + 4 * (j % (2 * NB))) & 0x7FFF7FFFu;
-            const u16x2 larger = __builtin_elementwise_max(__builtin_bit_cast(u16x2, v), most[i]);
-            any |= __builtin_bit_cast(uint32_t, larger) != __builtin_bit_cast(uint32_t, most[i]);
+            v[i] = __builtin_bit_cast(u16x2, *(const uint32_t*)(lds + kScales + (32 * (j / (2 * NB)) + 8 * g) * NB + 4 * (j % (2 * NB))) & 0x7FFF7FFFu);
         }
+    }
+    __device__ static __forceinline__ bool above(const u16x2 (&v)[kParts], const u16x2 (&most)[kParts]) {
+        bool any = false;
+#pragma unroll
+        for (int i = 0; i < kParts; ++i)
+            any |= __builtin_bit_cast(uint32_t, __builtin_elementwise_max(v[i], most[i])) != __builtin_bit_cast(uint32_t, most[i]);
         return any;
     }
     // The step's scales without those that are not finite, by the whole wave.
@@ -1158,9 +1162,11 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
             vals.keep_words();
             char* const scales = ring + kDepth * S::kKeys + k % kDepth * S::kVals;
             // Scales that some row's folds leave no room for, seen or not: seldom after the first step.
-            if (__any(Stage<VT, NB>::above(scales, there & 15, there >> 4, room))) {
+            u16x2 part[kParts];
+            Stage<VT, NB>::parts(scales, there & 15, there >> 4, part);
+            if (__any(Stage<VT, NB>::above(part, room))) {
                 asm volatile("");
-                vals.keep_words();  // (read again at the end: the registers go to the sums)
+                vals.keep_words();
                 const auto largest = [&](u16x2(&most)[RT][kPairs]) {
 #pragma unroll
                     for (int x = 0; x < RT; ++x) {
@@ -1179,14 +1185,17 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
                 // out, and makes its block NaN in the rows that do.
                 u16x2 finite[kParts];
                 int odd[RT] = {};
+                float up[RT][NB];
+                bool any_odd = false;
 #pragma unroll
                 for (int i = 0; i < kParts; ++i) finite[i] = u16x2{0x7BFF, 0x7BFF};
-                if (__any(Stage<VT, NB>::above(scales, there & 15, there >> 4, finite))) {
+                if (__any(Stage<VT, NB>::above(part, finite))) {
                     largest(most);
 #pragma unroll
                     for (int x = 0; x < RT; ++x)
 #pragma unroll
                         for (int b = 0; b < NB; ++b) odd[x] |= most[x][b / 2][b % 2] >= 0x7C00 ? 1 << b : 0;
+                    any_odd = true;
                     Stage<VT, NB>::keep_finite(scales, there);
                     vals.read_scales(there, scales);
                 }
@@ -1200,26 +1209,30 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
                     for (int i = 0; i < kPairs; ++i) {
                         const u16x2 d = most[x][i];
                         uint32_t now[2];
-                        float up[2];
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             // (a zero's is beyond kFoldMost)
                             const uint32_t scale = __builtin_bit_cast(uint32_t, h2f(d[e]));
                             now[e] = min(((127u + 13u + 127u) << 23) - (scale & 0x7F800000u), fold_bits(x, 2 * i + e));
-                            up[e] = odd[x] >> (2 * i + e) & 1 ? NAN : __builtin_bit_cast(float, now[e] - fold_bits(x, 2 * i + e) + (127u << 23));
-                            if (2 * i + e < NB) {
-                                o[x][2 * (2 * i + e)] *= up[e];
-                                o[x][2 * (2 * i + e) + 1] *= up[e];
-                            }
+                            const float change = odd[x] >> (2 * i + e) & 1 ? NAN : __builtin_bit_cast(float, now[e] - fold_bits(x, 2 * i + e) + (127u << 23));
+                            if (2 * i + e < NB) up[x][2 * i + e] = change;
                         }
                         fold[x][i] = now[0] >> 16 | now[1];
                         const u16x2 limit = __builtin_bit_cast(u16x2, __builtin_convertvector((float2_t{over<15>(now[0]), over<15>(now[1])}), half2_t));
                         least[i] = __builtin_elementwise_min(least[i], limit - u16x2{1, 1});
                     }
                 }
+                if (k > 0 || any_odd) {  // (the first step's sums are zeros)
+#pragma unroll
+                    for (int x = 0; x < RT; ++x)
+#pragma unroll
+                        for (int t = 0; t < kTiles; ++t) o[x][t] *= up[x][t / 2];
+                }
                 Stage<VT, NB>::share(there & 15, least, room);
-                asm volatile("" ::: "memory");
-                vals.read_scales(there, scales);
+                if constexpr (NB * RT > 4) {  // (their registers go to the sums)
+                    asm volatile("" ::: "memory");
+                    vals.read_scales(there, scales);
+                }
                 vals.keep_words();
             }
             vals.keep_words();
