@@ -629,12 +629,12 @@ struct Values {
     // Whether a binary16 value is not finite: its product with zero is a NaN then, one instruction a dword.
     __device__ __forceinline__ bool any_odd() const {
         const half2_t zero = {0, 0};
-        half2_t sum[2] = {zero, zero};
+        half2_t sum[4] = {zero, zero, zero, zero};
 #pragma unroll
         for (int x = 0; x < 8; ++x)
 #pragma unroll
-            for (int i = 0; i < kWords; ++i) sum[x & 1] = __builtin_elementwise_fma(__builtin_bit_cast(half2_t, w[x][i]), zero, sum[x & 1]);
-        return odd_halves(__builtin_bit_cast(uint32_t, sum[0] + sum[1])) != 0;
+            for (int i = 0; i < kWords; ++i) sum[x & 3] = __builtin_elementwise_fma(__builtin_bit_cast(half2_t, w[x][i]), zero, sum[x & 3]);
+        return odd_halves(__builtin_bit_cast(uint32_t, (sum[0] + sum[1]) + (sum[2] + sum[3]))) != 0;
     }
     // The scales as they are loaded, two a register, also past a branch that may change them.
     __device__ __forceinline__ void keep_words() {
