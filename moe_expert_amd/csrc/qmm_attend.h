@@ -327,12 +327,22 @@ __device__ __forceinline__ uint32_t odd_halves(uint32_t v) { return ((v & 0x7C00
 // The halves that are finite, zeros for the others.
 __device__ __forceinline__ uint32_t finite_halves(uint32_t v) { return v & ~((odd_halves(v) >> 15) * 0xFFFFu); }
 
-// The least of the 16 lanes of a row, both halves apart.
+template <int CTRL>
+__device__ __forceinline__ u16x2 dpp_pair(u16x2 v) { return __builtin_bit_cast(u16x2, dpp_i<CTRL>(__builtin_bit_cast(int, v))); }
+// The least of the 16 lanes of a row, both halves apart; the most of the lanes n, n + 16, n + 32, n + 48.
 __device__ __forceinline__ u16x2 min16_pair(u16x2 v) {
-    v = __builtin_elementwise_min(v, __builtin_bit_cast(u16x2, dpp_i<0xB1>(__builtin_bit_cast(int, v))));
-    v = __builtin_elementwise_min(v, __builtin_bit_cast(u16x2, dpp_i<0x4E>(__builtin_bit_cast(int, v))));
-    v = __builtin_elementwise_min(v, __builtin_bit_cast(u16x2, dpp_i<0x141>(__builtin_bit_cast(int, v))));
-    return __builtin_elementwise_min(v, __builtin_bit_cast(u16x2, dpp_i<0x140>(__builtin_bit_cast(int, v))));
+    v = __builtin_elementwise_min(v, dpp_pair<0xB1>(v));
+    v = __builtin_elementwise_min(v, dpp_pair<0x4E>(v));
+    v = __builtin_elementwise_min(v, dpp_pair<0x141>(v));
+    return __builtin_elementwise_min(v, dpp_pair<0x140>(v));
+}
+__device__ __forceinline__ u16x2 rows_max16(u16x2 v) {
+    const int x = __builtin_bit_cast(int, v);
+    auto r = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    v = __builtin_elementwise_max(__builtin_bit_cast(u16x2, (int)r[0]), __builtin_bit_cast(u16x2, (int)r[1]));
+    const int y = __builtin_bit_cast(int, v);
+    r = __builtin_amdgcn_permlane32_swap(y, y, false, false);
+    return __builtin_elementwise_max(__builtin_bit_cast(u16x2, (int)r[0]), __builtin_bit_cast(u16x2, (int)r[1]));
 }
 
 // 32 positions of a block format, as they lie in a page: the factors of both 16-position halves, then their scales,
@@ -436,10 +446,28 @@ struct Stage {
         for (int i = lane; i < 16 * NB; i += 64) w[i] = finite_halves(w[i]);
         wave_fence();
     }
-    // What is compared there: the least of the rows' (of the lanes n) values for blocks 2i and 2i + 1 in v[i].
-    __device__ static __forceinline__ void share(int n, u16x2 (&v)[(NB + 1) / 2], u16x2 (&most)[kParts]) {
+    // The blocks' largest of a step, from all lanes' parts: of two, four or eight blocks the lanes whose n are the same modulo
+    // their pairs hold the same blocks.
+    static constexpr bool kWhole = (NB & (NB - 1)) == 0;
+    __device__ static __forceinline__ void largest(const u16x2 (&v)[kParts], u16x2 (&most)[(NB + 1) / 2]) {
+        static_assert(kWhole, "pairs of blocks that divide the lanes of a quad");
+        u16x2 w = v[0];
 #pragma unroll
-        for (u16x2& w : v) w = min16_pair(w);
+        for (int i = 1; i < kParts; ++i) w = __builtin_elementwise_max(w, v[i]);
+        if constexpr (NB < 4) w = __builtin_elementwise_max(w, dpp_pair<0xB1>(w));
+        if constexpr (NB < 8) w = __builtin_elementwise_max(w, dpp_pair<0x4E>(w));
+        w = __builtin_elementwise_max(w, dpp_pair<0x124>(w));  // row_ror 4, 8
+        w = __builtin_elementwise_max(w, dpp_pair<0x128>(w));
+        w = rows_max16(w);
+        most[0] = dpp_pair<0x00>(w);
+        if constexpr (NB >= 4) most[1] = dpp_pair<0x55>(w);
+        if constexpr (NB >= 8) {
+            most[2] = dpp_pair<0xAA>(w);
+            most[3] = dpp_pair<0xFF>(w);
+        }
+    }
+    // What is compared there, of the values for blocks 2i and 2i + 1 in v[i].
+    __device__ static __forceinline__ void share(int n, const u16x2 (&v)[(NB + 1) / 2], u16x2 (&most)[kParts]) {
 #pragma unroll
         for (int i = 0; i < kParts; ++i) {
             const int first = 2 * part(n, i) % NB;  // of the blocks
@@ -552,15 +580,6 @@ struct Keys {
 };
 
 __device__ __forceinline__ bool not_finite(uint32_t half) { return (half & 0x7C00u) == 0x7C00u; }
-
-__device__ __forceinline__ u16x2 rows_max16(u16x2 v) {
-    const int x = __builtin_bit_cast(int, v);
-    auto r = __builtin_amdgcn_permlane16_swap(x, x, false, false);
-    v = __builtin_elementwise_max(__builtin_bit_cast(u16x2, (int)r[0]), __builtin_bit_cast(u16x2, (int)r[1]));
-    const int y = __builtin_bit_cast(int, v);
-    r = __builtin_amdgcn_permlane32_swap(y, y, false, false);
-    return __builtin_elementwise_max(__builtin_bit_cast(u16x2, (int)r[0]), __builtin_bit_cast(u16x2, (int)r[1]));
-}
 
 // The values of 32 positions: lane (n, g) holds, of the positions 4g .. 4g+3 of both halves, the dims that
 // row n of the 2 NB operands V^T takes: tile (b, i) dim 32b + 16i + n (binary16: tile j dim 2 NB n + j).
@@ -688,9 +707,8 @@ struct Mix {
     float minus, zero;
     __device__ __forceinline__ Mix() : minus(-1.0f), zero(0.0f) { asm("" : "+s"(minus), "+s"(zero)); }
     __device__ __forceinline__ float rest(float x, _Float16 h) const { return __builtin_fmaf((float)h, minus, x); }
-    // A product with a factor h, rounded to binary16, and what that leaves, the same way (v_fma_mixlo_f16, v_fma_mixhi_f16).
-    __device__ __forceinline__ _Float16 high(float x, _Float16 h) const { return (_Float16)__builtin_fmaf((float)h, x, zero); }
-    __device__ __forceinline__ _Float16 low(float x, _Float16 h, _Float16 high) const { return (_Float16)__builtin_fmaf((float)h, x, -(float)high); }
+    __device__ __forceinline__ float product(float x, _Float16 h) const { return __builtin_fmaf((float)h, x, zero); }
+    __device__ __forceinline__ float product_rest(float x, _Float16 h, _Float16 near) const { return __builtin_fmaf((float)h, x, -(float)near); }
 };
 
 // Two binary16 parts of pairs of values: the nearest, and the nearest of what is left.
@@ -701,30 +719,22 @@ __device__ __forceinline__ void two_parts(const Mix& mix, float x, float y, uint
     lo = __builtin_bit_cast(uint32_t, __builtin_convertvector(rest, half2_t));
 }
 
-// The same of eight values' products with factors, by v_fma_mixlo_f16 and v_fma_mixhi_f16: four instructions a pair, where
-// products and the parts above are six.  (The empty asm keeps the compiler from rounding the two of a pair together.  All
-// pairs at once: what takes the half that an instruction leaves waits for one more.)
+// The same of eight values' products with factors.  (All pairs' nearest before what they leave: a conversion waits for the two
+// values that it takes.  v_fma_mixlo_f16 and v_fma_mixhi_f16 would take four instructions a pair, these are six, but
+// take longer: 1 x 131071 q8_0/iq4_nl 34.3 us, these 33.1.)
 template <class F>
 __device__ __forceinline__ void scaled_parts(const Mix& mix, const float (&u)[8], F factor, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
-    _Float16 part[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        part[i] = mix.high(u[2 * i], factor(2 * i));
-        asm("" : "+v"(part[i]));
+        const float2_t p = {mix.product(u[2 * i], factor(2 * i)), mix.product(u[2 * i + 1], factor(2 * i + 1))};
+        hi[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(p, half2_t));
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        hi[i] = __builtin_bit_cast(uint32_t, half2_t{part[i], mix.high(u[2 * i + 1], factor(2 * i + 1))});
-        asm("" : "+v"(hi[i]));
+        const half2_t h = __builtin_bit_cast(half2_t, hi[i]);
+        const float2_t rest = {mix.product_rest(u[2 * i], factor(2 * i), h.x), mix.product_rest(u[2 * i + 1], factor(2 * i + 1), h.y)};
+        lo[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(rest, half2_t));
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        part[i] = mix.low(u[2 * i], factor(2 * i), __builtin_bit_cast(half2_t, hi[i]).x);
-        asm("" : "+v"(part[i]));
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        lo[i] = __builtin_bit_cast(uint32_t, half2_t{part[i], mix.low(u[2 * i + 1], factor(2 * i + 1), __builtin_bit_cast(half2_t, hi[i]).y)});
 }
 
 // Maximum and sum over the lanes n, n + 16, n + 32, n + 48.
@@ -1061,7 +1071,7 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
                 // A key's infinity times the second part of a query's value, zero or of the other sign, would make NaN of the
                 // infinity that the first part gives: there the second parts meet the finite values alone.  (The keys are read
                 // again, a block at a time, so that they need no registers here where they are finite.)
-                if (__any(odd)) {
+                if (__builtin_expect(__any(odd), 0)) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const char* rows_h = rows_of(krows, 2 * (k - block) + h);
@@ -1167,66 +1177,80 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
             if (__any(Stage<VT, NB>::above(part, room))) {
                 asm volatile("");
                 vals.keep_words();
-                const auto largest = [&](u16x2(&most)[RT][kPairs]) {
+                // The blocks' largest scales that each row sees.
+                u16x2 most[RT][kPairs];
+                const auto look = [&]() {
 #pragma unroll
                     for (int x = 0; x < RT; ++x) {
                         if (masked) {
                             vals.template largest<true>(seen[x], most[x]);
-                        } else if (x == 0) {
-                            vals.template largest<false>(0, most[0]);
-                        } else {
+                        } else if (x > 0) {
 #pragma unroll
                             for (int i = 0; i < kPairs; ++i) most[x][i] = most[0][i];
+                        } else if constexpr (Stage<VT, NB>::kWhole) {
+                            Stage<VT, NB>::largest(part, most[0]);
+                        } else {
+                            vals.template largest<false>(0, most[0]);
                         }
                     }
                 };
-                u16x2 most[RT][kPairs];
+                look();
                 // A scale that is not finite must not meet the weight 0 of a row that does not see it: it is left
                 // out, and makes its block NaN in the rows that do.
                 u16x2 finite[kParts];
-                int odd[RT] = {};
-                float up[RT][NB];
+                int odd[RT];
                 bool any_odd = false;
 #pragma unroll
                 for (int i = 0; i < kParts; ++i) finite[i] = u16x2{0x7BFF, 0x7BFF};
-                if (__any(Stage<VT, NB>::above(part, finite))) {
-                    largest(most);
+                if (__builtin_expect(__any(Stage<VT, NB>::above(part, finite)), 0)) {
+                    any_odd = true;
 #pragma unroll
-                    for (int x = 0; x < RT; ++x)
+                    for (int x = 0; x < RT; ++x) {
+                        odd[x] = 0;
 #pragma unroll
                         for (int b = 0; b < NB; ++b) odd[x] |= most[x][b / 2][b % 2] >= 0x7C00 ? 1 << b : 0;
-                    any_odd = true;
+                    }
                     Stage<VT, NB>::keep_finite(scales, there);
                     vals.read_scales(there, scales);
+                    Stage<VT, NB>::parts(scales, there & 15, there >> 4, part);
+                    look();
                 }
-                largest(most);
+                uint32_t was[RT][kPairs];
                 u16x2 least[kPairs];
 #pragma unroll
                 for (int i = 0; i < kPairs; ++i) least[i] = u16x2{0x7BFF, 0x7BFF};
 #pragma unroll
-                for (int x = 0; x < RT; ++x) {
+                for (int x = 0; x < RT; ++x)
 #pragma unroll
                     for (int i = 0; i < kPairs; ++i) {
-                        const u16x2 d = most[x][i];
                         uint32_t now[2];
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             // (a zero's is beyond kFoldMost)
-                            const uint32_t scale = __builtin_bit_cast(uint32_t, h2f(d[e]));
+                            const uint32_t scale = __builtin_bit_cast(uint32_t, h2f(most[x][i][e]));
                             now[e] = min(((127u + 13u + 127u) << 23) - (scale & 0x7F800000u), fold_bits(x, 2 * i + e));
-                            const float change = odd[x] >> (2 * i + e) & 1 ? NAN : __builtin_bit_cast(float, now[e] - fold_bits(x, 2 * i + e) + (127u << 23));
-                            if (2 * i + e < NB) up[x][2 * i + e] = change;
                         }
+                        was[x][i] = fold[x][i];
                         fold[x][i] = now[0] >> 16 | now[1];
                         const u16x2 limit = __builtin_bit_cast(u16x2, __builtin_convertvector((float2_t{over<15>(now[0]), over<15>(now[1])}), half2_t));
                         least[i] = __builtin_elementwise_min(least[i], limit - u16x2{1, 1});
                     }
-                }
                 if (k > 0 || any_odd) {  // (the first step's sums are zeros)
 #pragma unroll
                     for (int x = 0; x < RT; ++x)
 #pragma unroll
-                        for (int t = 0; t < kTiles; ++t) o[x][t] *= up[x][t / 2];
+                        for (int b = 0; b < NB; ++b) {
+                            const uint32_t old = b & 1 ? was[x][b / 2] & 0xFFFF0000u : was[x][b / 2] << 16;
+                            float up = __builtin_bit_cast(float, fold_bits(x, b) - old + (127u << 23));
+                            if (any_odd && odd[x] >> b & 1) up = NAN;
+                            o[x][2 * b] *= up;
+                            o[x][2 * b + 1] *= up;
+                        }
+                }
+                // (the first step's rows are alike where they all see all of it)
+                if (masked || k > 0) {
+#pragma unroll
+                    for (u16x2& v : least) v = min16_pair(v);
                 }
                 Stage<VT, NB>::share(there & 15, least, room);
                 if constexpr (NB * RT > 4) {  // (their registers go to the sums)
@@ -1250,7 +1274,7 @@ __device__ __forceinline__ void attend_piece(const SeqWork& w, int tile, int fro
                     for (int e = 0; e < Values<VT, NB>::kWords; ++e) vals.w[i][e] = some ? vals.w[i][e] : 0u;
                 }
             }
-            if (__any(vals.any_odd())) {
+            if (__builtin_expect(__any(vals.any_odd()), 0)) {
                 if (!masked) {
 #pragma unroll
                     for (int x = 0; x < RT; ++x) seen[x] = 0xFF;
