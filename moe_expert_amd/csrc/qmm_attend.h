@@ -20,8 +20,8 @@
 // zero: 7 times the bound of the binary32 sums with one power for all, a hundredth of it so).
 //
 // Bounds.  Binary16: the cache's bytes (32 sequences of 8192 positions, 4 heads of 128: 98 us, 5.5 TB/s).  Block formats:
-// the vector instructions of a step, some 380 for 32 positions of q8_0 and 590 of iq4_nl at 128 wide, most of them to unpack
-// the bytes and to scale and cut the weights once a block (63 us, 4.5 TB/s; 62 us, 2.4 TB/s); the matrix units are
+// the vector instructions of a step, some 450 for 32 positions of q8_0 and 650 of iq4_nl at 128 wide, most of them to unpack
+// the bytes and to scale and cut the weights once a block (62 us, 4.6 TB/s; 59 us, 2.6 TB/s); the matrix units are
 // busy an eighth of the time.  Few positions: one load after the other (arguments, lengths, pages, keys), 5 us until
 // the first step, 1 us behind the last, and the join's launch.
 #pragma once

@@ -102,7 +102,7 @@ struct KvSpot {
 // lies within 5e-5 of a tie (2^-10 of a doubled middle): then, and for a scale beyond what this holds for,
 // zero or not finite, or a NaN, the wave divides the block again as the definition does.
 //   8192 tokens of 4 heads of 128, binary16 to q8_0, keys and values: 12.6 us, 2.0 TB/s
-// (17.7 with every quotient divided out and a byte a store); 8 tokens: 3.3 us, two dependent loads and a launch.
+// (17.7 with every quotient divided out and a byte a store); 8 tokens: 3.9 us, two dependent loads and a launch.
 template <int NB>
 struct KvWrite {
     uint32_t raw[2 * NB], table;
